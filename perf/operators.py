@@ -247,10 +247,14 @@ def work(case):
 def exact(case, seed):
     op = case["op"]
     gen = _generator(seed)
-    if op in ("pack4", "gemv4"):
-        w = _weight(case, gen)
-        if op == "pack4":
-            w = w.to(TYPES[case["dtype"]])
+    if op == "gemv4":
+        # the weights are given in 4 bits: the product alone is the operator
+        q, s = _quantised(_weight(case, gen), case["group"])
+        x = torch.empty(case["tokens"], case["cols"], device=DEV, dtype=torch.float32).normal_(0.0, 1.0, generator=gen)
+        value = (q.double() * s.double()).flatten(1)[:, :case["cols"]]
+        return torch.matmul(x.to(TYPES[case["dtype"]]).double(), value.t())
+    if op == "pack4":
+        w = _weight(case, gen).to(TYPES[case["dtype"]])
         N, K, G = case["rows"], case["cols"], case["group"]
         n = -(-K // G)
         full = torch.zeros(N, n * G, device=DEV, dtype=torch.float64)
@@ -263,11 +267,7 @@ def exact(case, seed):
         unit = torch.exp2(e - 7)
         scale = (torch.floor(scale / unit) * unit) * (scale >= 2.0 ** -126)
         full = torch.round(full / scale.clamp_min(1e-300)[:, None]).clamp(-7, 7) * scale[:, None]
-        full = full.reshape(N, n * G)[:, :K]
-        if op == "pack4":
-            return full
-        x = torch.empty(case["tokens"], K, device=DEV, dtype=torch.float32).normal_(0.0, 1.0, generator=gen)
-        return torch.matmul(x.to(TYPES[case["dtype"]]).double(), full.t())
+        return full.reshape(N, n * G)[:, :K]
     x, tokens = _logits(case, gen)
     R, V = x.shape
     if op == "grad":
