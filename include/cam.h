@@ -675,6 +675,129 @@ int cam_adopt_keep_drift(int32_t n_tensors, const int64_t* numel, float* const* 
                          const float* const* global, const void* const* pushed,
                          cam_dtype pushed_dtype, void* stream);
 
+/*
+ * Beside the merge: publishing a merged global in 4 bits, answering from it,
+ * and probing it on held-out tokens. The DiffuRefill-1B merger publishes each
+ * global and probes it every round ("DiffuRefill-1B" technical report,
+ * section 3, Table 2, and section 5); the pages store the globals in full
+ * precision, so the 4-bit form below is this library's own. These calls need
+ * no context and allocate nothing. Every array is a device pointer of the
+ * current CUDA device; the work is queued on `stream` (a cudaStream_t, NULL
+ * for the default stream), may be captured into a CUDA graph, and the call
+ * returns before it runs. Outputs may not overlap inputs unless a call says
+ * so. Results are the same bits from call to call. Strides count elements
+ * between the starts of rows; a row's elements are contiguous. No pointer
+ * needs more than its element type's alignment, `packed` excepted (16 bytes);
+ * 16-byte aligned rows take the vectorised path. Argument checks come before
+ * any CUDA call.
+ */
+
+/*
+ * The 4-bit form of a row-major rows x cols matrix. Each row is cut into
+ * groups of `group` (32, 64 or 128) columns, the last of them possibly short.
+ * Per group, in binary32:
+ *
+ *   s = max|w| / 7 with its low 16 bits cleared (a bf16 rounded toward zero,
+ *       so 7 s never passes max|w|), or 0 when that is below 2^-126
+ *   q = w * (1 / s) rounded to the nearest integer, ties to even, held to
+ *       [-7, 7]; 0 when s is 0
+ *
+ * and the group stands for the values q * s. A group that holds a NaN or an
+ * infinity stands for NaN (s = NaN, q = 0): a broken weight stays visible.
+ * The bytes, for users who store or send them: the matrix is tiled by 16 rows
+ * x 128 columns, tiles in row-major order of tiles, rows and columns past the
+ * end held as q = 0. A tile is 1,024 bytes of q, then 32 * (128 / group)
+ * bytes of s. The 32-bit little-endian word at byte 16 * l + 4 * i of
+ * half h (h = 0, 1, 512 bytes each; l = 0..31; i = 0..3) holds row
+ * 8 * h + l / 4, columns 32 * i + 8 * (l % 4) + c for c = 0..7, as q + 8, in
+ * nibbles 0, 4, 1, 5, 2, 6, 3, 7 for c = 0..7 (nibble 0 is the least
+ * significant). The scales are bf16, that of row 8 * h + r (r = 0..7) and
+ * group j of the tile at index (2 * r + h) * (128 / group) + j.
+ */
+#define CAM_PACK4_MAX_COLS (1 << 17)
+
+/* The bytes of the 4-bit form. rows >= 0, cols in [0, CAM_PACK4_MAX_COLS].
+ * Errors: CAM_E_ARG. */
+int cam_pack4_bytes(int64_t rows, int64_t cols, int32_t group, int64_t* out);
+
+/* Writes the 4-bit form of w (fp32 or bf16, `stride` >= cols) into packed
+ * (cam_pack4_bytes bytes, 16-byte aligned). Errors: CAM_E_ARG, CAM_E_CUDA. */
+int cam_pack4(int64_t rows, int64_t cols, const void* w, int64_t stride, cam_dtype dtype,
+              int32_t group, void* packed, void* stream);
+
+/* Writes the values q * s that packed stands for, exact in fp32 and rounded
+ * to nearest-even in bf16. Errors: CAM_E_ARG, CAM_E_CUDA. */
+int cam_unpack4(int64_t rows, int64_t cols, const void* packed, int32_t group, void* values,
+                int64_t stride, cam_dtype dtype, void* stream);
+
+/*
+ * y = x W^T for W (rows x cols) in the 4-bit form: y[m][n] is the sum over
+ * groups of s * (sum of q * x[m]), for each of `tokens` rows x[m] of cols
+ * elements, into y[m] of rows elements. Products are exact and sums are held
+ * in binary32, whatever the types of x and y (fp32 or bf16); y is rounded
+ * once. Made for the few tokens of a decoding step: the weights are read once
+ * for up to 32 bf16 tokens (10 in fp32) and again for each further such set.
+ * A group's sum of q * x is formed before its scale, so |x| above about 1e35
+ * may overflow where q * s * x would not. cols = 0 writes zeros.
+ * Errors: CAM_E_ARG, CAM_E_CUDA.
+ */
+int cam_gemv4(int64_t tokens, int64_t rows, int64_t cols, const void* x, int64_t x_stride,
+              cam_dtype x_dtype, const void* packed, int32_t group, void* y, int64_t y_stride,
+              cam_dtype y_dtype, void* stream);
+
+/*
+ * What a model says of given tokens: for each of `rows` rows x of `vocab`
+ * logits (fp32 or bf16),
+ *
+ *   lse     = log sum_j exp(x_j)
+ *   logp    = x[token] - lse         0 for a negative token id (no token)
+ *   entropy = -sum_j p_j log p_j     p_j = exp(x_j - lse), nats
+ *   top     the `top` largest x_j - lse, largest first, with their ids; equal
+ *           logits in the order of their ids
+ *
+ * in binary32. lse_lo is what rounding lse to binary32 left out: the pair
+ * lse + lse_lo serves the gradient of confident rows, whose log p is far
+ * smaller than lse. tokens (int64, [rows]) and logp may both be NULL; entropy,
+ * lse, lse_lo, and top_logp / top_ids (row-major [rows][top]) may each be
+ * NULL.
+ * top in [0, min(vocab, CAM_LOGPROBS_MAX_TOP)].
+ * Logits of -inf are tokens that cannot occur (p = 0). A row of them alone
+ * has lse = logp = top_logp = -inf and entropy 0; a row with a NaN or a +inf
+ * has NaN throughout, its ids ordered with NaN above +inf. A token id of
+ * `vocab` or more reads nothing and gives a logp of NaN.
+ * Errors: CAM_E_ARG, CAM_E_CUDA.
+ */
+#define CAM_LOGPROBS_MAX_TOP 32
+#define CAM_LOGPROBS_MAX_VOCAB (1 << 24)
+int cam_token_logprobs(int64_t rows, int64_t vocab, const void* logits, int64_t stride,
+                       cam_dtype dtype, const int64_t* tokens, int32_t top, float* logp,
+                       float* entropy, float* lse, float* lse_lo, float* top_logp,
+                       int64_t* top_ids, void* stream);
+
+/*
+ * The gradient of cam_token_logprobs with respect to the logits, for the
+ * gradients grad_logp (g) of logp and grad_entropy (h) of entropy, fp32
+ * [rows]:
+ *
+ *   grad_logits_j = g * (1[j = token] - p_j) - h * p_j * (log p_j + entropy)
+ *
+ * written in the logits' dtype, rounded once. Either of grad_logp (with
+ * tokens) and grad_entropy (with entropy) may be NULL, not both. lse, lse_lo
+ * and entropy are as cam_token_logprobs wrote them for these logits; lse_lo
+ * may be NULL (then log p has lse's rounding).
+ * A negative token id counts as g = 0. A row whose g and h are 0 gets zeros
+ * and its logits are not read; so does a row whose lse is -inf. A row whose
+ * lse is NaN, and one whose token id is `vocab` or more (with g other than
+ * 0), gets NaN. grad_logits may be the logits' own buffer (same pointer and
+ * stride): each element is read before it is written.
+ * Errors: CAM_E_ARG, CAM_E_CUDA.
+ */
+int cam_token_logprobs_backward(int64_t rows, int64_t vocab, const void* logits, int64_t stride,
+                                cam_dtype dtype, const int64_t* tokens, const float* lse,
+                                const float* lse_lo, const float* entropy,
+                                const float* grad_logp, const float* grad_entropy,
+                                void* grad_logits, int64_t grad_stride, void* stream);
+
 /* Message describing the calling thread's last error ("" if none). */
 const char* cam_last_error(void);
 
