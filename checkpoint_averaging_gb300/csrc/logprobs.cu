@@ -36,12 +36,20 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kLpThreads = 512;
-constexpr int kLpWarps = kLpThreads / 32;
-constexpr int kLpGroups = 32;      // groups of 16 threads
-constexpr int kLpList = 1024;      // candidates a block keeps
+constexpr int kLpBatch = 4;          // vectors of a thread in flight while as many are summed
+constexpr int kLpMaxStream = 384;    // streaming threads of a block
+constexpr int kLpSelect = 2;         // selecting warps: even and odd rows
+constexpr int kLpBufs = 3;           // rows whose sums are handed over or being made
+constexpr int kLpUnits = 8;          // parts of a thread's share of a row, each with its largest logit
+constexpr int kLpMaxBlock = kLpMaxStream + 32 * kLpSelect;
+constexpr int kLpList = 1024;        // candidates a block's share of a row may have
+constexpr int kLpFewThreads = 96;    // threads whose vectors are scanned as a matter of course
 constexpr int kLpMaxCluster = 8;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kInf = INFINITY;
+// Logits beyond this are summed with care, by one warp; below its negative they are masks.
+constexpr float kHuge = 1e36f;
 
 struct LogprobArgs {
     const void* logits;
@@ -53,15 +61,51 @@ struct LogprobArgs {
     float* lse_lo;
     float* top_logp;
     int64_t* top_ids;
+    int32_t rows;
     int32_t vocab;
     int32_t top;
     int32_t cluster;
+    int32_t stream;   // streaming threads of a block, a multiple of 32
+    int32_t iters;    // vectors of a thread per row at most
+    int32_t unit;     // of which a unit has so many (a multiple of kLpBatch)
 };
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+    return m;
+}
+
+// Two binary32 in one 64-bit register and the operations on both at once.
+using Pair = unsigned long long;
+__device__ __forceinline__ Pair pair(float lo, float hi) {
+    Pair p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(lo), "f"(hi));
+    return p;
+}
+__device__ __forceinline__ void split(Pair p, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p));
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+    Pair d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+    Pair d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+    Pair d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
 }
 
 // One 16-byte vector of logits, widened on access.
@@ -75,6 +119,27 @@ struct Vec16<float> {
     __device__ __forceinline__ float get(int j) const {
         return __uint_as_float(j == 0 ? u.x : j == 1 ? u.y : j == 2 ? u.z : u.w);
     }
+    __device__ __forceinline__ float largest() const {  // NaN apart
+        return fmaxf(fmaxf(get(0), get(1)), fmaxf(get(2), get(3)));
+    }
+    // the largest of N vectors, NaN if one holds a NaN
+    template <int N>
+    static __device__ __forceinline__ float largest_nan(const Vec16 (&v)[N]) {
+        float m = v[0].get(0);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) m = max_nan(m, v[i].get(j));
+        return m;
+    }
+    __device__ __forceinline__ Vec16 held_finite() const {  // NaN stays
+        Vec16 v;
+        v.u = make_uint4(low(u.x), low(u.y), low(u.z), low(u.w));
+        return v;
+    }
+    static __device__ __forceinline__ uint32_t low(uint32_t w) {
+        return __float_as_uint(max_nan(__uint_as_float(w), -2e38f));
+    }
 };
 
 template <>
@@ -85,12 +150,38 @@ struct Vec16<uint16_t> {
         const uint32_t w = j < 2 ? u.x : j < 4 ? u.y : j < 6 ? u.z : u.w;
         return __uint_as_float((j & 1) ? w & 0xFFFF0000u : w << 16);
     }
+    __device__ __forceinline__ float largest() const {
+        const __nv_bfloat162 m =
+            __hmax2(__hmax2(as2(u.x), as2(u.y)), __hmax2(as2(u.z), as2(u.w)));
+        return fmaxf(__low2float(m), __high2float(m));
+    }
+    template <int N>
+    static __device__ __forceinline__ float largest_nan(const Vec16 (&v)[N]) {
+        __nv_bfloat162 m = as2(v[0].u.x);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            m = __hmax2_nan(__hmax2_nan(m, __hmax2_nan(as2(v[i].u.x), as2(v[i].u.y))),
+                            __hmax2_nan(as2(v[i].u.z), as2(v[i].u.w)));
+        return max_nan(__low2float(m), __high2float(m));
+    }
+    __device__ __forceinline__ Vec16 held_finite() const {  // NaN stays
+        Vec16 v;
+        v.u = make_uint4(low(u.x), low(u.y), low(u.z), low(u.w));
+        return v;
+    }
+    static __device__ __forceinline__ uint32_t low(uint32_t w) {
+        const __nv_bfloat162 m = __hmax2_nan(as2(w), as2(0xFF16FF16u));
+        return *reinterpret_cast<const uint32_t*>(&m);
+    }
+    static __device__ __forceinline__ __nv_bfloat162 as2(uint32_t w) {
+        return *reinterpret_cast<const __nv_bfloat162*>(&w);
+    }
 };
 
 template <typename T>
 __device__ __forceinline__ Vec16<T> load16(const T* p) {
     Vec16<T> v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
+    asm volatile("ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];"
                  : "=r"(v.u.x), "=r"(v.u.y), "=r"(v.u.z), "=r"(v.u.w)
                  : "l"(p));
     return v;
@@ -101,18 +192,57 @@ __device__ __forceinline__ float widen1(uint16_t v) {
     return __uint_as_float(static_cast<uint32_t>(v) << 16);
 }
 
-// A logit and its id as one whole number: larger for a larger logit (NaN
-// above +inf, -0 as +0) and, among equals, for a lower id. Never 0.
-__device__ __forceinline__ unsigned long long make_key(float x, uint32_t id) {
-    uint32_t u = __float_as_uint(x + 0.0f);
-    if ((u & 0x7FFFFFFFu) > 0x7F800000u) u = 0x7FFFFFFEu;  // (all ones stays free)
-    u ^= (u >> 31) ? 0xFFFFFFFFu : 0x80000000u;
-    return (static_cast<unsigned long long>(u) << 32) | (0xFFFFFFFFu - id);
+__device__ __forceinline__ float warp_max(float v) {  // NaN apart
+    float m;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+    return m;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
 }
 
-__device__ __forceinline__ float key_logit(unsigned long long key) {
+// Named barriers of a block. Full: a row's sums handed to its selecting warp; the
+// rows that share one (every sixth) have the same selecting warp and the same
+// buffer, so no warp comes to it early in another's place. Free: a buffer handed
+// back.
+constexpr int kLpFull = kLpSelect * kLpBufs;
+constexpr int kBarFull = 1, kBarFree = kBarFull + kLpFull;
+static_assert(kBarFree + kLpBufs <= 16, "a block has 16 barriers");
+__device__ __forceinline__ void bar_sync(int id, int n) {
+    asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(int id, int n) {
+    asm volatile("barrier.cta.arrive %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// A logit and its id as one whole number: larger for a larger logit (NaN
+// above +inf, -0 as +0) and, among equals, for a lower id. Never 0 nor ~0.
+using Key = unsigned long long;
+__device__ __forceinline__ Key make_key(float x, uint32_t id) {
+    uint32_t u = __float_as_uint(x + 0.0f);
+    if ((u & 0x7FFFFFFFu) > 0x7F800000u) u = 0x7FFFFFFEu;
+    u ^= (u >> 31) ? 0xFFFFFFFFu : 0x80000000u;
+    return (static_cast<Key>(u) << 32) | (0xFFFFFFFFu - id);
+}
+__device__ __forceinline__ float key_logit(Key key) {
     const uint32_t u = static_cast<uint32_t>(key >> 32);
     return __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xFFFFFFFFu));
+}
+__device__ __forceinline__ int64_t key_id(Key key) {
+    return 0xFFFFFFFFu - static_cast<uint32_t>(key);
+}
+__device__ __forceinline__ Key warp_max_key(Key v) {
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) v = max(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    return v;
 }
 
 // The n-th largest (n = 1..32) of the warp's 32 values, on every lane: a
@@ -132,235 +262,557 @@ __device__ __forceinline__ float nth_of_warp(float v, int n) {
 
 // What a block knows of its share of a row.
 struct Share {
-    float m;    // largest logit (NaN apart), -inf where there is none
-    float c;    // logits equal to m
-    float r;    // sum of exp(x - m) over the others
-    float t;    // sum of exp(x - m) (x - m)
+    float m;  // largest logit (NaN apart), -inf where there is none
+    float c;  // logits equal to m
+    float r;  // sum of exp(x - m) over the others
+    float t;  // sum of exp(x - m) (x - m)
 };
 
-// T: the logits' type. NV: vectors each thread holds in registers; 0 reads
-// the share from memory (its second and later readings from L2) instead.
-template <typename T, int NV>
-__global__ void __launch_bounds__(kLpThreads, NV > 0 && NV <= 8 ? 2 : 1)
-    token_logprobs(const __grid_constant__ LogprobArgs a) {
+// What a streaming warp hands over of its vectors of a row. Sums are of
+// 2^(x log2(e) - m log2(e)) and of that times its exponent; those of the lane
+// that holds m stand apart, so that a confident row can leave m itself out.
+struct WarpSums {
+    float m;             // largest logit
+    float s, t;          // sums of the lanes whose largest is less
+    float top_s, top_t;  // and of the others
+    int top_lane;        // one of the others
+};
+
+struct LogprobShared {
+    WarpSums warps[kLpBufs][kLpMaxStream / 32];
+    float thread_max[kLpBufs][kLpMaxStream];  // largest logit of each thread's vectors
+    Key list[kLpSelect][kLpList];
+    Key best[kLpSelect][CAM_LOGPROBS_MAX_TOP];
+    Key all_best[kLpMaxCluster][CAM_LOGPROBS_MAX_TOP];  // the leader's: every block's
+    Share shares[kLpMaxCluster];                        // the leader's
+    uint16_t threads[kLpSelect][kLpMaxStream];
+    uint16_t units[kLpSelect][kLpFewThreads * kLpUnits];
+    // then, [kLpBufs][stream][kLpUnits]: the largest logit of each unit
+};
+
+// Where a row's vectors lie: [0, head) and the last `tail` logits singly (by
+// the leader of the cluster), 16-byte vectors between, dealt out to the
+// cluster's streaming threads in turn.
+template <typename T>
+struct RowPlan {
+    const T* x;
+    int head, n_vec, tail;
+    __device__ __forceinline__ RowPlan(const T* row, int vocab) : x(row) {
+        head = min(vocab, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) /
+                              static_cast<int>(sizeof(T)));
+        n_vec = (vocab - head) / Vec16<T>::kN;
+        tail = vocab - head - n_vec * Vec16<T>::kN;
+    }
+    __device__ __forceinline__ int single_id(int i, int vocab) const {  // i in [0, head + tail)
+        return i < head ? i : vocab - tail + (i - head);
+    }
+};
+
+// The block's largest logits into `out[0..top)`, in order (0 where there are
+// none), by one warp. `bad`: the share holds a NaN.
+template <typename T>
+__device__ __noinline__ void select(const LogprobArgs& a, LogprobShared& sh, const RowPlan<T>& row,
+                                    int par, int buf, int rank, bool bad, Key* out) {
+    Key* list = sh.list[par];
+    uint16_t* threads = sh.threads[par];
+    uint16_t* units = sh.units[par];
+    const float* unit_max =
+        reinterpret_cast<const float*>(&sh + 1) + buf * a.stream * kLpUnits;
     constexpr int kN = Vec16<T>::kN;
-    constexpr float kInf = INFINITY;
-    __shared__ float group_max[kLpGroups];
-    __shared__ float warp_sums[3][kLpWarps];
-    __shared__ unsigned long long list[kLpList];
-    __shared__ unsigned long long best[kLpMaxCluster][CAM_LOGPROBS_MAX_TOP];  // the leader's
-    __shared__ Share shares[kLpMaxCluster];                                   // the leader's
-    __shared__ unsigned long long round_best[kLpWarps];
-    __shared__ int n_listed;
-
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int rank = a.cluster > 1 ? static_cast<int>(cg::this_cluster().block_rank()) : 0;
-    const int64_t row = blockIdx.x / a.cluster;
-    const T* x = static_cast<const T*>(a.logits) + row * a.stride;
-    // [0, head) and the last `tail` logits singly, by the leader; vectors between
-    const int head = min(a.vocab, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) /
-                                      static_cast<int>(sizeof(T)));
-    const int n_vec = (a.vocab - head) / kN;
-    const int tail = a.vocab - head - n_vec * kN;
-    const T* xv = x + head;
-    const int v0 = rank * kLpThreads + tid, v_step = a.cluster * kLpThreads;
-
-    float single = -kInf;  // this thread's single logit
-    int single_id = -1;
-    if (rank == 0 && tid < head + tail) {
-        single_id = tid < head ? tid : a.vocab - tail + (tid - head);
-        single = widen1(x[single_id]);
-    }
-    Vec16<T> held[NV > 0 ? NV : 1];
-    if constexpr (NV > 0) {
-        const uint32_t pad = sizeof(T) == 4 ? 0xFF800000u : 0xFF80FF80u;  // -inf
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            held[i].u = make_uint4(pad, pad, pad, pad);
-            if (v0 + i * v_step < n_vec) held[i] = load16(xv + int64_t(v0 + i * v_step) * kN);
+    constexpr uint32_t kAll = 0xFFFFFFFFu;
+    const int lane = threadIdx.x & 31;
+    const uint32_t below = (1u << lane) - 1u;
+    const int singles = rank == 0 ? row.head + row.tail : 0;
+    const int across = a.stream * a.cluster, n_warps = a.stream >> 5;
+    const float* thread_max = sh.thread_max[buf];
+    int n = 0;  // candidates so far, the same on every lane
+    // each lane's logits of `hits` (bit j: id + j, read by get(j)) onto the list
+    auto put = [&](uint32_t hits, int id, auto&& get) {
+        for (uint32_t who = __ballot_sync(kAll, hits != 0); who != 0;
+             who = __ballot_sync(kAll, hits != 0)) {
+            if (hits != 0) {
+                const int j = __ffs(hits) - 1, at = n + __popc(who & below);
+                if (at < kLpList) list[at] = make_key(get(j), static_cast<uint32_t>(id + j));
+                hits &= hits - 1;
+            }
+            n += __popc(who);
         }
-    }
-    // f(vector, id of its first logit) over this thread's vectors
-    auto each = [&](auto&& f) {
-        if constexpr (NV > 0) {
+    };
+    auto vector_hits = [&](const Vec16<T>& v, bool valid, auto&& wanted) {
+        uint32_t hits = 0;
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (v0 + i * v_step < n_vec) f(held[i], head + (v0 + i * v_step) * kN);
+        for (int j = 0; j < kN; ++j) hits |= (valid && wanted(v.get(j))) ? 1u << j : 0u;
+        return hits;
+    };
+    if (!bad) {
+        // 32 sets of threads, or the warps where they suffice: the top-th largest of the sets'
+        // largest is a bound that at least `top` logits reach
+        float m = -kInf;
+        if (a.top <= n_warps) {
+            if (lane < n_warps) m = sh.warps[buf][lane].m;
         } else {
-            for (int v = v0; v < n_vec; v += v_step) f(load16(xv + int64_t(v) * kN), head + v * kN);
+            for (int j = lane; j < a.stream; j += 32) m = fmaxf(m, thread_max[j]);
         }
-    };
-
-    // the largest logit (fmaxf drops NaN: the sums show it)
-    float m = single == single ? single : -kInf;
-    each([&](const Vec16<T>& v, int) {
+        const float bound = a.top == 1 ? warp_max(m) : nth_of_warp(m, a.top);
+        if (singles > 0) {
+            const int id = lane < singles ? row.single_id(lane, a.vocab) : 0;
+            const float v = lane < singles ? widen1(row.x[id]) : 0.0f;
+            put(lane < singles && v >= bound ? 1u : 0u, id, [&](int) { return v; });
+        }
+        // the threads that reach the bound (or pass it)
+        int n_thr = 0;
+        auto list_threads = [&](bool strictly) {
+            n_thr = 0;
+            const float w = lane < n_warps ? sh.warps[buf][lane].m : -kInf;
+            uint32_t warps =
+                __ballot_sync(kAll, lane < n_warps && (strictly ? w > bound : w >= bound));
+            while (warps != 0) {
+                float v[4];
+                int at[4];
 #pragma unroll
-        for (int j = 0; j < kN; ++j) m = fmaxf(m, v.get(j));
+                for (int k = 0; k < 4; ++k) {
+                    at[k] = warps != 0 ? (__ffs(warps) - 1) * 32 + lane : -1;
+                    warps &= warps - 1;
+                    v[k] = at[k] >= 0 ? thread_max[at[k]] : -kInf;
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const bool hit = at[k] >= 0 && (strictly ? v[k] > bound : v[k] >= bound);
+                    const uint32_t who = __ballot_sync(kAll, hit);
+                    if (hit) threads[n_thr + __popc(who & below)] = static_cast<uint16_t>(at[k]);
+                    n_thr += __popc(who);
+                }
+            }
+            __syncwarp();
+        };
+        // what of their vectors does: the units that reach it, four lanes to a unit's vectors
+        auto scan_threads = [&](auto&& wanted) {
+            for (int q0 = 0; q0 < n_thr; q0 += kLpFewThreads) {
+                const int pairs = min(n_thr - q0, kLpFewThreads) * kLpUnits;
+                int n_units = 0;
+                for (int u0 = 0; u0 < pairs; u0 += 32) {
+                    const int u = u0 + lane;
+                    int at = 0;
+                    bool hit = false;
+                    if (u < pairs) {
+                        at = threads[q0 + u / kLpUnits] * kLpUnits + u % kLpUnits;
+                        hit = wanted(unit_max[at]);
+                    }
+                    const uint32_t who = __ballot_sync(kAll, hit);
+                    if (hit) units[n_units + __popc(who & below)] = static_cast<uint16_t>(at);
+                    n_units += __popc(who);
+                }
+                __syncwarp();
+                for (int i0 = 0; i0 < a.unit; i0 += 4)
+                    for (int u0 = 0; u0 < n_units; u0 += 32) {
+                        Vec16<T> v[4];
+                        int w[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int u = u0 + 8 * k + (lane >> 2);
+                            w[k] = row.n_vec;
+                            if (u < n_units) {
+                                const int at = units[u], i = at % kLpUnits * a.unit + i0 + (lane & 3);
+                                if (i < a.iters)
+                                    w[k] = i * across + rank * a.stream + at / kLpUnits;
+                            }
+                            if (w[k] < row.n_vec) v[k] = load16(row.x + row.head + w[k] * kN);
+                        }
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (u0 + 8 * k < n_units)
+                                put(vector_hits(v[k], w[k] < row.n_vec, wanted),
+                                    row.head + w[k] * kN, [&](int j) { return v[k].get(j); });
+                    }
+                __syncwarp();
+            }
+        };
+        list_threads(false);
+        if (n_thr <= kLpFewThreads) {
+            scan_threads([&](float v) { return v >= bound; });
+        } else {
+            // many logits equal to the bound: those above it from their threads, and of the
+            // equal ones the first `top` in the order of ids
+            list_threads(true);
+            scan_threads([&](float v) { return v > bound; });
+            const int enough = n + a.top;
+            for (int u = lane; n < enough; u += 32) {
+                // the share's vector number u, in the order of ids
+                const int w = (u / a.stream) * across + rank * a.stream + u % a.stream;
+                if (__all_sync(kAll, w >= row.n_vec)) break;
+                Vec16<T> v;
+                if (w < row.n_vec) v = load16(row.x + row.head + w * kN);
+                put(vector_hits(v, w < row.n_vec, [&](float e) { return e == bound; }),
+                    row.head + w * kN, [&](int j) { return v.get(j); });
+            }
+        }
+        __syncwarp();
+    }
+    if (!bad && n <= kLpList) {
+        if (lane < a.top && lane >= n) out[lane] = 0;
+        if (n <= 128) {  // a candidate's place is the number before it
+            for (int i = lane; i < n; i += 32) {
+                const Key key = list[i];
+                int place = 0;
+#pragma unroll 4
+                for (int k = 0; k < n; ++k) place += list[k] > key;
+                if (place < a.top) out[place] = key;
+            }
+        } else {
+            Key last = ~0ull;
+            for (int p = 0; p < a.top; ++p) {
+                Key key = 0;
+                for (int i = lane; i < n; i += 32) {
+                    const Key u = list[i];
+                    if (u < last) key = max(key, u);
+                }
+                last = warp_max_key(key);
+                if (lane == 0) out[p] = last;
+            }
+        }
+    } else {
+        // a NaN, or more candidates than the list holds: one maximum at a time over the share
+        Key last = ~0ull;
+        for (int p = 0; p < a.top; ++p) {
+            Key key = 0;
+            auto look = [&](float v, int id) {
+                const Key u = make_key(v, static_cast<uint32_t>(id));
+                if (u < last) key = max(key, u);
+            };
+            for (int i = lane; i < singles; i += 32) {
+                const int id = row.single_id(i, a.vocab);
+                look(widen1(row.x[id]), id);
+            }
+            for (int u = lane;; u += 32) {
+                const int w = (u / a.stream) * across + rank * a.stream + u % a.stream;
+                if (w >= row.n_vec) break;
+                const Vec16<T> v = load16(row.x + row.head + w * kN);
+#pragma unroll
+                for (int j = 0; j < kN; ++j) look(v.get(j), row.head + w * kN + j);
+            }
+            last = warp_max_key(key);
+            if (lane == 0) out[p] = last;
+        }
+    }
+    __syncwarp();
+}
+
+// A share summed by one warp, its largest logit first: for rows with a NaN or
+// logits beyond kHuge.
+template <typename T>
+__device__ __noinline__ Share careful(const LogprobArgs& a, const RowPlan<T>& row, int rank) {
+    constexpr int kN = Vec16<T>::kN;
+    const int lane = threadIdx.x & 31, singles = rank == 0 ? row.head + row.tail : 0;
+    const int across = a.stream * a.cluster;
+    auto each = [&](auto&& f) {
+        for (int i = lane; i < singles; i += 32) f(widen1(row.x[row.single_id(i, a.vocab)]));
+        for (int i = 0; i < a.iters; ++i)
+            for (int j = lane; j < a.stream; j += 32) {
+                const int w = i * across + rank * a.stream + j;
+                if (w >= row.n_vec) continue;
+                const Vec16<T> v = load16(row.x + row.head + int64_t(w) * kN);
+#pragma unroll
+                for (int e = 0; e < kN; ++e) f(v.get(e));
+            }
+    };
+    float m = -kInf, r = 0.0f, c = 0.0f, t = 0.0f;
+    each([&](float x) {
+        m = fmaxf(m, x);
+        if (x != x || x == kInf) r = NAN;
     });
-    const float mine = m;
-#pragma unroll
-    for (int o = 1; o < 16; o *= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    if ((lane & 15) == 0) group_max[tid >> 4] = m;
-    if (tid == 0) n_listed = 0;
-    __syncthreads();
-    m = group_max[lane];
-    float bound = kInf;
-    if (a.top > 1) bound = nth_of_warp(m, a.top);
-#pragma unroll
-    for (int o = 1; o < 32; o *= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    if (a.top == 1) bound = m;
-    const float zero = m == -kInf ? 0.0f : m;  // what to subtract
-
-    // the sums, and the logits that reach the bound
-    float c = 0.0f, r = 0.0f, t = 0.0f;
-    auto put = [&](float v, int id) {
-        const int at = atomicAdd(&n_listed, 1);
-        if (at < kLpList) list[at] = make_key(v, static_cast<uint32_t>(id));
-    };
-    auto add = [&](float v, bool may_be_largest) {
-        const float d = v - zero;
-        const float e = ex2(d * kLog2e);
-        if (may_be_largest && v == m) {
+    m = warp_max(m);
+    const float from = m == -kInf ? 0.0f : m;
+    each([&](float x) {
+        if (x == m) {
             if (m != -kInf) c += 1.0f;
         } else {
+            const float d = max_nan(x - from, -200.0f), e = ex2(d * kLog2e);
             r += e;
-            t = fmaf(e, fmaxf(d, -1e30f), t);  // 0 for a logit of -inf
+            t += e * d;
         }
+    });
+    return Share{m, warp_sum(c), warp_sum(r), warp_sum(t)};
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kLpMaxBlock, 2)
+    token_logprobs(const __grid_constant__ LogprobArgs a) {
+    constexpr int kN = Vec16<T>::kN;
+    extern __shared__ __align__(128) uint8_t smem[];
+    LogprobShared& sh = *reinterpret_cast<LogprobShared*>(smem);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int n_warps = a.stream >> 5, both = a.stream + 32;
+    const bool clustered = a.cluster > 1;  // (then a block has one row)
+    const int rank = clustered ? static_cast<int>(cg::this_cluster().block_rank()) : 0;
+    const int first = blockIdx.x / a.cluster, step = gridDim.x / a.cluster;
+    const int n_rows = first < a.rows ? (a.rows - first - 1) / step + 1 : 0;
+    const int across = a.stream * a.cluster;
+    const T* logits = static_cast<const T*>(a.logits);
+    auto plan = [&](int k) {
+        return RowPlan<T>(logits + (first + int64_t(k) * step) * a.stride, a.vocab);
     };
-    if (mine == m) {
-        each([&](const Vec16<T>& v, int) {
-#pragma unroll
-            for (int j = 0; j < kN; ++j) add(v.get(j), true);
-        });
-    } else {
-        each([&](const Vec16<T>& v, int) {
-#pragma unroll
-            for (int j = 0; j < kN; ++j) add(v.get(j), false);
-        });
-    }
-    if (single_id >= 0) add(single, true);
-    if (a.top > 0 && mine >= bound) {
-        each([&](const Vec16<T>& v, int id) {
-#pragma unroll
-            for (int j = 0; j < kN; ++j)
-                if (v.get(j) >= bound) put(v.get(j), id + j);
-        });
-        if (single_id >= 0 && single >= bound) put(single, single_id);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o /= 2) {
-        c += __shfl_xor_sync(0xFFFFFFFFu, c, o);
-        r += __shfl_xor_sync(0xFFFFFFFFu, r, o);
-        t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
-    }
-    if (lane == 0) warp_sums[0][warp] = c, warp_sums[1][warp] = r, warp_sums[2][warp] = t;
-    __syncthreads();
-    c = r = t = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kLpWarps; ++w)
-        c += warp_sums[0][w], r += warp_sums[1][w], t += warp_sums[2][w];
-
-    cg::cluster_group cluster = cg::this_cluster();
-    unsigned long long* places =
-        a.cluster > 1 ? cluster.map_shared_rank(&best[rank][0], 0) : &best[0][0];
-    if (a.cluster > 1) {
-        cluster.sync();  // the leader has started
-        if (tid == 0) *cluster.map_shared_rank(&shares[rank], 0) = Share{m, c, r, t};
-    } else if (tid == 0) {
-        shares[0] = Share{m, c, r, t};
+    if (clustered) {  // every block of the cluster has started
+        cluster_arrive();
+        cluster_wait();
     }
 
-    // the block's own largest, in order
-    const int n = n_listed;
-    if (a.top > 0) {
-        if (n <= kLpList && r == r) {
-            if (tid < a.top && tid >= n) places[tid] = 0;
-            for (int i = tid; i < n; i += kLpThreads) {
-                const unsigned long long key = list[i];
-                int place = 0;
-                for (int k = 0; k < n; ++k) place += list[k] > key;
-                if (place < a.top) places[place] = key;
+    if (warp < n_warps) {
+        // ---- streaming ---------------------------------------------------------------
+        // The sums are taken relative to a reference of the thread's own: its first batch's
+        // largest logit, moved up when a batch passes it by 16, so that no term overflows and
+        // none that counts is lost. No thread waits for another within a row.
+        using Batch = Vec16<T>[kLpBatch];
+        const int w0 = rank * a.stream + warp * 32;  // the warp's first vector
+        int l_row = 0, l_w = w0, l_vecs = 0;         // the next batch to load
+        const T* l_at = nullptr;
+        auto load = [&](Batch& v, int& w, int& n_vec) {
+            if (l_w == w0 && l_row < n_rows) {
+                const RowPlan<T> p = plan(l_row);
+                l_vecs = p.n_vec;
+                l_at = p.x + p.head + int64_t(w0 + lane) * kN;
             }
-        } else {
-            unsigned long long last = ~0ull;
-            for (int k = 0; k < a.top; ++k) {
-                unsigned long long key = 0;
-                auto look = [&](float v, int id) {
-                    const unsigned long long u = make_key(v, static_cast<uint32_t>(id));
-                    if (u < last && u > key) key = u;
-                };
-                each([&](const Vec16<T>& v, int id) {
+            w = l_w;
+            n_vec = l_row < n_rows ? l_vecs : 0;
+            constexpr uint32_t kPad = sizeof(T) == 4 ? 0xFF800000u : 0xFF80FF80u;  // -inf
 #pragma unroll
-                    for (int j = 0; j < kN; ++j) look(v.get(j), id + j);
-                });
-                if (single_id >= 0) look(single, single_id);
-#pragma unroll
-                for (int o = 16; o > 0; o /= 2)
-                    key = max(key, __shfl_xor_sync(0xFFFFFFFFu, key, o));
-                __syncthreads();
-                if (lane == 0) round_best[warp] = key;
-                __syncthreads();
-#pragma unroll
-                for (int w = 0; w < kLpWarps; ++w) key = max(key, round_best[w]);
-                if (tid == 0) places[k] = key;
-                last = key;
-                if (key == 0) last = 1;  // none left: nothing is below 1 but 0
+            for (int j = 0; j < kLpBatch; ++j) {
+                v[j].u = make_uint4(kPad, kPad, kPad, kPad);
+                if (w + lane + j * across < n_vec) v[j] = load16(l_at + int64_t(j) * across * kN);
             }
-        }
-    }
-    if (a.cluster > 1) cluster.sync();
-    else __syncthreads();
-    if (rank != 0) return;
+            l_w += kLpBatch * across;
+            l_at += int64_t(kLpBatch) * across * kN;
+            if (l_w >= a.iters * across + w0) l_w = w0, ++l_row;
+        };
 
-    // the row, from its shares
-    float M = -kInf;
-    for (int k = 0; k < a.cluster; ++k) M = fmaxf(M, shares[k].m);
-    c = r = t = 0.0f;
-    for (int k = 0; k < a.cluster; ++k) {
-        const Share s = shares[k];
-        if (s.m == M) {
-            c += s.c, r += s.r, t += s.t;
+        const Pair log2e = pair(kLog2e, kLog2e);
+        float m = -kInf, limit = -kHuge, ref = 0.0f;  // ref: minus the reference times log2(e)
+        float unit_m = -kInf;                         // the largest of the unit under way
+        const int unit_batches = a.unit / kLpBatch;
+        int unit_left = unit_batches;
+        float* unit_max = reinterpret_cast<float*>(&sh + 1) + tid * kLpUnits;
+        float* unit_at = unit_max;
+        Pair s2 = pair(0.0f, 0.0f), t2 = s2;
+        auto add = [&](const Batch& v, int w, int n_vec) {
+            const float big = Vec16<T>::largest_nan(v);
+            if (!(big <= limit)) {
+                if (big < kHuge) {
+                    const float up = -big * kLog2e, by = up - ref;
+                    const float f = limit == -kHuge ? 0.0f : ex2(by);
+                    s2 = mul2(s2, pair(f, f));
+                    t2 = limit == -kHuge ? t2 : fma2(t2, pair(f, f), mul2(s2, pair(by, by)));
+                    ref = up;
+                    limit = big + 16.0f;
+                } else {  // NaN, or too large
+                    s2 = pair(NAN, NAN);
+                }
+            }
+            m = fmaxf(m, big);
+            unit_m = fmaxf(unit_m, big);
+            if (--unit_left == 0) {
+                *unit_at++ = unit_m;
+                unit_m = -kInf, unit_left = unit_batches;
+            }
+            const Pair ref2 = pair(ref, ref);
+#pragma unroll
+            for (int j = 0; j < kLpBatch; ++j) {
+                if (w + j * across >= n_vec) break;  // (the whole warp's)
+                // a mask held finite: its exponent times its term is then 0 and not NaN
+                const Vec16<T> u = v[j].held_finite();
+#pragma unroll
+                for (int q = 0; q < kN; q += 2) {
+                    const Pair y = fma2(pair(u.get(q), u.get(q + 1)), log2e, ref2);
+                    float y0, y1;
+                    split(y, y0, y1);
+                    const Pair e = pair(ex2(y0), ex2(y1));
+                    s2 = add2(s2, e);
+                    t2 = fma2(e, y, t2);
+                }
+            }
+        };
+        auto finish = [&](int k) {  // the warp's sums of row k, relative to its largest
+            const int buf = k % kLpBufs;
+            float s, t, hi;
+            split(s2, s, hi);
+            s += hi;
+            split(t2, t, hi);
+            t += hi;
+            const float wm = warp_max(m);
+            const bool top = m == wm;
+            const float y = fmaf(wm, kLog2e, ref);  // >= 0 where the lane has a reference
+            const float f = s == 0.0f ? 0.0f : ex2(-y);
+            t = s == 0.0f ? 0.0f : f * fmaf(-y, s, t);
+            s *= f;
+            const float rest_s = warp_sum(top ? 0.0f : s), rest_t = warp_sum(top ? 0.0f : t);
+            const uint32_t who = __ballot_sync(0xFFFFFFFFu, top);
+            const int top_lane = __ffs(who) - 1;
+            float top_s = s, top_t = t;  // (on the top lane)
+            if (who & (who - 1)) {
+                top_s = warp_sum(top ? s : 0.0f);
+                top_t = warp_sum(top ? t : 0.0f);
+            }
+            if (unit_left < unit_batches) *unit_at = unit_m;
+            sh.thread_max[buf][tid] = m;
+            if (lane == top_lane)
+                sh.warps[buf][warp] = WarpSums{wm, rest_s, rest_t, top_s, top_t, top_lane};
+            bar_arrive(kBarFull + k % kLpFull, both);
+            m = -kInf, limit = -kHuge, ref = 0.0f;
+            s2 = t2 = pair(0.0f, 0.0f);
+            // the next row's buffer
+            unit_m = -kInf, unit_left = unit_batches;
+            const int next = (k + 1) % kLpBufs;
+            unit_at = unit_max + next * a.stream * kLpUnits;
+            if (k + 1 >= kLpBufs && k + 1 < n_rows) bar_sync(kBarFree + next, both);
+        };
+
+        Batch v0, v1;
+        int at0, at1, n0, n1;
+        const int batches = (a.iters + kLpBatch - 1) / kLpBatch;
+        int left = batches, k = 0;
+        load(v0, at0, n0);
+        while (k < n_rows) {
+            load(v1, at1, n1);
+            add(v0, at0, n0);
+            if (--left == 0) {
+                finish(k);
+                left = batches;
+                if (++k == n_rows) break;
+            }
+            load(v0, at0, n0);
+            add(v1, at1, n1);
+            if (--left == 0) finish(k), left = batches, ++k;
+        }
+        if (clustered) {
+            __syncwarp();
+            cluster_arrive();
+            cluster_wait();
+        }
+        return;
+    }
+
+    // ---- a selecting warp: every second row's results while the next rows stream ----
+    const int par = warp - n_warps;
+    for (int k = par; k < n_rows; k += kLpSelect) {
+        const int buf = k % kLpBufs;
+        const int64_t r_at = first + int64_t(k) * step;
+        const RowPlan<T> row = plan(k);
+        const int singles = rank == 0 ? row.head + row.tail : 0;
+        // (asked for early: these loads overlap the wait)
+        const int64_t token = a.logp && rank == 0 ? a.tokens[r_at] : -1;
+        const float single = lane < singles ? widen1(row.x[row.single_id(lane, a.vocab)]) : -kInf;
+        const float x_token = token >= 0 && token < a.vocab ? widen1(row.x[token]) : 0.0f;
+        bar_sync(kBarFull + k % kLpFull, both);
+        const WarpSums ws = lane < n_warps ? sh.warps[buf][lane]
+                                           : WarpSums{-kInf, 0.0f, 0.0f, 0.0f, 0.0f, 0};
+        Share s;
+        s.m = fmaxf(warp_max(ws.m), warp_max(fmaxf(single, -kInf)));
+        const float from = s.m == -kInf ? 0.0f : s.m;
+        // the warps' sums and the single logits, relative to m
+        const float d = fmaxf(ws.m - from, -1e30f) * kLog2e, f = ex2(d);
+        const float one_y = max_nan((single - from) * kLog2e, -150.0f), one = ex2(one_y);
+        s.c = 0.0f;
+        s.r = warp_sum(f * (ws.s + ws.top_s) + one);
+        s.t = warp_sum(f * (ws.t + ws.top_t + d * (ws.s + ws.top_s)) + one * one_y) * kLn2;
+        bool bad = false;
+        if (!(s.r < 1.5f) || s.m == -kInf) {
+            // (a sum that lost its row: a NaN, logits beyond kHuge either way)
+            bad = s.r != s.r || fabsf(s.m) >= kHuge;
+            if (bad && !(s.m == -kInf && s.r == 0.0f)) s = careful<T>(a, row, rank);
+            bad = s.r != s.r;
+        } else if (fabsf(s.m) >= kHuge) {
+            s = careful<T>(a, row, rank);
+            bad = s.r != s.r;
         } else {
-            const float d = fmaxf(s.m - M, -1e30f), e = ex2(d * kLog2e);
-            r += e * (s.c + s.r);
-            t += e * (s.t + d * (s.c + s.r));
+            // One logit has most of the probability. What the others add to it would drown in
+            // the sum, so the sum is taken again without it: its own thread's vectors are read
+            // once more, all else is apart already.
+            s.c = 1.0f;
+            const bool mine = lane < n_warps && ws.m == s.m;
+            float r = mine ? ws.s : f * (ws.s + ws.top_s);
+            float t = mine ? ws.t : f * (ws.t + ws.top_t + d * (ws.s + ws.top_s));
+            if (single != s.m) r += one, t += one * one_y;
+            const uint32_t who = __ballot_sync(0xFFFFFFFFu, mine);
+            if (who != 0) {
+                const int w = __ffs(who) - 1;
+                const int v0 = rank * a.stream + w * 32 + __shfl_sync(0xFFFFFFFFu, ws.top_lane, w);
+                for (int i = lane; i < a.iters; i += 32) {
+                    if (v0 + i * across >= row.n_vec) break;
+                    const Vec16<T> v = load16(row.x + row.head + int64_t(v0 + i * across) * kN);
+#pragma unroll
+                    for (int j = 0; j < kN; ++j) {
+                        if (v.get(j) == s.m) continue;
+                        const float y = fmaxf((v.get(j) - s.m) * kLog2e, -150.0f), e = ex2(y);
+                        r += e;
+                        t += e * y;
+                    }
+                }
+            }
+            s.r = warp_sum(r);
+            s.t = warp_sum(t) * kLn2;
         }
-    }
-    if (M == kInf) r = NAN;
-    // no distribution: c and r are 0; a NaN or +inf: r is NaN
-    const bool dead = M == -kInf && r == 0.0f;
-    const float log_s = dead ? 0.0f : log1pf((c - 1.0f) + r);
-    auto logp_of = [&](float v) { return dead ? -kInf : (v - M) - log_s; };
-    if (tid == 0) {
-        const float lse = dead ? -kInf : M + log_s;
-        if (a.lse) a.lse[row] = lse;
-        if (a.lse_lo) {  // what the sum's rounding left out, exactly (no order of the two is needed)
-            const float b = __fsub_rn(lse, M);
-            const float lo = __fadd_rn(__fsub_rn(M, __fsub_rn(lse, b)), __fsub_rn(log_s, b));
-            a.lse_lo[row] = isfinite(lse) ? lo : 0.0f;
+        Key* best = sh.best[par];
+        if (a.top > 0) {
+            if (clustered) best = cg::this_cluster().map_shared_rank(&sh.all_best[rank][0], 0);
+            select<T>(a, sh, row, par, buf, rank, bad, best);
         }
-        if (a.entropy) a.entropy[row] = dead ? 0.0f : log_s - t / (c + r);
-        if (a.logp) {
-            const int64_t token = a.tokens[row];
-            float p = 0.0f;
-            if (token >= a.vocab) p = NAN;
-            else if (token >= 0) p = logp_of(widen1(x[token]));
-            a.logp[row] = p;
+        if (k + kLpBufs < n_rows) bar_arrive(kBarFree + buf, both);
+        if (clustered) {
+            if (lane == 0) *cg::this_cluster().map_shared_rank(&sh.shares[rank], 0) = s;
+            __syncwarp();
+            cluster_arrive();
+            cluster_wait();
+            if (rank != 0) return;
+            // the row from its shares
+            float M = -kInf;
+            for (int j = 0; j < a.cluster; ++j) M = fmaxf(M, sh.shares[j].m);
+            Share all{M, 0.0f, 0.0f, 0.0f};
+            for (int j = 0; j < a.cluster; ++j) {
+                const Share o = sh.shares[j];
+                if (o.m == M) {
+                    all.c += o.c, all.r += o.r, all.t += o.t;
+                } else {
+                    const float d = fmaxf(o.m - M, -1e30f), e = ex2(d * kLog2e);
+                    all.r += e * (o.c + o.r);
+                    all.t += e * (o.t + d * (o.c + o.r));
+                }
+            }
+            s = all;
         }
-    }
-    if (a.top > 0) {
-        const unsigned long long* all = &best[0][0];
-        for (int i = tid; i < a.cluster * a.top; i += kLpThreads) {
-            const unsigned long long key = all[i / a.top * CAM_LOGPROBS_MAX_TOP + i % a.top];
+        if (s.m == kInf) s.r = NAN;
+        // no distribution: c and r are 0; a NaN or +inf: r is NaN
+        const bool dead = s.m == -kInf && s.r == 0.0f;
+        const float log_s = dead ? 0.0f : log1pf((s.c - 1.0f) + s.r);
+        auto logp_of = [&](float v) { return dead ? -kInf : (v - s.m) - log_s; };
+        if (lane == 0) {
+            const float lse = dead ? -kInf : s.m + log_s;
+            if (a.lse) a.lse[r_at] = lse;
+            if (a.lse_lo) {  // what the sum's rounding left out, exactly (the order of the two is free)
+                const float b = __fsub_rn(lse, s.m);
+                const float lo = __fadd_rn(__fsub_rn(s.m, __fsub_rn(lse, b)), __fsub_rn(log_s, b));
+                a.lse_lo[r_at] = isfinite(lse) ? lo : 0.0f;
+            }
+            if (a.entropy) a.entropy[r_at] = dead ? 0.0f : log_s - s.t / (s.c + s.r);
+            if (a.logp)
+                a.logp[r_at] = token >= a.vocab ? NAN : token >= 0 ? logp_of(x_token) : 0.0f;
+        }
+        for (int i = lane; i < a.cluster * a.top; i += 32) {
+            const Key key = clustered ? sh.all_best[i / a.top][i % a.top] : best[i];
             if (key == 0) continue;
-            int place = 0;
-            for (int k = 0; k < a.cluster; ++k)
-                for (int j = 0; j < a.top; ++j) place += all[k * CAM_LOGPROBS_MAX_TOP + j] > key;
-            if (place >= a.top) continue;
-            if (a.top_ids)
-                a.top_ids[row * a.top + place] = 0xFFFFFFFFu - static_cast<uint32_t>(key);
-            if (a.top_logp) a.top_logp[row * a.top + place] = logp_of(key_logit(key));
+            int place = i;
+            if (clustered) {
+                place = 0;
+                for (int j = 0; j < a.cluster; ++j)
+                    for (int q = 0; q < a.top; ++q) place += sh.all_best[j][q] > key;
+                if (place >= a.top) continue;
+            }
+            if (a.top_ids) a.top_ids[r_at * a.top + place] = key_id(key);
+            if (a.top_logp) a.top_logp[r_at * a.top + place] = logp_of(key_logit(key));
         }
+        __syncwarp();
+    }
+    if (clustered && par >= n_rows) {  // the selecting warps without the cluster's one row
+        cluster_arrive();
+        cluster_wait();
     }
 }
 
@@ -479,14 +931,6 @@ __global__ void __launch_bounds__(kLbThreads)
     }
 }
 
-template <typename T>
-const void* forward_kernel(int nv) {
-    return nv == 0   ? reinterpret_cast<const void*>(token_logprobs<T, 0>)
-           : nv <= 2 ? reinterpret_cast<const void*>(token_logprobs<T, 2>)
-           : nv <= 5 ? reinterpret_cast<const void*>(token_logprobs<T, 5>)
-                     : reinterpret_cast<const void*>(token_logprobs<T, 8>);
-}
-
 int check_logits(const char* fn, int64_t rows, int64_t vocab, const void* logits, int64_t stride,
                  cam_dtype dtype) {
     if (rows < 0 || rows > (int64_t(1) << 27))
@@ -529,22 +973,43 @@ CAM_API int cam_token_logprobs(int64_t rows, int64_t vocab, const void* logits, 
     if (ce != cudaSuccess)
         return record_error(CAM_E_CUDA, "%s: no usable CUDA device: %s", fn, cudaGetErrorString(ce));
     LogprobArgs a{logits, stride, tokens, logp, entropy, lse, lse_lo, top_logp, top_ids,
-                  static_cast<int32_t>(vocab), top_logp || top_ids ? top : 0, 1};
-    // blocks per row: enough that a share fits the registers, and more while SMs idle
-    const int kn = dtype == CAM_F32 ? 4 : 8;
-    const int64_t n_vec = vocab / kn;
-    while (a.cluster < kLpMaxCluster &&
-           (n_vec > int64_t(a.cluster) * kLpThreads * 5 ||
-            (rows * a.cluster * 2 <= sms && n_vec > int64_t(a.cluster) * kLpThreads)))
+                  static_cast<int32_t>(rows), static_cast<int32_t>(vocab),
+                  top_logp || top_ids ? top : 0, 1, 0, 0, 0};
+    // Streaming threads per block: about 16 vectors each. Where rows are few, a cluster of
+    // blocks shares each of them.
+    const int64_t n_vec = std::max<int64_t>(1, vocab / (dtype == CAM_F32 ? 4 : 8));
+    auto threads_for = [&](int64_t share) {
+        return static_cast<int32_t>(
+            std::min<int64_t>(kLpMaxStream, std::max<int64_t>(64, (share / 16 + 31) / 32 * 32)));
+    };
+    auto bytes_for = [](int32_t threads) {
+        return static_cast<int>(sizeof(LogprobShared)) + kLpBufs * threads * kLpUnits * 4;
+    };
+    auto blocks_per_sm = [&](int32_t threads) {
+        return std::min(228 * 1024 / (bytes_for(threads) + 1024),
+                        1024 / (threads + 32 * kLpSelect));
+    };
+    a.stream = threads_for(n_vec);
+    while (a.cluster < kLpMaxCluster && n_vec > int64_t(a.cluster) * 256 &&
+           rows * a.cluster * 2 <= int64_t(sms) * blocks_per_sm(kLpMaxStream))
         a.cluster *= 2;
-    int64_t nv = (n_vec + int64_t(a.cluster) * kLpThreads - 1) / (int64_t(a.cluster) * kLpThreads);
-    if (nv > 8) nv = 0;
-    else if (nv == 0) nv = 1;
-    const void* kern = dtype == CAM_F32 ? forward_kernel<float>(static_cast<int>(nv))
-                                        : forward_kernel<uint16_t>(static_cast<int>(nv));
+    const int64_t share = (n_vec + a.cluster - 1) / a.cluster;
+    if (a.cluster > 1)  // (one row each: all of it at once)
+        a.stream = static_cast<int32_t>(
+            std::min<int64_t>(kLpMaxStream, std::max<int64_t>(64, (share + 31) / 32 * 32)));
+    a.iters = static_cast<int32_t>((share + a.stream - 1) / a.stream);
+    a.unit = (a.iters + kLpBatch * kLpUnits - 1) / (kLpBatch * kLpUnits) * kLpBatch;
+    const int64_t clusters =
+        a.cluster > 1 ? rows : int64_t(sms) * std::max(1, blocks_per_sm(a.stream));
+    const void* kern = dtype == CAM_F32 ? reinterpret_cast<const void*>(token_logprobs<float>)
+                                        : reinterpret_cast<const void*>(token_logprobs<uint16_t>);
+    ce = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    if (ce != cudaSuccess)
+        return record_error(CAM_E_CUDA, "%s: %s", fn, cudaGetErrorString(ce));
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(rows * a.cluster));
-    cfg.blockDim = dim3(kLpThreads);
+    cfg.gridDim = dim3(static_cast<unsigned>(std::min(rows, clusters) * a.cluster));
+    cfg.blockDim = dim3(a.stream + 32 * kLpSelect);
+    cfg.dynamicSmemBytes = bytes_for(a.stream);
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;
