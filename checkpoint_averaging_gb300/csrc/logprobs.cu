@@ -37,12 +37,13 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kLpBatch = 4;          // vectors of a thread in flight while as many are summed
-constexpr int kLpMaxStream = 384;    // streaming threads of a block
-constexpr int kLpSelect = 2;         // selecting warps: even and odd rows
-constexpr int kLpBufs = 3;           // rows whose sums are handed over or being made
+constexpr int kLpMaxStream = 352;    // streaming threads of a block
+constexpr int kLpSelect = 3;         // selecting warps: every third row each
+constexpr int kLpBufs = kLpSelect;   // rows whose sums are handed over or being made
 constexpr int kLpUnits = 8;          // parts of a thread's share of a row, each with its largest logit
 constexpr int kLpMaxBlock = kLpMaxStream + 32 * kLpSelect;
 constexpr int kLpList = 1024;        // candidates a block's share of a row may have
+constexpr int kLpFewVectors = 128;   // vectors looked through at once
 constexpr int kLpFewThreads = 96;    // threads whose vectors are scanned as a matter of course
 constexpr int kLpMaxCluster = 8;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -203,13 +204,11 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// Named barriers of a block. Full: a row's sums handed to its selecting warp; the
-// rows that share one (every sixth) have the same selecting warp and the same
-// buffer, so no warp comes to it early in another's place. Free: a buffer handed
-// back.
-constexpr int kLpFull = kLpSelect * kLpBufs;
-constexpr int kBarFull = 1, kBarFree = kBarFull + kLpFull;
-static_assert(kBarFree + kLpBufs <= 16, "a block has 16 barriers");
+// Named barriers of a block: a row's sums handed to its selecting warp, and its
+// buffers handed back. There is one of each for every selecting warp, so that
+// none comes to a barrier in another's place.
+constexpr int kBarFull = 1, kBarFree = kBarFull + kLpSelect;
+static_assert(kBarFree + kLpSelect <= 16, "a block has 16 barriers");
 __device__ __forceinline__ void bar_sync(int id, int n) {
     asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
 }
@@ -282,6 +281,8 @@ struct LogprobShared {
     WarpSums warps[kLpBufs][kLpMaxStream / 32];
     float thread_max[kLpBufs][kLpMaxStream];  // largest logit of each thread's vectors
     Key list[kLpSelect][kLpList];
+    uint4 vectors[kLpSelect][kLpFewVectors];
+    int vector_ids[kLpSelect][kLpFewVectors];
     Key best[kLpSelect][CAM_LOGPROBS_MAX_TOP];
     Key all_best[kLpMaxCluster][CAM_LOGPROBS_MAX_TOP];  // the leader's: every block's
     Share shares[kLpMaxCluster];                        // the leader's
@@ -312,76 +313,71 @@ struct RowPlan {
 // none), by one warp. `bad`: the share holds a NaN.
 template <typename T>
 __device__ __noinline__ void select(const LogprobArgs& a, LogprobShared& sh, const RowPlan<T>& row,
-                                    int par, int buf, int rank, bool bad, Key* out) {
-    Key* list = sh.list[par];
-    uint16_t* threads = sh.threads[par];
-    uint16_t* units = sh.units[par];
-    const float* unit_max =
-        reinterpret_cast<const float*>(&sh + 1) + buf * a.stream * kLpUnits;
+                                    int buf, int rank, bool bad, Key* out) {
     constexpr int kN = Vec16<T>::kN;
     constexpr uint32_t kAll = 0xFFFFFFFFu;
+    Key* list = sh.list[buf];
+    uint16_t* threads = sh.threads[buf];
+    uint16_t* units = sh.units[buf];
+    uint4* vectors = sh.vectors[buf];
+    int* vector_ids = sh.vector_ids[buf];
+    const float* thread_max = sh.thread_max[buf];
+    const float* unit_max = reinterpret_cast<const float*>(&sh + 1) + buf * a.stream * kLpUnits;
     const int lane = threadIdx.x & 31;
     const uint32_t below = (1u << lane) - 1u;
     const int singles = rank == 0 ? row.head + row.tail : 0;
-    const int across = a.stream * a.cluster, n_warps = a.stream >> 5;
-    const float* thread_max = sh.thread_max[buf];
+    const int across = a.stream * a.cluster;
     int n = 0;  // candidates so far, the same on every lane
-    // each lane's logits of `hits` (bit j: id + j, read by get(j)) onto the list
-    auto put = [&](uint32_t hits, int id, auto&& get) {
-        for (uint32_t who = __ballot_sync(kAll, hits != 0); who != 0;
-             who = __ballot_sync(kAll, hits != 0)) {
-            if (hits != 0) {
-                const int j = __ffs(hits) - 1, at = n + __popc(who & below);
-                if (at < kLpList) list[at] = make_key(get(j), static_cast<uint32_t>(id + j));
-                hits &= hits - 1;
-            }
-            n += __popc(who);
+    auto put = [&](bool hit, float v, int id) {
+        const uint32_t who = __ballot_sync(kAll, hit);
+        if (hit) {
+            const int at = n + __popc(who & below);
+            if (at < kLpList) list[at] = make_key(v, static_cast<uint32_t>(id));
         }
+        n += __popc(who);
     };
-    auto vector_hits = [&](const Vec16<T>& v, bool valid, auto&& wanted) {
-        uint32_t hits = 0;
-#pragma unroll
-        for (int j = 0; j < kN; ++j) hits |= (valid && wanted(v.get(j))) ? 1u << j : 0u;
-        return hits;
+    // vectors with something wanted, kept until they are looked through
+    int n_vectors = 0;
+    auto keep = [&](bool hit, const Vec16<T>& v, int id) {
+        const uint32_t who = __ballot_sync(kAll, hit);
+        if (hit) {
+            const int at = n_vectors + __popc(who & below);
+            vectors[at] = v.u;
+            vector_ids[at] = id;
+        }
+        n_vectors += __popc(who);
+    };
+    auto look_through = [&](auto&& wanted) {  // a lane to a logit
+        __syncwarp();
+        const T* flat = reinterpret_cast<const T*>(vectors);
+        for (int i = lane; i < ((n_vectors * kN + 31) & ~31); i += 32) {
+            const bool valid = i < n_vectors * kN;
+            const float v = valid ? widen1(flat[i]) : 0.0f;
+            put(valid && wanted(v), v, valid ? vector_ids[i / kN] + i % kN : 0);
+        }
+        n_vectors = 0;
+        __syncwarp();
     };
     if (!bad) {
-        // 32 sets of threads, or the warps where they suffice: the top-th largest of the sets'
-        // largest is a bound that at least `top` logits reach
+        // 32 sets of threads: the top-th largest of the sets' largest is a bound that at least
+        // `top` logits reach
         float m = -kInf;
-        if (a.top <= n_warps) {
-            if (lane < n_warps) m = sh.warps[buf][lane].m;
-        } else {
-            for (int j = lane; j < a.stream; j += 32) m = fmaxf(m, thread_max[j]);
-        }
+        for (int j = lane; j < a.stream; j += 32) m = fmaxf(m, thread_max[j]);
         const float bound = a.top == 1 ? warp_max(m) : nth_of_warp(m, a.top);
         if (singles > 0) {
             const int id = lane < singles ? row.single_id(lane, a.vocab) : 0;
             const float v = lane < singles ? widen1(row.x[id]) : 0.0f;
-            put(lane < singles && v >= bound ? 1u : 0u, id, [&](int) { return v; });
+            put(lane < singles && v >= bound, v, id);
         }
         // the threads that reach the bound (or pass it)
         int n_thr = 0;
-        auto list_threads = [&](bool strictly) {
+        auto list_threads = [&](auto&& wanted) {
             n_thr = 0;
-            const float w = lane < n_warps ? sh.warps[buf][lane].m : -kInf;
-            uint32_t warps =
-                __ballot_sync(kAll, lane < n_warps && (strictly ? w > bound : w >= bound));
-            while (warps != 0) {
-                float v[4];
-                int at[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    at[k] = warps != 0 ? (__ffs(warps) - 1) * 32 + lane : -1;
-                    warps &= warps - 1;
-                    v[k] = at[k] >= 0 ? thread_max[at[k]] : -kInf;
-                }
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const bool hit = at[k] >= 0 && (strictly ? v[k] > bound : v[k] >= bound);
-                    const uint32_t who = __ballot_sync(kAll, hit);
-                    if (hit) threads[n_thr + __popc(who & below)] = static_cast<uint16_t>(at[k]);
-                    n_thr += __popc(who);
-                }
+            for (int j = lane; j < a.stream; j += 32) {
+                const bool hit = wanted(thread_max[j]);
+                const uint32_t who = __ballot_sync(kAll, hit);
+                if (hit) threads[n_thr + __popc(who & below)] = static_cast<uint16_t>(j);
+                n_thr += __popc(who);
             }
             __syncwarp();
         };
@@ -421,29 +417,36 @@ __device__ __noinline__ void select(const LogprobArgs& a, LogprobShared& sh, con
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             if (u0 + 8 * k < n_units)
-                                put(vector_hits(v[k], w[k] < row.n_vec, wanted),
-                                    row.head + w[k] * kN, [&](int j) { return v[k].get(j); });
+                                keep(w[k] < row.n_vec && wanted(v[k].largest()), v[k],
+                                     row.head + w[k] * kN);
+                        look_through(wanted);
                     }
-                __syncwarp();
             }
         };
-        list_threads(false);
+        const auto reaches = [&](float v) { return v >= bound; };
+        const auto passes = [&](float v) { return v > bound; };
+        list_threads(reaches);
         if (n_thr <= kLpFewThreads) {
-            scan_threads([&](float v) { return v >= bound; });
+            scan_threads(reaches);
         } else {
             // many logits equal to the bound: those above it from their threads, and of the
             // equal ones the first `top` in the order of ids
-            list_threads(true);
-            scan_threads([&](float v) { return v > bound; });
+            list_threads(passes);
+            scan_threads(passes);
             const int enough = n + a.top;
             for (int u = lane; n < enough; u += 32) {
                 // the share's vector number u, in the order of ids
                 const int w = (u / a.stream) * across + rank * a.stream + u % a.stream;
                 if (__all_sync(kAll, w >= row.n_vec)) break;
                 Vec16<T> v;
-                if (w < row.n_vec) v = load16(row.x + row.head + w * kN);
-                put(vector_hits(v, w < row.n_vec, [&](float e) { return e == bound; }),
-                    row.head + w * kN, [&](int j) { return v.get(j); });
+                bool hit = false;
+                if (w < row.n_vec) {
+                    v = load16(row.x + row.head + w * kN);
+#pragma unroll
+                    for (int j = 0; j < kN; ++j) hit |= v.get(j) == bound;
+                }
+                keep(hit, v, row.head + w * kN);
+                look_through([&](float e) { return e == bound; });
             }
         }
         __syncwarp();
@@ -534,174 +537,28 @@ __device__ __noinline__ Share careful(const LogprobArgs& a, const RowPlan<T>& ro
     return Share{m, warp_sum(c), warp_sum(r), warp_sum(t)};
 }
 
+// A selecting warp: the results of rows par, par + kLpSelect, ... of the block
+// while later rows stream.
 template <typename T>
-__global__ void __launch_bounds__(kLpMaxBlock, 2)
-    token_logprobs(const __grid_constant__ LogprobArgs a) {
+__device__ __noinline__ void select_rows(const LogprobArgs& a, LogprobShared& sh, int par,
+                                         int rank, int first, int step, int n_rows) {
     constexpr int kN = Vec16<T>::kN;
-    extern __shared__ __align__(128) uint8_t smem[];
-    LogprobShared& sh = *reinterpret_cast<LogprobShared*>(smem);
-
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int n_warps = a.stream >> 5, both = a.stream + 32;
-    const bool clustered = a.cluster > 1;  // (then a block has one row)
-    const int rank = clustered ? static_cast<int>(cg::this_cluster().block_rank()) : 0;
-    const int first = blockIdx.x / a.cluster, step = gridDim.x / a.cluster;
-    const int n_rows = first < a.rows ? (a.rows - first - 1) / step + 1 : 0;
+    const int lane = threadIdx.x & 31, n_warps = a.stream >> 5, both = a.stream + 32;
+    const bool clustered = a.cluster > 1;
     const int across = a.stream * a.cluster;
-    const T* logits = static_cast<const T*>(a.logits);
-    auto plan = [&](int k) {
-        return RowPlan<T>(logits + (first + int64_t(k) * step) * a.stride, a.vocab);
-    };
-    if (clustered) {  // every block of the cluster has started
-        cluster_arrive();
-        cluster_wait();
-    }
-
-    if (warp < n_warps) {
-        // ---- streaming ---------------------------------------------------------------
-        // The sums are taken relative to a reference of the thread's own: its first batch's
-        // largest logit, moved up when a batch passes it by 16, so that no term overflows and
-        // none that counts is lost. No thread waits for another within a row.
-        using Batch = Vec16<T>[kLpBatch];
-        const int w0 = rank * a.stream + warp * 32;  // the warp's first vector
-        int l_row = 0, l_w = w0, l_vecs = 0;         // the next batch to load
-        const T* l_at = nullptr;
-        auto load = [&](Batch& v, int& w, int& n_vec) {
-            if (l_w == w0 && l_row < n_rows) {
-                const RowPlan<T> p = plan(l_row);
-                l_vecs = p.n_vec;
-                l_at = p.x + p.head + int64_t(w0 + lane) * kN;
-            }
-            w = l_w;
-            n_vec = l_row < n_rows ? l_vecs : 0;
-            constexpr uint32_t kPad = sizeof(T) == 4 ? 0xFF800000u : 0xFF80FF80u;  // -inf
-#pragma unroll
-            for (int j = 0; j < kLpBatch; ++j) {
-                v[j].u = make_uint4(kPad, kPad, kPad, kPad);
-                if (w + lane + j * across < n_vec) v[j] = load16(l_at + int64_t(j) * across * kN);
-            }
-            l_w += kLpBatch * across;
-            l_at += int64_t(kLpBatch) * across * kN;
-            if (l_w >= a.iters * across + w0) l_w = w0, ++l_row;
-        };
-
-        const Pair log2e = pair(kLog2e, kLog2e);
-        float m = -kInf, limit = -kHuge, ref = 0.0f;  // ref: minus the reference times log2(e)
-        float unit_m = -kInf;                         // the largest of the unit under way
-        const int unit_batches = a.unit / kLpBatch;
-        int unit_left = unit_batches;
-        float* unit_max = reinterpret_cast<float*>(&sh + 1) + tid * kLpUnits;
-        float* unit_at = unit_max;
-        Pair s2 = pair(0.0f, 0.0f), t2 = s2;
-        auto add = [&](const Batch& v, int w, int n_vec) {
-            const float big = Vec16<T>::largest_nan(v);
-            if (!(big <= limit)) {
-                if (big < kHuge) {
-                    const float up = -big * kLog2e, by = up - ref;
-                    const float f = limit == -kHuge ? 0.0f : ex2(by);
-                    s2 = mul2(s2, pair(f, f));
-                    t2 = limit == -kHuge ? t2 : fma2(t2, pair(f, f), mul2(s2, pair(by, by)));
-                    ref = up;
-                    limit = big + 16.0f;
-                } else {  // NaN, or too large
-                    s2 = pair(NAN, NAN);
-                }
-            }
-            m = fmaxf(m, big);
-            unit_m = fmaxf(unit_m, big);
-            if (--unit_left == 0) {
-                *unit_at++ = unit_m;
-                unit_m = -kInf, unit_left = unit_batches;
-            }
-            const Pair ref2 = pair(ref, ref);
-#pragma unroll
-            for (int j = 0; j < kLpBatch; ++j) {
-                if (w + j * across >= n_vec) break;  // (the whole warp's)
-                // a mask held finite: its exponent times its term is then 0 and not NaN
-                const Vec16<T> u = v[j].held_finite();
-#pragma unroll
-                for (int q = 0; q < kN; q += 2) {
-                    const Pair y = fma2(pair(u.get(q), u.get(q + 1)), log2e, ref2);
-                    float y0, y1;
-                    split(y, y0, y1);
-                    const Pair e = pair(ex2(y0), ex2(y1));
-                    s2 = add2(s2, e);
-                    t2 = fma2(e, y, t2);
-                }
-            }
-        };
-        auto finish = [&](int k) {  // the warp's sums of row k, relative to its largest
-            const int buf = k % kLpBufs;
-            float s, t, hi;
-            split(s2, s, hi);
-            s += hi;
-            split(t2, t, hi);
-            t += hi;
-            const float wm = warp_max(m);
-            const bool top = m == wm;
-            const float y = fmaf(wm, kLog2e, ref);  // >= 0 where the lane has a reference
-            const float f = s == 0.0f ? 0.0f : ex2(-y);
-            t = s == 0.0f ? 0.0f : f * fmaf(-y, s, t);
-            s *= f;
-            const float rest_s = warp_sum(top ? 0.0f : s), rest_t = warp_sum(top ? 0.0f : t);
-            const uint32_t who = __ballot_sync(0xFFFFFFFFu, top);
-            const int top_lane = __ffs(who) - 1;
-            float top_s = s, top_t = t;  // (on the top lane)
-            if (who & (who - 1)) {
-                top_s = warp_sum(top ? s : 0.0f);
-                top_t = warp_sum(top ? t : 0.0f);
-            }
-            if (unit_left < unit_batches) *unit_at = unit_m;
-            sh.thread_max[buf][tid] = m;
-            if (lane == top_lane)
-                sh.warps[buf][warp] = WarpSums{wm, rest_s, rest_t, top_s, top_t, top_lane};
-            bar_arrive(kBarFull + k % kLpFull, both);
-            m = -kInf, limit = -kHuge, ref = 0.0f;
-            s2 = t2 = pair(0.0f, 0.0f);
-            // the next row's buffer
-            unit_m = -kInf, unit_left = unit_batches;
-            const int next = (k + 1) % kLpBufs;
-            unit_at = unit_max + next * a.stream * kLpUnits;
-            if (k + 1 >= kLpBufs && k + 1 < n_rows) bar_sync(kBarFree + next, both);
-        };
-
-        Batch v0, v1;
-        int at0, at1, n0, n1;
-        const int batches = (a.iters + kLpBatch - 1) / kLpBatch;
-        int left = batches, k = 0;
-        load(v0, at0, n0);
-        while (k < n_rows) {
-            load(v1, at1, n1);
-            add(v0, at0, n0);
-            if (--left == 0) {
-                finish(k);
-                left = batches;
-                if (++k == n_rows) break;
-            }
-            load(v0, at0, n0);
-            add(v1, at1, n1);
-            if (--left == 0) finish(k), left = batches, ++k;
-        }
-        if (clustered) {
-            __syncwarp();
-            cluster_arrive();
-            cluster_wait();
-        }
-        return;
-    }
-
-    // ---- a selecting warp: every second row's results while the next rows stream ----
-    const int par = warp - n_warps;
+    const int buf = par;
+    const bool ask = a.logp && rank == 0;
+    int64_t next_token = ask && par < n_rows ? a.tokens[first + int64_t(par) * step] : -1;
     for (int k = par; k < n_rows; k += kLpSelect) {
-        const int buf = k % kLpBufs;
         const int64_t r_at = first + int64_t(k) * step;
-        const RowPlan<T> row = plan(k);
+        const RowPlan<T> row(static_cast<const T*>(a.logits) + r_at * a.stride, a.vocab);
         const int singles = rank == 0 ? row.head + row.tail : 0;
-        // (asked for early: these loads overlap the wait)
-        const int64_t token = a.logp && rank == 0 ? a.tokens[r_at] : -1;
+        // (these loads overlap the wait, and the next row's token the row)
+        const int64_t token = next_token;
+        if (ask && k + kLpSelect < n_rows) next_token = a.tokens[r_at + int64_t(kLpSelect) * step];
         const float single = lane < singles ? widen1(row.x[row.single_id(lane, a.vocab)]) : -kInf;
         const float x_token = token >= 0 && token < a.vocab ? widen1(row.x[token]) : 0.0f;
-        bar_sync(kBarFull + k % kLpFull, both);
+        bar_sync(kBarFull + buf, both);
         const WarpSums ws = lane < n_warps ? sh.warps[buf][lane]
                                            : WarpSums{-kInf, 0.0f, 0.0f, 0.0f, 0.0f, 0};
         Share s;
@@ -750,10 +607,10 @@ __global__ void __launch_bounds__(kLpMaxBlock, 2)
             s.r = warp_sum(r);
             s.t = warp_sum(t) * kLn2;
         }
-        Key* best = sh.best[par];
+        Key* best = sh.best[buf];
         if (a.top > 0) {
             if (clustered) best = cg::this_cluster().map_shared_rank(&sh.all_best[rank][0], 0);
-            select<T>(a, sh, row, par, buf, rank, bad, best);
+            select<T>(a, sh, row, buf, rank, bad, best);
         }
         if (k + kLpBufs < n_rows) bar_arrive(kBarFree + buf, both);
         if (clustered) {
@@ -791,7 +648,7 @@ __global__ void __launch_bounds__(kLpMaxBlock, 2)
                 const float lo = __fadd_rn(__fsub_rn(s.m, __fsub_rn(lse, b)), __fsub_rn(log_s, b));
                 a.lse_lo[r_at] = isfinite(lse) ? lo : 0.0f;
             }
-            if (a.entropy) a.entropy[r_at] = dead ? 0.0f : log_s - s.t / (s.c + s.r);
+            if (a.entropy) a.entropy[r_at] = dead ? 0.0f : log_s - __fdividef(s.t, s.c + s.r);
             if (a.logp)
                 a.logp[r_at] = token >= a.vocab ? NAN : token >= 0 ? logp_of(x_token) : 0.0f;
         }
@@ -814,6 +671,178 @@ __global__ void __launch_bounds__(kLpMaxBlock, 2)
         cluster_arrive();
         cluster_wait();
     }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kLpMaxBlock, 2)
+    token_logprobs(const __grid_constant__ LogprobArgs a) {
+    constexpr int kN = Vec16<T>::kN;
+    extern __shared__ __align__(128) uint8_t smem[];
+    LogprobShared& sh = *reinterpret_cast<LogprobShared*>(smem);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int n_warps = a.stream >> 5, both = a.stream + 32;
+    const bool clustered = a.cluster > 1;  // (then a block has one row)
+    const int rank = clustered ? static_cast<int>(cg::this_cluster().block_rank()) : 0;
+    const int first = blockIdx.x / a.cluster, step = gridDim.x / a.cluster;
+    const int n_rows = first < a.rows ? (a.rows - first - 1) / step + 1 : 0;
+    const int across = a.stream * a.cluster;
+    const T* logits = static_cast<const T*>(a.logits);
+    auto plan = [&](int k) {
+        return RowPlan<T>(logits + (first + int64_t(k) * step) * a.stride, a.vocab);
+    };
+    if (clustered) {  // every block of the cluster has started
+        cluster_arrive();
+        cluster_wait();
+    }
+
+    if (warp < n_warps) {
+        // ---- streaming ---------------------------------------------------------------
+        // The sums are taken relative to a reference of the thread's own: its first batch's
+        // largest logit, moved up when a batch passes it by 16, so that no term overflows and
+        // none that counts is lost. No thread waits for another within a row.
+        using Batch = Vec16<T>[kLpBatch];
+        const int w0 = rank * a.stream + warp * 32;  // the warp's first vector
+        int l_row = 0, l_w = w0, l_vecs = 0;         // the next batch to load
+        const T* l_at = nullptr;
+        const int64_t jump = int64_t(across) * kN;
+        auto whole = [&](int w, int n_vec) { return w + 32 + (kLpBatch - 1) * across <= n_vec; };
+        auto load = [&](Batch& v, int& w, int& n_vec) {
+            if (l_w == w0 && l_row < n_rows) {
+                const RowPlan<T> p = plan(l_row);
+                l_vecs = p.n_vec;
+                l_at = p.x + p.head + int64_t(w0 + lane) * kN;
+            }
+            w = l_w;
+            n_vec = l_row < n_rows ? l_vecs : 0;
+            if (whole(w, n_vec)) {
+#pragma unroll
+                for (int j = 0; j < kLpBatch; ++j) v[j] = load16(l_at + j * jump);
+            } else {
+                constexpr uint32_t kPad = sizeof(T) == 4 ? 0xFF800000u : 0xFF80FF80u;  // -inf
+#pragma unroll
+                for (int j = 0; j < kLpBatch; ++j) {
+                    v[j].u = make_uint4(kPad, kPad, kPad, kPad);
+                    if (w + lane + j * across < n_vec) v[j] = load16(l_at + j * jump);
+                }
+            }
+            l_w += kLpBatch * across;
+            l_at += kLpBatch * jump;
+            if (l_w >= a.iters * across + w0) l_w = w0, ++l_row;
+        };
+
+        const Pair log2e = pair(kLog2e, kLog2e);
+        float m = -kInf, limit = -kHuge, ref = 0.0f;  // ref: minus the reference times log2(e)
+        float unit_m = -kInf;                         // the largest of the unit under way
+        const int unit_batches = a.unit / kLpBatch;
+        int unit_left = unit_batches;
+        float* unit_max = reinterpret_cast<float*>(&sh + 1) + tid * kLpUnits;
+        float* unit_at = unit_max;
+        Pair s2 = pair(0.0f, 0.0f), t2 = s2;
+        auto add = [&](const Batch& v, int w, int n_vec) {
+            const float big = Vec16<T>::largest_nan(v);
+            if (!(big <= limit)) {
+                if (big < kHuge) {
+                    const float up = -big * kLog2e, by = up - ref;
+                    const float f = limit == -kHuge ? 0.0f : ex2(by);
+                    s2 = mul2(s2, pair(f, f));
+                    t2 = limit == -kHuge ? t2 : fma2(t2, pair(f, f), mul2(s2, pair(by, by)));
+                    ref = up;
+                    limit = big + 16.0f;
+                } else {  // NaN, or too large
+                    s2 = pair(NAN, NAN);
+                }
+            }
+            m = fmaxf(m, big);
+            unit_m = fmaxf(unit_m, big);
+            if (--unit_left == 0) {
+                *unit_at++ = unit_m;
+                unit_m = -kInf, unit_left = unit_batches;
+            }
+            const Pair ref2 = pair(ref, ref);
+            auto sum = [&](const Vec16<T>& x) {
+                // a mask held finite: its exponent times its term is then 0 and not NaN
+                const Vec16<T> u = x.held_finite();
+#pragma unroll
+                for (int q = 0; q < kN; q += 2) {
+                    const Pair y = fma2(pair(u.get(q), u.get(q + 1)), log2e, ref2);
+                    float y0, y1;
+                    split(y, y0, y1);
+                    const Pair e = pair(ex2(y0), ex2(y1));
+                    s2 = add2(s2, e);
+                    t2 = fma2(e, y, t2);
+                }
+            };
+            if (whole(w, n_vec)) {
+#pragma unroll
+                for (int j = 0; j < kLpBatch; ++j) sum(v[j]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < kLpBatch; ++j)
+                    if (w + j * across < n_vec) sum(v[j]);  // (the whole warp's)
+            }
+        };
+        auto finish = [&](int k) {  // the warp's sums of row k, relative to its largest
+            const int buf = k % kLpBufs;
+            float s, t, hi;
+            split(s2, s, hi);
+            s += hi;
+            split(t2, t, hi);
+            t += hi;
+            const float wm = warp_max(m);
+            const bool top = m == wm;
+            const float y = fmaf(wm, kLog2e, ref);  // >= 0 where the lane has a reference
+            const float f = s == 0.0f ? 0.0f : ex2(-y);
+            t = s == 0.0f ? 0.0f : f * fmaf(-y, s, t);
+            s *= f;
+            const float rest_s = warp_sum(top ? 0.0f : s), rest_t = warp_sum(top ? 0.0f : t);
+            const uint32_t who = __ballot_sync(0xFFFFFFFFu, top);
+            const int top_lane = __ffs(who) - 1;
+            float top_s = s, top_t = t;  // (on the top lane)
+            if (who & (who - 1)) {
+                top_s = warp_sum(top ? s : 0.0f);
+                top_t = warp_sum(top ? t : 0.0f);
+            }
+            if (unit_left < unit_batches) *unit_at = unit_m;
+            sh.thread_max[buf][tid] = m;
+            if (lane == top_lane)
+                sh.warps[buf][warp] = WarpSums{wm, rest_s, rest_t, top_s, top_t, top_lane};
+            bar_arrive(kBarFull + buf, both);
+            m = -kInf, limit = -kHuge, ref = 0.0f;
+            s2 = t2 = pair(0.0f, 0.0f);
+            // the next row's buffer
+            unit_m = -kInf, unit_left = unit_batches;
+            const int next = (k + 1) % kLpBufs;
+            unit_at = unit_max + next * a.stream * kLpUnits;
+            if (k + 1 >= kLpBufs && k + 1 < n_rows) bar_sync(kBarFree + next, both);
+        };
+
+        Batch v0, v1;
+        int at0, at1, n0, n1;
+        const int batches = (a.iters + kLpBatch - 1) / kLpBatch;
+        int left = batches, k = 0;
+        load(v0, at0, n0);
+        while (k < n_rows) {
+            load(v1, at1, n1);
+            add(v0, at0, n0);
+            if (--left == 0) {
+                finish(k);
+                left = batches;
+                if (++k == n_rows) break;
+            }
+            load(v0, at0, n0);
+            add(v1, at1, n1);
+            if (--left == 0) finish(k), left = batches, ++k;
+        }
+        if (clustered) {
+            __syncwarp();
+            cluster_arrive();
+            cluster_wait();
+        }
+        return;
+    }
+
+    select_rows<T>(a, sh, warp - n_warps, rank, first, step, n_rows);
 }
 
 // ---- backward ----------------------------------------------------------------
