@@ -9,11 +9,10 @@ Every step of a merge runs in libcam's CUDA kernels; there is no fallback.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import weakref
-from typing import NamedTuple, Sequence
+from typing import Sequence
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libcam.so")
@@ -497,216 +496,20 @@ def _stream_handle(stream) -> int:
 
 # ---- beside the merge: 4-bit publishing, its products, and the token probe -----------
 
-def _dtype_code(t, what: str) -> int:
-    torch = _torch()
-    if t.dtype == torch.float32:
-        return F32
-    if t.dtype == torch.bfloat16:
-        return BF16
-    raise ValueError(f"{what} must be fp32 or bf16, not {t.dtype}")
+# The torch-facing calls live in operators.py, which needs torch at import;
+# they are this module's too (binding.pack4, ...), looked up at first use.
+_OPERATORS = ("Packed4", "TokenLogprobs", "pack4", "pack4_bytes", "unpack4", "gemv4",
+              "token_logprobs", "token_logprobs_backward")
 
 
-def _row_stride(t, what: str) -> int:
-    """The elements between row starts of a 2-D CUDA tensor whose rows are contiguous."""
-    if t.dim() != 2 or not t.is_cuda:
-        raise ValueError(f"{what} must be a 2-D CUDA tensor")
-    rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
-        raise ValueError(f"{what} must have contiguous rows")
-    # a single row's stride is never used; rows that overlap have no stride
-    stride = t.stride(0) if rows > 1 else cols
-    if stride < cols:
-        raise ValueError(f"{what} must not have overlapping rows")
-    return stride
+def __getattr__(name: str):
+    if name in _OPERATORS:
+        from . import operators
 
-
-def _on(device, stream, tensors):
-    """(the torch stream's handle, a context that makes `device` current) for a
-    call on the given tensors; records them on a stream given explicitly."""
-    torch = _torch()
-    for t in tensors:
-        if t.device != device:
-            raise ValueError("tensors must live on one CUDA device")
-    guard = contextlib.nullcontext() if device.index == torch.cuda.current_device() \
-        else torch.cuda.device(device)
-    if stream is None:
-        return int(torch.cuda.current_stream(device).cuda_stream), guard
-    handle = int(stream.cuda_stream)
-    if not _capturing(stream):
-        _record_streams(tensors, stream, handle)
-    return handle, guard
-
-
-class Packed4:
-    """A matrix in the 4-bit form (include/cam.h): ``data`` is its bytes (uint8,
-    1-D, on the GPU), which may be saved and made a Packed4 of again."""
-
-    __slots__ = ("data", "rows", "cols", "group")
-
-    def __init__(self, data, rows: int, cols: int, group: int):
-        torch = _torch()
-        if not data.is_cuda or data.dtype != torch.uint8 or not data.is_contiguous() \
-                or data.data_ptr() % 16:
-            raise ValueError("data must be a contiguous 16-byte aligned uint8 CUDA tensor")
-        if data.numel() != pack4_bytes(rows, cols, group):
-            raise ValueError(f"data must hold {pack4_bytes(rows, cols, group)} bytes")
-        self.data, self.rows, self.cols, self.group = data, rows, cols, group
-
-    @property
-    def shape(self):
-        return (self.rows, self.cols)
-
-
-def pack4_bytes(rows: int, cols: int, group: int = 64) -> int:
-    out = ctypes.c_int64()
-    _check(lib().cam_pack4_bytes(rows, cols, group, ctypes.byref(out)))
-    return out.value
-
-
-def pack4(weight, group: int = 64, *, stream=None) -> Packed4:
-    """The 4-bit form of a matrix (cam_pack4): a merged global's weight as it is
-    published. weight is 2-D, fp32 or bf16, its rows contiguous; `group`
-    columns (32, 64 or 128) share a scale."""
-    torch = _torch()
-    ld = _row_stride(weight, "weight")
-    dt = _dtype_code(weight, "weight")
-    rows, cols = weight.shape
-    data = torch.empty(pack4_bytes(rows, cols, group), dtype=torch.uint8, device=weight.device)
-    handle, guard = _on(weight.device, stream, (weight, data))
-    with guard:
-        _check(lib().cam_pack4(rows, cols, weight.data_ptr(), ld, dt, group, data.data_ptr(),
-                               handle or None))
-    return Packed4(data, rows, cols, group)
-
-
-def unpack4(packed: Packed4, dtype=None, *, out=None, stream=None):
-    """The values a 4-bit matrix stands for (cam_unpack4), as a new tensor of
-    `dtype` (fp32 by default, or bf16) or into `out`."""
-    torch = _torch()
-    if out is None:
-        out = torch.empty(packed.rows, packed.cols, dtype=dtype or torch.float32,
-                          device=packed.data.device)
-    elif tuple(out.shape) != packed.shape or (dtype is not None and out.dtype != dtype):
-        raise ValueError("out must match the packed matrix")
-    ld = _row_stride(out, "out")
-    dt = _dtype_code(out, "out")
-    handle, guard = _on(packed.data.device, stream, (packed.data, out))
-    with guard:
-        _check(lib().cam_unpack4(packed.rows, packed.cols, packed.data.data_ptr(), packed.group,
-                                 out.data_ptr(), ld, dt, handle or None))
-    return out
-
-
-def gemv4(x, packed: Packed4, *, out=None, out_dtype=None, stream=None):
-    """x W^T for a 4-bit W and a few rows x (cam_gemv4): x is [cols] or
-    [tokens, cols], fp32 or bf16; the result is [rows] or [tokens, rows] in
-    x's dtype (or `out_dtype`, or into `out`). For serving: no gradient."""
-    torch = _torch()
-    one = x.dim() == 1
-    xs = x.unsqueeze(0) if one else x
-    ld = _row_stride(xs, "x")
-    dt = _dtype_code(xs, "x")
-    tokens, cols = xs.shape
-    if cols != packed.cols:
-        raise ValueError(f"x has {cols} columns, the matrix {packed.cols}")
-    if out is None:
-        ys = torch.empty(tokens, packed.rows, dtype=out_dtype or x.dtype, device=x.device)
-    else:
-        ys = out.unsqueeze(0) if one and out.dim() == 1 else out
-        if tuple(ys.shape) != (tokens, packed.rows) or \
-                (out_dtype is not None and out.dtype != out_dtype):
-            raise ValueError("out must match x and the matrix")
-    ldy = _row_stride(ys, "out")
-    dty = _dtype_code(ys, "out")
-    handle, guard = _on(x.device, stream, (x, packed.data, ys if out is None else out))
-    with guard:
-        _check(lib().cam_gemv4(tokens, packed.rows, cols, xs.data_ptr(), ld, dt,
-                               packed.data.data_ptr(), packed.group, ys.data_ptr(), ldy, dty,
-                               handle or None))
-    if out is not None:
-        return out
-    return ys[0] if one else ys
-
-
-class TokenLogprobs(NamedTuple):
-    """What token_logprobs found, one entry per row of logits (fp32; ids int64)."""
-    logp: object      # of the given tokens, or None without tokens
-    entropy: object
-    lse: object
-    top_logp: object  # [rows, top], or None for top = 0
-    top_ids: object
-    lse_lo: object    # what rounding lse to fp32 left out, for the gradient
-
-
-def _check_tokens(tokens, rows: int):
-    torch = _torch()
-    if tokens.dtype != torch.int64 or tuple(tokens.shape) != (rows,) or not tokens.is_contiguous():
-        raise ValueError("tokens must be a contiguous int64 tensor with one id per row")
-
-
-def token_logprobs(logits, tokens=None, *, top: int = 0, stream=None) -> TokenLogprobs:
-    """Log probabilities of given tokens, with the entropy and the `top` most
-    likely alternatives of each row (cam_token_logprobs). logits is [rows,
-    vocab], fp32 or bf16, its rows contiguous; a negative id is no token."""
-    torch = _torch()
-    ld = _row_stride(logits, "logits")
-    dt = _dtype_code(logits, "logits")
-    rows, vocab = logits.shape
-    dev = logits.device
-    if tokens is not None:
-        _check_tokens(tokens, rows)
-    if not 0 <= top <= LOGPROBS_MAX_TOP:
-        raise ValueError(f"top must be in [0, {LOGPROBS_MAX_TOP}]")
-    # one allocation: logp, entropy, lse and lse_lo are its rows
-    stats = torch.empty((4, rows), dtype=torch.float32, device=dev)
-    top_logp = torch.empty((rows, top), dtype=torch.float32, device=dev) if top else None
-    top_ids = torch.empty((rows, top), dtype=torch.int64, device=dev) if top else None
-    used = [t for t in (logits, tokens, stats, top_logp, top_ids) if t is not None]
-    handle, guard = _on(dev, stream, used)
-    at = stats.data_ptr()
-    with guard:
-        _check(lib().cam_token_logprobs(
-            rows, vocab, logits.data_ptr(), ld, dt, None if tokens is None else tokens.data_ptr(),
-            top, None if tokens is None else at, at + 4 * rows, at + 8 * rows,
-            at + 12 * rows, top_logp.data_ptr() if top else None, top_ids.data_ptr() if top else None,
-            handle or None))
-    logp, entropy, lse, lse_lo = stats.unbind(0)
-    return TokenLogprobs(None if tokens is None else logp, entropy, lse, top_logp, top_ids, lse_lo)
-
-
-def token_logprobs_backward(logits, tokens, lse, entropy, grad_logp=None, grad_entropy=None, *,
-                            lse_lo=None, out=None, stream=None):
-    """The gradient of token_logprobs' logp and entropy with respect to the
-    logits (cam_token_logprobs_backward), in the logits' dtype: a new tensor or
-    into `out`, which may be `logits` itself. lse, entropy and lse_lo (optional)
-    are as token_logprobs returned them; either gradient may be None, not both."""
-    torch = _torch()
-    ld = _row_stride(logits, "logits")
-    dt = _dtype_code(logits, "logits")
-    rows, vocab = logits.shape
-    if tokens is not None:
-        _check_tokens(tokens, rows)
-    for t in (lse, lse_lo, entropy, grad_logp, grad_entropy):
-        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (rows,)
-                              or not t.is_contiguous()):
-            raise ValueError("lse, entropy and the gradients must be contiguous fp32, one per row")
-    if out is None:
-        out = torch.empty((rows, vocab), dtype=logits.dtype, device=logits.device)
-    elif out.shape != logits.shape or out.dtype != logits.dtype:
-        raise ValueError("out must match logits")
-    ldo = _row_stride(out, "out")
-    used = [t for t in (logits, tokens, lse, lse_lo, entropy, grad_logp, grad_entropy, out)
-            if t is not None]
-    handle, guard = _on(logits.device, stream, used)
-
-    def ptr(t):
-        return None if t is None else t.data_ptr()
-
-    with guard:
-        _check(lib().cam_token_logprobs_backward(
-            rows, vocab, logits.data_ptr(), ld, dt, ptr(tokens), ptr(lse), ptr(lse_lo),
-            ptr(entropy), ptr(grad_logp), ptr(grad_entropy), out.data_ptr(), ldo, handle or None))
-    return out
+        for n in _OPERATORS:
+            globals()[n] = getattr(operators, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 class Merger:

@@ -31,6 +31,7 @@
 #include <atomic>
 
 #include "cam_internal.h"
+#include "op_launch.h"
 #include "pack4_layout.h"
 
 #define CAM_API extern "C" __attribute__((visibility("default")))
@@ -44,7 +45,6 @@ constexpr int kGvThreads = 256;
 constexpr int kGvWarps = kGvThreads / 32;
 constexpr int kGvDepth = 4;     // ring slots per warp
 constexpr int kGvMaxCols = 32;  // columns of x in one pass (four 8-column operands)
-constexpr int kGvSmem = 227 * 1024;
 
 struct GemvArgs {
     const void* x;
@@ -400,8 +400,7 @@ CAM_API int cam_gemv4(int64_t tokens, int64_t rows, int64_t cols, const void* x,
     if (reinterpret_cast<uintptr_t>(x) % x_size != 0 || reinterpret_cast<uintptr_t>(y) % y_size != 0)
         return record_error(CAM_E_ARG, "%s: an array is not aligned to its elements", fn);
     int dev = 0, sms = 0;
-    cudaError_t ce = cudaGetDevice(&dev);
-    if (ce == cudaSuccess) ce = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    cudaError_t ce = current_device(&dev, &sms);
     if (ce != cudaSuccess)
         return record_error(CAM_E_CUDA, "%s: no usable CUDA device: %s", fn, cudaGetErrorString(ce));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -437,7 +436,7 @@ CAM_API int cam_gemv4(int64_t tokens, int64_t rows, int64_t cols, const void* x,
         nt = C <= 8 ? 1 : C <= 16 ? 2 : 4;
         a.red_bufs = C <= 8 ? 2 : 1;
         red = a.red_bufs * kGvWarps * C * (rt * 16 + 4) * 4;
-        const int x_room = kGvSmem - ring - red;
+        const int x_room = kMaxSharedBytes - ring - red;
         // the columns split over a cluster until x fits, and further while blocks are fewer
         // than SMs
         a.cluster = 1;
@@ -457,7 +456,11 @@ CAM_API int cam_gemv4(int64_t tokens, int64_t rows, int64_t cols, const void* x,
     const int clusters = std::max(1, std::min(a.units, sms * per_sm / a.cluster / passes));
 
     const void* kern = kernel_for(rt, nt, group);
-    ce = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kGvSmem);
+    if (bytes > 48 * 1024) {
+        static std::atomic<uint64_t> shared_ok[2][3][3];
+        ce = allow_shared(kern, dev,
+                          shared_ok[rt - 1][nt == 4 ? 2 : nt - 1][group == 32 ? 0 : group / 64]);
+    }
     if (ce == cudaSuccess) {
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3(clusters * a.cluster, passes);

@@ -28,6 +28,7 @@
 #include <cmath>
 
 #include "cam_internal.h"
+#include "op_launch.h"
 
 #define CAM_API extern "C" __attribute__((visibility("default")))
 
@@ -997,8 +998,7 @@ CAM_API int cam_token_logprobs(int64_t rows, int64_t vocab, const void* logits, 
         return record_error(CAM_E_ARG, "%s: logp needs tokens", fn);
     if (rows == 0) return CAM_OK;
     int dev = 0, sms = 0;
-    cudaError_t ce = cudaGetDevice(&dev);
-    if (ce == cudaSuccess) ce = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    cudaError_t ce = current_device(&dev, &sms);
     if (ce != cudaSuccess)
         return record_error(CAM_E_CUDA, "%s: no usable CUDA device: %s", fn, cudaGetErrorString(ce));
     LogprobArgs a{logits, stride, tokens, logp, entropy, lse, lse_lo, top_logp, top_ids,
@@ -1032,7 +1032,8 @@ CAM_API int cam_token_logprobs(int64_t rows, int64_t vocab, const void* logits, 
         a.cluster > 1 ? rows : int64_t(sms) * std::max(1, blocks_per_sm(a.stream));
     const void* kern = dtype == CAM_F32 ? reinterpret_cast<const void*>(token_logprobs<float>)
                                         : reinterpret_cast<const void*>(token_logprobs<uint16_t>);
-    ce = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    static std::atomic<uint64_t> shared_ok[2];
+    ce = allow_shared(kern, dev, shared_ok[dtype == CAM_F32 ? 0 : 1]);
     if (ce != cudaSuccess)
         return record_error(CAM_E_CUDA, "%s: %s", fn, cudaGetErrorString(ce));
     cudaLaunchConfig_t cfg{};
