@@ -43,7 +43,6 @@ namespace cg = cooperative_groups;
 
 constexpr int kGvThreads = 256;
 constexpr int kGvWarps = kGvThreads / 32;
-constexpr int kGvDepth = 4;     // ring slots per warp
 constexpr int kGvMaxCols = 32;  // columns of x in one pass (four 8-column operands)
 
 struct GemvArgs {
@@ -65,11 +64,8 @@ struct GemvArgs {
     int32_t x_bf16, y_bf16, x_vec;
 };
 
-__device__ __forceinline__ void cp16(void* smem, const void* gmem) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
-                 :
-                 : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(smem))), "l"(gmem)
-                 : "memory");
+__device__ __forceinline__ void cp16(uint32_t smem, const void* gmem) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" : : "r"(smem), "l"(gmem) : "memory");
 }
 
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -88,10 +84,23 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+__device__ __forceinline__ void mma_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                          uint32_t a3, uint32_t b0, uint32_t b1) {  // c = a b
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+        "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
 // Nibbles p and p + 4 of a word as two bf16: 0x4300 is 128, whose last
 // mantissa bit is 1, so 0x4300 | nibble is 128 + nibble, and less 136 it is q.
+// (One three-input operation takes the nibbles and sets the rest.)
 __device__ __forceinline__ uint32_t widen(uint32_t word, int p) {
-    const uint32_t u = ((word >> (4 * p)) & 0x000F000Fu) | 0x43004300u;
+    uint32_t u;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;"
+        : "=r"(u)
+        : "r"(word >> (4 * p)), "r"(0x000F000Fu), "r"(0x43004300u));
     const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&u),
                                      __nv_bfloat162(__ushort_as_bfloat16(0x4308),
                                                     __ushort_as_bfloat16(0x4308)));
@@ -171,10 +180,14 @@ __device__ __forceinline__ uint16_t round_bf16(float v) {
     return __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
+// Ring slots per warp: enough that every SM has some 64 KB of weights on their way.
+__host__ __device__ constexpr int gv_depth(int rt) { return rt == 1 ? 6 : 4; }
+
 template <int RT, int NT, int GROUP>
-__global__ void __launch_bounds__(kGvThreads, NT <= 2 ? 2 : 1)
+__global__ void __launch_bounds__(kGvThreads, RT * NT == 1 ? 3 : NT <= 2 ? 2 : 1)
     gemv4(const __grid_constant__ GemvArgs a) {
     constexpr int kTile = p4_tile_bytes(GROUP);
+    constexpr int kGvDepth = gv_depth(RT);
     constexpr int kPer = kP4Cols / GROUP;    // scales per row of a tile
     constexpr int kSlot = RT * kTile;
     constexpr int kRedRow = RT * 16 + 4;     // padded: the lanes' rows and columns miss each other's banks
@@ -200,29 +213,46 @@ __global__ void __launch_bounds__(kGvThreads, NT <= 2 ? 2 : 1)
 
     // this warp's steps: for each unit, its tiles across wk, wk + a.wk, ...
     const int per_unit = n_my > wk ? (n_my - wk + a.wk - 1) / a.wk : 0;
-    int l_unit = cluster_id, l_b = 0;  // the next step to load
-    auto load = [&](int slot) {
-        if (l_unit < a.units && per_unit > 0) {
-            const int blk = blk0 + wk + l_b * a.wk;
+    int l_unit = per_unit > 0 ? cluster_id : a.units, l_b = 0;  // the next step to load
+    const uint8_t* l_src[RT];
+    uint32_t l_dst = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + lane * 16;
+    const uint32_t ring_end = l_dst + kGvDepth * kSlot;
+    const int l_jump = a.wk * kTile;
+    auto load = [&]() {
+        if (l_unit < a.units) {
+            if (l_b == 0) {
+#pragma unroll
+                for (int r = 0; r < RT; ++r) {
+                    const int tile = min(l_unit * unit_tiles + wr * RT + r, a.n_tiles - 1);
+                    l_src[r] = a.packed + (int64_t(tile) * a.n_blk + blk0 + wk) * kTile + lane * 16;
+                }
+            }
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
-                const int tile = min(l_unit * unit_tiles + wr * RT + r, a.n_tiles - 1);
-                const uint8_t* src = a.packed + (int64_t(tile) * a.n_blk + blk) * kTile;
-                uint8_t* dst = ring + slot * kSlot + r * kTile;
-                cp16(dst + lane * 16, src + lane * 16);
-                cp16(dst + 512 + lane * 16, src + 512 + lane * 16);
-                if (lane < kPer * 2) cp16(dst + 1024 + lane * 16, src + 1024 + lane * 16);
+                const uint32_t dst = l_dst + r * kTile;
+                cp16(dst, l_src[r]);
+                cp16(dst + 512, l_src[r] + 512);
+                if (lane < kPer * 2) cp16(dst + 1024, l_src[r] + 1024);
+                l_src[r] += l_jump;
             }
             if (++l_b == per_unit) l_b = 0, l_unit += n_clusters;
         }
         cp_commit();
+        l_dst += kSlot;
+        if (l_dst == ring_end) l_dst -= kGvDepth * kSlot;
     };
 #pragma unroll
-    for (int s = 0; s < kGvDepth - 1; ++s) load(s);
+    for (int s = 0; s < kGvDepth - 1; ++s) load();
 
     if (a.x_bf16) stage_x<false>(a, xs, m0, n_tok, C, blk0, n_my);
     else stage_x<true>(a, xs, m0, n_tok, C, blk0, n_my);
     __syncthreads();
+
+    // this lane's column of each operand; past the last column any will do, those results are
+    // not kept
+    int x_lane[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) x_lane[n] = min(8 * n + g, C - 1) * 4 + t;
 
     int slot = 0, buf = 0;
     for (int unit = cluster_id; unit < a.units; unit += n_clusters) {
@@ -237,7 +267,7 @@ __global__ void __launch_bounds__(kGvThreads, NT <= 2 ? 2 : 1)
         for (int b = 0; b < per_unit; ++b) {
             cp_wait<kGvDepth - 2>();
             __syncwarp();  // every lane's copies are in, and every lane is done with the slot before
-            load(slot == 0 ? kGvDepth - 1 : slot - 1);
+            load();
             const uint8_t* q = ring + slot * kSlot;
             if (++slot == kGvDepth) slot = 0;
             const uint4* xb = xs + (wk + b * a.wk) * 16 * C;
@@ -264,20 +294,9 @@ __global__ void __launch_bounds__(kGvThreads, NT <= 2 ? 2 : 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 constexpr int kSteps = GROUP / 32;  // steps of 32 columns per group
-                if (i % kSteps == 0) {
-#pragma unroll
-                    for (int r = 0; r < RT; ++r)
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) part[r][n][j] = 0.0f;
-                }
                 uint4 x[NT];
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    x[n] = make_uint4(0, 0, 0, 0);
-                    if (8 * n + g < C) x[n] = xb[(i * C + 8 * n + g) * 4 + t];
-                }
+                for (int n = 0; n < NT; ++n) x[n] = xb[i * C * 4 + x_lane[n]];
 #pragma unroll
                 for (int r = 0; r < RT; ++r) {
                     const uint32_t lo = i == 0 ? w[r][0].x : i == 1 ? w[r][0].y : i == 2 ? w[r][0].z : w[r][0].w;
@@ -287,7 +306,10 @@ __global__ void __launch_bounds__(kGvThreads, NT <= 2 ? 2 : 1)
                     for (int p = 0; p < 4; ++p) al[p] = widen(lo, p), ah[p] = widen(hi, p);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
-                        mma(part[r][n], al[0], ah[0], al[1], ah[1], x[n].x, x[n].y);
+                        if (i % kSteps == 0)
+                            mma_first(part[r][n], al[0], ah[0], al[1], ah[1], x[n].x, x[n].y);
+                        else
+                            mma(part[r][n], al[0], ah[0], al[1], ah[1], x[n].x, x[n].y);
                         mma(part[r][n], al[2], ah[2], al[3], ah[3], x[n].z, x[n].w);
                     }
                     if (i % kSteps == kSteps - 1) {
@@ -423,10 +445,7 @@ CAM_API int cam_gemv4(int64_t tokens, int64_t rows, int64_t cols, const void* x,
     // where the longest rows of x would not fit even a cluster
     const int planes = a.x_bf16 ? 1 : 3;
     int most = kGvMaxCols / planes;
-    // two row tiles per step where there are rows enough: x's operand is read once for both
-    const int rt = a.n_tiles >= 4 * sms ? 2 : 1;
-    const int ring = kGvWarps * kGvDepth * rt * p4_tile_bytes(group);
-    int passes, C, nt, red;
+    int passes, C, nt, red, rt, ring;
     for (;; most /= 2) {
         if (most == 0) return record_error(CAM_E_ARG, "%s: cols too large", fn);
         passes = (a.tokens + most - 1) / most;
@@ -434,6 +453,10 @@ CAM_API int cam_gemv4(int64_t tokens, int64_t rows, int64_t cols, const void* x,
         passes = (a.tokens + a.pass_tokens - 1) / a.pass_tokens;
         C = a.pass_tokens * planes;
         nt = C <= 8 ? 1 : C <= 16 ? 2 : 4;
+        // two row tiles per step where x's operand is wide and rows are enough: it is read once
+        // for both
+        rt = nt > 1 && a.n_tiles >= 4 * sms ? 2 : 1;
+        ring = kGvWarps * gv_depth(rt) * rt * p4_tile_bytes(group);
         a.red_bufs = C <= 8 ? 2 : 1;
         red = a.red_bufs * kGvWarps * C * (rt * 16 + 4) * 4;
         const int x_room = kMaxSharedBytes - ring - red;
@@ -448,12 +471,21 @@ CAM_API int cam_gemv4(int64_t tokens, int64_t rows, int64_t cols, const void* x,
         if (int64_t(a.cta_blk) * 256 * C <= x_room) break;
     }
     if (passes > 65535) return record_error(CAM_E_ARG, "%s: too many tokens", fn);
-    a.wk = a.cta_blk >= 8 ? 8 : a.cta_blk >= 4 ? 4 : a.cta_blk >= 2 ? 2 : 1;
-    const int unit_tiles = kGvWarps / a.wk * rt;
-    a.units = (a.n_tiles + unit_tiles - 1) / unit_tiles;
     const int bytes = ring + red + a.cta_blk * 256 * C;
-    const int per_sm = nt <= 2 && 2 * (bytes + 1024) <= 228 * 1024 ? 2 : 1;
-    const int clusters = std::max(1, std::min(a.units, sms * per_sm / a.cluster / passes));
+    const int room = 228 * 1024 / (bytes + 1024);
+    const int per_sm = std::min(room, rt * nt == 1 ? 3 : nt <= 2 ? 2 : 1);
+    const int slots = std::max(1, sms * per_sm / a.cluster / passes);
+    // Warps along the columns: more of them even the work out over the blocks, fewer meet less
+    // often. In units of one step, a meeting costs about two.
+    int64_t best = INT64_MAX;
+    for (int wk = 1; wk <= kGvWarps && (wk == 1 || wk <= a.cta_blk); wk *= 2) {
+        const int unit_tiles = kGvWarps / wk * rt;
+        const int units = (a.n_tiles + unit_tiles - 1) / unit_tiles;
+        const int64_t cost =
+            int64_t((units + slots - 1) / slots) * ((a.cta_blk + wk - 1) / wk + 2);
+        if (cost < best) best = cost, a.wk = wk, a.units = units;
+    }
+    const int clusters = std::min(a.units, slots);
 
     const void* kern = kernel_for(rt, nt, group);
     if (bytes > 48 * 1024) {
