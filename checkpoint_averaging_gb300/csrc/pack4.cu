@@ -3,10 +3,9 @@
 // include/cam.h, its layout in pack4_layout.h).
 //
 // Both are streaming, HBM-bound: 4 B (fp32) or 2 B (bf16) per weight on one
-// side, 1/2 + 2 / group B on the other. One warp makes one tile of 16 rows x
-// 128 columns: a row of the tile is one 16-byte (fp32) or 8-byte (bf16) load
-// per lane, all rows' loads in flight before the first use; a group's largest
-// magnitude is a shuffle reduction among the 8, 16 or 32 lanes that hold it.
+// side, 1/2 + 2 / group B on the other. One warp takes one tile of 16 rows x
+// 128 columns, its loads in flight before their first use.
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -21,43 +20,152 @@ namespace {
 
 constexpr int kPkThreads = 256;
 
-// Four columns of one row, widened to fp32; columns past the end are 0.
-__device__ __forceinline__ void load4(const float* p, int n, bool vec, float (&v)[4]) {
-    if (vec && n >= 4) {
-        asm volatile("ld.global.nc.L1::no_allocate.v4.f32 {%0,%1,%2,%3}, [%4];"
-                     : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
-                     : "l"(p));
-        return;
-    }
+__device__ __forceinline__ float widen(uint32_t bits) { return __uint_as_float(bits << 16); }
+__device__ __forceinline__ float load1(const uint16_t* p) { return widen(__ldg(p)); }
+
+// Eight columns of a row as loaded. `fetch` reads them from a row aligned to 16
+// bytes (`eight`: to eight elements), columns past the end as 0. Rows without
+// that alignment, as every odd number of columns gives, are read four bytes to
+// a lane, so that a load is still one run of memory (`gather`, of the row's 128
+// columns), and turned in shared memory (`put`, then `take`).
+template <typename T>
+struct Eight;
+
+template <>
+struct Eight<float> {
+    static constexpr int kBatch = 4;  // steps of two rows whose loads are in flight together
+    float v[8];
+    struct Row {
+        float e[4];
+    };
+    __device__ __forceinline__ void fetch(const float* p, int n, bool eight) {
+        if (eight && n >= 8) {
+            asm volatile(
+                "ld.global.nc.L1::no_allocate.L2::evict_first.v8.f32 "
+                "{%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]),
+                  "=f"(v[6]), "=f"(v[7])
+                : "l"(p));
+            return;
+        }
+        if (n >= 8) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = j < n ? __ldg(p + j) : 0.0f;
-}
-
-__device__ __forceinline__ void load4(const uint16_t* p, int n, bool vec, float (&v)[4]) {
-    if (vec && n >= 4) {
-        uint32_t a, b;
-        asm volatile("ld.global.nc.L1::no_allocate.v2.b32 {%0,%1}, [%2];"
-                     : "=r"(a), "=r"(b)
-                     : "l"(p));
-        v[0] = __uint_as_float(a << 16);
-        v[1] = __uint_as_float(a & 0xFFFF0000u);
-        v[2] = __uint_as_float(b << 16);
-        v[3] = __uint_as_float(b & 0xFFFF0000u);
-        return;
-    }
+            for (int h = 0; h < 2; ++h)
+                asm volatile("ld.global.nc.L1::no_allocate.v4.f32 {%0,%1,%2,%3}, [%4];"
+                             : "=f"(v[4 * h]), "=f"(v[4 * h + 1]), "=f"(v[4 * h + 2]),
+                               "=f"(v[4 * h + 3])
+                             : "l"(p + 4 * h));
+            return;
+        }
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-        v[j] = j < n ? __uint_as_float(static_cast<uint32_t>(__ldg(p + j)) << 16) : 0.0f;
+        for (int j = 0; j < 8; ++j) v[j] = j < n ? __ldg(p + j) : 0.0f;
+    }
+    // n: the row's columns from p on (0 for a row past the end)
+    static __device__ __forceinline__ void gather(Row& r, const float* p, int n, int lane) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r.e[i] = lane + 32 * i < n ? __ldg(p + lane + 32 * i) : 0.0f;
+    }
+    static __device__ __forceinline__ void put(const Row& r, uint32_t* turn, int lane) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) turn[lane + 32 * i] = __float_as_uint(r.e[i]);
+    }
+    __device__ __forceinline__ void take(const uint32_t* turn, int run, const float*) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float4 f = *reinterpret_cast<const float4*>(turn + 8 * run + 4 * h);
+            v[4 * h] = f.x, v[4 * h + 1] = f.y, v[4 * h + 2] = f.z, v[4 * h + 3] = f.w;
+        }
+    }
+    __device__ __forceinline__ float get(int j) const { return v[j]; }
+};
+
+template <>
+struct Eight<uint16_t> {
+    static constexpr int kBatch = 8;
+    uint32_t u[4];
+    // Word j of a row that starts in the upper half of a word (odd) has columns 2 j - 1 and
+    // 2 j, else 2 j and 2 j + 1.
+    struct Row {
+        uint32_t e[3];
+    };
+    static __device__ __forceinline__ int odd(const uint16_t* p) {
+        return static_cast<int>(reinterpret_cast<uintptr_t>(p) >> 1) & 1;
+    }
+    __device__ __forceinline__ void fetch(const uint16_t* p, int n, bool) {
+        if (n >= 8) {
+            asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3])
+                         : "l"(p));
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            u[j] = (2 * j < n ? __ldg(p + 2 * j) : 0u) |
+                   (2 * j + 1 < n ? static_cast<uint32_t>(__ldg(p + 2 * j + 1)) << 16 : 0u);
+    }
+    static __device__ __forceinline__ void gather(Row& r, const uint16_t* p, int n, int lane) {
+        const int o = odd(p);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            const int j = lane + 32 * i, c = 2 * j - o;
+            r.e[i] = 0;
+            if (i == 2 && lane > 0) break;  // (word 64 alone)
+            if (c >= 0 && c + 1 < n)
+                r.e[i] = __ldg(reinterpret_cast<const uint32_t*>(p + c));
+            else if (c >= 0 && c < n)
+                r.e[i] = __ldg(p + c);
+            else if (c == -1 && n > 0)
+                r.e[i] = static_cast<uint32_t>(__ldg(p)) << 16;
+        }
+    }
+    static __device__ __forceinline__ void put(const Row& r, uint32_t* turn, int lane) {
+        turn[lane] = r.e[0];
+        turn[lane + 32] = r.e[1];
+        if (lane == 0) turn[64] = r.e[2];
+    }
+    __device__ __forceinline__ void take(const uint32_t* turn, int run, const uint16_t* p) {
+        const uint4 w = *reinterpret_cast<const uint4*>(turn + 4 * run);
+        const uint32_t last = turn[4 * run + 4];
+        const int by = 16 * odd(p);
+        u[0] = __funnelshift_r(w.x, w.y, by);
+        u[1] = __funnelshift_r(w.y, w.z, by);
+        u[2] = __funnelshift_r(w.z, w.w, by);
+        u[3] = __funnelshift_r(w.w, last, by);
+    }
+    __device__ __forceinline__ float get(int j) const {
+        return __uint_as_float((j & 1) ? u[j >> 1] & 0xFFFF0000u : u[j >> 1] << 16);
+    }
+};
+
+// big / 7 rounded to nearest: the product with 1/7 and one correction by the
+// remainder, which an fma gives exactly (Markstein's step); tiny dividends, whose
+// remainder may not be exact, divide.
+__device__ __forceinline__ float seventh(float big) {
+    if (big < 1e-30f) return __fdiv_rn(big, 7.0f);
+    constexpr float kSeventh = 1.0f / 7.0f;
+    const float q = __fmul_rn(big, kSeventh);
+    return __fmaf_rn(__fmaf_rn(-7.0f, q, big), kSeventh, q);
 }
 
-__device__ __forceinline__ uint32_t to_bf16(float v) {  // nearest-even; NaN stays NaN
-    const uint32_t u = __float_as_uint(v);
-    if ((u & 0x7FFFFFFFu) > 0x7F800000u) return 0x7FFFu;
-    return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
+// 1 / s rounded to nearest for a normal s of 8 significant bits: one Newton step
+// on the hardware's estimate (all 128 significands are tested).
+__device__ __forceinline__ float reciprocal(float s) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+    return __fmaf_rn(__fmaf_rn(-s, r, 1.0f), r, r);
 }
 
-__device__ __forceinline__ void store4(float* p, int n, bool vec, const float (&v)[4]) {
-    if (vec && n >= 4) {
+__device__ __forceinline__ uint32_t to_bf16x2(float lo, float hi) {  // nearest-even
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint16_t to_bf16(float v) {
+    return __bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
+
+// 16 bytes of a row of which n columns are left.
+__device__ __forceinline__ void store16(float* p, int n, const float (&v)[4]) {
+    if (n >= 4) {
         __stcs(reinterpret_cast<float4*>(p), make_float4(v[0], v[1], v[2], v[3]));
         return;
     }
@@ -66,108 +174,200 @@ __device__ __forceinline__ void store4(float* p, int n, bool vec, const float (&
         if (j < n) p[j] = v[j];
 }
 
-__device__ __forceinline__ void store4(uint16_t* p, int n, bool vec, const float (&v)[4]) {
-    if (vec && n >= 4) {
-        __stcs(reinterpret_cast<uint2*>(p), make_uint2(to_bf16(v[0]) | (to_bf16(v[1]) << 16),
-                                                       to_bf16(v[2]) | (to_bf16(v[3]) << 16)));
+__device__ __forceinline__ void store16(uint16_t* p, int n, const float (&v)[8]) {
+    if (n >= 8) {
+        uint32_t u[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) u[j] = to_bf16x2(v[2 * j], v[2 * j + 1]);
+        __stcs(reinterpret_cast<uint4*>(p), make_uint4(u[0], u[1], u[2], u[3]));
         return;
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-        if (j < n) p[j] = static_cast<uint16_t>(to_bf16(v[j]));
+    for (int j = 0; j < 8; ++j)
+        if (j < n) p[j] = to_bf16(v[j]);
 }
 
-template <typename T, int GROUP>
+// One warp makes one tile: 16 lanes to a row, a lane to one word of 8 columns.
+// An integer is rounded by adding 1.5 * 2^23 (+ 8, the nibbles' offset), whose
+// last place is 1: the sum's low bits are q + 8, and as its high bits are the
+// same for all, eight sums shifted to their nibbles and added, less what the
+// high bits add up to, are the word. |w| (1 / s) is at most 7.06, so q never
+// needs holding to [-7, 7].
+template <typename T, int GROUP, bool ALIGNED>
 __global__ void __launch_bounds__(kPkThreads)
-    pack4(int64_t rows, int64_t cols, const T* __restrict__ w, int64_t stride, bool vec,
+    pack4(int64_t rows, int64_t cols, const T* __restrict__ w, int64_t stride, bool eight,
           uint8_t* __restrict__ packed, int64_t n_tiles, int32_t tiles_across) {
     constexpr int kPer = kP4Cols / GROUP;
-    const int lane = threadIdx.x & 31;
+    constexpr float kRound = 12582912.0f + 8.0f;
+    constexpr int kBatch = Eight<T>::kBatch;
+    constexpr int kTurn = 128 / (4 / sizeof(T)) + 4;  // words of a row, and one more
+    __shared__ __align__(16) uint32_t turn[ALIGNED ? 1 : kPkThreads / 32][8][ALIGNED ? 4 : kTurn];
+    const int lane = threadIdx.x & 31, run = lane & 15, odd = lane >> 4, warp = threadIdx.x >> 5;
     const int64_t step = int64_t(gridDim.x) * (kPkThreads / 32);
     for (int64_t tile = int64_t(blockIdx.x) * (kPkThreads / 32) + (threadIdx.x >> 5);
          tile < n_tiles; tile += step) {
-        const int64_t row0 = tile / tiles_across * kP4Rows;
-        const int64_t col = tile % tiles_across * kP4Cols + 4 * lane;
-        const int n = static_cast<int>(max(int64_t(0), min(int64_t(4), cols - col)));
+        const int64_t row0 = tile / tiles_across * kP4Rows + odd;
+        const int64_t col = tile % tiles_across * kP4Cols + 8 * run;
+        const int n = static_cast<int>(max(int64_t(0), min(int64_t(8), cols - col)));
         uint8_t* out = packed + tile * p4_tile_bytes(GROUP);
         uint16_t* scales = reinterpret_cast<uint16_t*>(out + kP4Quants);
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            float v[8][4];
+        for (int b = 0; b < 8 / kBatch; ++b) {
+            Eight<T> v[kBatch];
+            if constexpr (ALIGNED) {
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                const int64_t row = row0 + 8 * half + r;
-                load4(w + row * stride + col, row < rows ? n : 0, vec, v[r]);
+                for (int r = 0; r < kBatch; ++r) {
+                    const int64_t row = row0 + 2 * (b * kBatch + r);
+                    v[r].fetch(w + row * stride + col, row < rows ? n : 0, eight);
+                }
+            } else {
+                const int64_t base = tile / tiles_across * kP4Rows;
+                const int64_t col0 = tile % tiles_across * kP4Cols;
+                const int in_cols = static_cast<int>(min(int64_t(kP4Cols), cols - col0));
+#pragma unroll
+                for (int q = 0; q < kBatch / 4; ++q) {  // eight rows at a time
+                    typename Eight<T>::Row got[8];
+                    const int64_t first = base + 2 * b * kBatch + 8 * q;
+#pragma unroll
+                    for (int r = 0; r < 8; ++r)
+                        Eight<T>::gather(got[r], w + (first + r) * stride + col0,
+                                         first + r < rows ? in_cols : 0, lane);
+                    __syncwarp();
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) Eight<T>::put(got[r], turn[warp][r], lane);
+                    __syncwarp();
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        v[4 * q + r].take(turn[warp][2 * r + odd], run,
+                                          w + (first + 2 * r + odd) * stride + col0);
+                }
             }
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
+            for (int r = 0; r < kBatch; ++r) {
+                const int row = 2 * (b * kBatch + r) + odd;
                 // the group's largest magnitude as bits: for non-negative floats the order of
                 // the bits is the order of the values, with NaN above infinity
                 uint32_t big = 0;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) big = max(big, __float_as_uint(v[r][j]) & 0x7FFFFFFFu);
+                for (int j = 0; j < 8; ++j) big = max(big, __float_as_uint(v[r].get(j)) & 0x7FFFFFFFu);
 #pragma unroll
-                for (int o = 1; o < GROUP / 4; o *= 2)
+                for (int o = 1; o < GROUP / 8; o *= 2)
                     big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, o));
                 const bool fine = big < 0x7F800000u;
-                uint32_t sb = __float_as_uint(__fdiv_rn(__uint_as_float(big), 7.0f)) & 0xFFFF0000u;
-                if (sb < 0x00800000u) sb = 0;  // below 2^-126
-                if (!fine) sb = 0x7FC00000u;
-                const float inv = sb != 0 && fine ? __frcp_rn(__uint_as_float(sb)) : 0.0f;
-                uint32_t word = 0;
+                uint32_t s = __float_as_uint(seventh(__uint_as_float(big))) & 0xFFFF0000u;
+                const bool live = fine && s >= 0x00800000u;  // from 2^-126
+                if (!live) s = fine ? 0u : 0x7FC00000u;
+                const float inv = reciprocal(__uint_as_float(live ? s : 0x3F800000u));
+                // column c of the eight belongs in nibble c / 2 + 4 (c % 2)
+                uint32_t word = 0, high = 0;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int q = __float2int_rn(fine ? __fmul_rn(v[r][j], inv) : 0.0f);
-                    const uint32_t nib = static_cast<uint32_t>(min(max(q, -7), 7) + 8);
-                    // column j of the word's lower (even lane) or upper four: see the layout
-                    const int c = 4 * (lane & 1) + j;
-                    word |= nib << (4 * ((c >> 1) + 4 * (c & 1)));
+                for (int c = 0; c < 8; ++c) {
+                    const int at = 4 * ((c >> 1) + 4 * (c & 1));
+                    word += __float_as_uint(__fadd_rn(__fmul_rn(v[r].get(c), inv), kRound)) << at;
+                    high += 0x4B400000u << at;
                 }
-                word |= __shfl_xor_sync(0xFFFFFFFFu, word, 1);
-                if ((lane & 1) == 0)
-                    *reinterpret_cast<uint32_t*>(out + p4_word(8 * half + r, lane >> 1)) = word;
-                if (lane % (GROUP / 4) == 0)
-                    scales[p4_scale(8 * half + r, lane / (GROUP / 4), kPer)] =
-                        static_cast<uint16_t>(sb >> 16);
+                word = live ? word - high : 0x88888888u;
+                *reinterpret_cast<uint32_t*>(out + p4_word(row, run)) = word;
+                if (run % (GROUP / 8) == 0)
+                    scales[p4_scale(row, run / (GROUP / 8), kPer)] = static_cast<uint16_t>(s >> 16);
             }
         }
     }
 }
 
-template <typename T, int GROUP>
+// The value of one of a word's eight columns: a nibble set into 2^23 is
+// 2^23 + q + 8, exactly.
+__device__ __forceinline__ float value(uint32_t word, int column, float s) {
+    uint32_t u;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;"
+        : "=r"(u)
+        : "r"(word >> (4 * ((column >> 1) + 4 * (column & 1)))), "r"(0xFu), "r"(0x4B000000u));
+    return __fmul_rn(__fsub_rn(__uint_as_float(u), 8388608.0f + 8.0f), s);
+}
+
+// One warp takes one tile. Aligned rows are written 16 bytes to a lane, others
+// an element (fp32) or an aligned pair of them (bf16) to a lane, so that a store
+// is still one run of memory.
+template <typename T, int GROUP, bool ALIGNED>
 __global__ void __launch_bounds__(kPkThreads)
     unpack4(int64_t rows, int64_t cols, const uint8_t* __restrict__ packed, T* __restrict__ values,
-            int64_t stride, bool vec, int64_t n_tiles, int32_t tiles_across) {
+            int64_t stride, int64_t n_tiles, int32_t tiles_across) {
     constexpr int kPer = kP4Cols / GROUP;
+    constexpr int kC = 16 / sizeof(T);       // columns of a 16-byte store
+    constexpr int kRows = 32 / (128 / kC);   // rows of a warp's store
     const int lane = threadIdx.x & 31;
     const int64_t step = int64_t(gridDim.x) * (kPkThreads / 32);
     for (int64_t tile = int64_t(blockIdx.x) * (kPkThreads / 32) + (threadIdx.x >> 5);
          tile < n_tiles; tile += step) {
         const int64_t row0 = tile / tiles_across * kP4Rows;
-        const int64_t col = tile % tiles_across * kP4Cols + 4 * lane;
-        const int n = static_cast<int>(max(int64_t(0), min(int64_t(4), cols - col)));
+        const int64_t col0 = tile % tiles_across * kP4Cols;
+        const int in_rows = static_cast<int>(min(int64_t(kP4Rows), rows - row0));
+        const int in_cols = static_cast<int>(min(int64_t(kP4Cols), cols - col0));
         const uint8_t* in = packed + tile * p4_tile_bytes(GROUP);
         const uint16_t* scales = reinterpret_cast<const uint16_t*>(in + kP4Quants);
-        uint32_t word[kP4Rows];
-        float s[kP4Rows];
+        T* out = values + row0 * stride + col0;
+        auto word_of = [&](int r, int col) {
+            return __ldg(reinterpret_cast<const uint32_t*>(in + p4_word(r, col >> 3)));
+        };
+        auto scale_of = [&](int r, int col) {
+            return load1(scales + p4_scale(r, col / GROUP, kPer));
+        };
+        if constexpr (ALIGNED) {
+            const int col = kC * (lane % (128 / kC)), sub = lane / (128 / kC);
+            uint32_t word[kP4Rows / kRows];
+            float s[kP4Rows / kRows];
 #pragma unroll
-        for (int r = 0; r < kP4Rows; ++r) {
-            word[r] = __ldg(reinterpret_cast<const uint32_t*>(in + p4_word(r, lane >> 1)));
-            s[r] = __uint_as_float(
-                static_cast<uint32_t>(__ldg(scales + p4_scale(r, lane / (GROUP / 4), kPer))) << 16);
-        }
-#pragma unroll
-        for (int r = 0; r < kP4Rows; ++r) {
-            const int64_t row = row0 + r;
-            if (row >= rows) break;
-            float v[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int c = 4 * (lane & 1) + j;
-                const int nib = (word[r] >> (4 * ((c >> 1) + 4 * (c & 1)))) & 15;
-                v[j] = __fmul_rn(static_cast<float>(nib - 8), s[r]);
+            for (int r = 0; r < kP4Rows / kRows; ++r) {
+                word[r] = word_of(kRows * r + sub, col);
+                s[r] = scale_of(kRows * r + sub, col);
             }
-            store4(values + row * stride + col, n, vec, v);
+#pragma unroll
+            for (int r = 0; r < kP4Rows / kRows; ++r) {
+                const int row = kRows * r + sub;
+                if (row >= in_rows) break;
+                float v[kC];
+#pragma unroll
+                for (int j = 0; j < kC; ++j) v[j] = value(word[r], (col & 7) + j, s[r]);
+                store16(out + row * stride + col, in_cols - col, v);
+            }
+        } else if constexpr (sizeof(T) == 4) {
+#pragma unroll 4
+            for (int r = 0; r < in_rows; ++r) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int col = lane + 32 * i;
+                    const float v = value(word_of(r, col), col & 7, scale_of(r, col));
+                    if (col < in_cols) out[r * stride + col] = v;
+                }
+            }
+        } else {
+#pragma unroll 4
+            for (int r = 0; r < in_rows; ++r) {
+                T* at = out + r * stride;
+                const int odd = static_cast<int>(reinterpret_cast<uintptr_t>(at) >> 1) & 1;
+                uint32_t before = 0;  // the last pair of the block before, on every lane
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int col = 64 * i + 2 * lane;
+                    const uint32_t word = word_of(r, col);
+                    const float s = scale_of(r, col);
+                    const uint32_t both = to_bf16x2(value(word, col & 7, s), value(word, (col & 7) + 1, s));
+                    // columns c, c + 1 of the aligned word that starts with col, or ends with it
+                    const uint32_t left = __shfl_up_sync(0xFFFFFFFFu, both, 1);
+                    const int c = col - odd;
+                    const uint32_t pair =
+                        odd ? __funnelshift_r(lane == 0 ? before : left, both, 16) : both;
+                    if (c >= 0 && c + 1 < in_cols)
+                        *reinterpret_cast<uint32_t*>(at + c) = pair;
+                    else if (c >= 0 && c < in_cols)
+                        at[c] = static_cast<uint16_t>(pair);
+                    else if (c == -1)
+                        at[0] = static_cast<uint16_t>(both);
+                    before = __shfl_sync(0xFFFFFFFFu, both, 31);
+                    if (odd && i == 1 && lane == 31 && in_cols == kP4Cols)
+                        at[kP4Cols - 1] = static_cast<uint16_t>(both >> 16);
+                }
+            }
         }
     }
 }
@@ -198,18 +398,18 @@ int check_matrix(const char* fn, int64_t rows, int64_t cols, const void* m, int6
     return CAM_OK;
 }
 
-template <typename T>
+template <typename T, bool ALIGNED>
 const void* pack_kernel(int32_t group) {
-    return group == 32   ? reinterpret_cast<const void*>(pack4<T, 32>)
-           : group == 64 ? reinterpret_cast<const void*>(pack4<T, 64>)
-                         : reinterpret_cast<const void*>(pack4<T, 128>);
+    return group == 32   ? reinterpret_cast<const void*>(pack4<T, 32, ALIGNED>)
+           : group == 64 ? reinterpret_cast<const void*>(pack4<T, 64, ALIGNED>)
+                         : reinterpret_cast<const void*>(pack4<T, 128, ALIGNED>);
 }
 
-template <typename T>
+template <typename T, bool ALIGNED>
 const void* unpack_kernel(int32_t group) {
-    return group == 32   ? reinterpret_cast<const void*>(unpack4<T, 32>)
-           : group == 64 ? reinterpret_cast<const void*>(unpack4<T, 64>)
-                         : reinterpret_cast<const void*>(unpack4<T, 128>);
+    return group == 32   ? reinterpret_cast<const void*>(unpack4<T, 32, ALIGNED>)
+           : group == 64 ? reinterpret_cast<const void*>(unpack4<T, 64, ALIGNED>)
+                         : reinterpret_cast<const void*>(unpack4<T, 128, ALIGNED>);
 }
 
 }  // namespace
@@ -233,10 +433,14 @@ CAM_API int cam_pack4(int64_t rows, int64_t cols, const void* w, int64_t stride,
     int32_t across = static_cast<int32_t>((cols + cam::kP4Cols - 1) / cam::kP4Cols);
     int64_t tiles = (rows + cam::kP4Rows - 1) / cam::kP4Rows * across;
     const int size = dtype == CAM_F32 ? 4 : 2;
-    bool vec = cam::row_aligned(w, stride, size, 4 * size);
-    void* args[] = {&rows, &cols, &w, &stride, &vec, &packed, &tiles, &across};
+    const bool aligned = cam::row_aligned(w, stride, size, 16);
+    bool eight = cam::row_aligned(w, stride, size, 8 * size);
+    void* args[] = {&rows, &cols, &w, &stride, &eight, &packed, &tiles, &across};
     const cudaError_t ce = cudaLaunchKernel(
-        dtype == CAM_F32 ? cam::pack_kernel<float>(group) : cam::pack_kernel<uint16_t>(group),
+        dtype == CAM_F32
+            ? aligned ? cam::pack_kernel<float, true>(group) : cam::pack_kernel<float, false>(group)
+        : aligned ? cam::pack_kernel<uint16_t, true>(group)
+                  : cam::pack_kernel<uint16_t, false>(group),
         dim3(cam::blocks_for(tiles)), dim3(cam::kPkThreads), args, 0,
         static_cast<cudaStream_t>(stream));
     if (ce != cudaSuccess)
@@ -253,10 +457,13 @@ CAM_API int cam_unpack4(int64_t rows, int64_t cols, const void* packed, int32_t 
     int32_t across = static_cast<int32_t>((cols + cam::kP4Cols - 1) / cam::kP4Cols);
     int64_t tiles = (rows + cam::kP4Rows - 1) / cam::kP4Rows * across;
     const int size = dtype == CAM_F32 ? 4 : 2;
-    bool vec = cam::row_aligned(values, stride, size, 4 * size);
-    void* args[] = {&rows, &cols, &packed, &values, &stride, &vec, &tiles, &across};
+    const bool aligned = cam::row_aligned(values, stride, size, 16);
+    void* args[] = {&rows, &cols, &packed, &values, &stride, &tiles, &across};
     const cudaError_t ce = cudaLaunchKernel(
-        dtype == CAM_F32 ? cam::unpack_kernel<float>(group) : cam::unpack_kernel<uint16_t>(group),
+        dtype == CAM_F32
+            ? aligned ? cam::unpack_kernel<float, true>(group) : cam::unpack_kernel<float, false>(group)
+        : aligned ? cam::unpack_kernel<uint16_t, true>(group)
+                  : cam::unpack_kernel<uint16_t, false>(group),
         dim3(cam::blocks_for(tiles)), dim3(cam::kPkThreads), args, 0,
         static_cast<cudaStream_t>(stream));
     if (ce != cudaSuccess)

@@ -132,6 +132,27 @@ def test_zero_tiny_huge_and_broken_groups():
         assert (np.delete(v[r], np.s_[32 * j:32 * j + 32]) == 0).all()
 
 
+@pytest.mark.parametrize("exponent", [-126, -120, -60, 0, 60, 121])
+def test_every_scale_is_divided_by_exactly(exponent):
+    # one group for each of the 128 significands a scale can have, at its smallest and its
+    # largest |w|, the other weights anywhere below
+    m = np.arange(128)
+    s = ((1 + m / 128) * 2.0 ** exponent).astype(np.float32)
+    g = np.random.default_rng(1)
+    w = (g.uniform(-7, 7, (256, 64)) * np.concatenate([s, s])[:, None]).astype(np.float32)
+    w[:128, 0] = s * np.float32(7)
+    w[128:, 0] = -(s.astype(np.float64) * 7 * (1 + 1 / 128 / (1 + m / 128) - 1e-6)).astype(np.float32)
+    w[:, 1] = np.float32(0.5) * np.concatenate([s, s])  # ties, and next to them
+    w[:, 2] = np.float32(-2.5) * np.concatenate([s, s])
+    w[:, 3] = np.nextafter(np.float32(1.5) * np.concatenate([s, s]), np.float32(0))
+    q, want = form(w, 64)
+    pk = B.pack4(torch.from_numpy(w).to(DEV), 64)
+    dq, ds = decode(pk.data.cpu().numpy(), 256, 64, 64)
+    np.testing.assert_array_equal(ds[:256, :1], want)
+    np.testing.assert_array_equal(dq[:256, :64], q[:, 0])
+    assert len(np.unique(want)) >= 128
+
+
 def check_product(x, pk, w, group, y):
     q, s = form(w, group)
     v = values(q, s, w.shape[1]).astype(np.float64)
