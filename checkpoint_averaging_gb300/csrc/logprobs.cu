@@ -850,7 +850,7 @@ __global__ void __launch_bounds__(kLpMaxBlock, 2)
 
 constexpr int kLbThreads = 256;
 constexpr int kLbBatch = 4;   // vectors per thread in flight
-constexpr int kLbBlocks = 4;  // blocks per SM
+constexpr int kLbBlocks = 5;  // blocks per SM that rows are cut for
 
 struct LogprobGradArgs {
     const void* logits;
@@ -865,7 +865,6 @@ struct LogprobGradArgs {
     int64_t pieces;  // rows * parts
     int32_t vocab;
     int32_t parts;   // pieces per row
-    int32_t team;    // threads of a piece: 32 to kLbThreads, a power of two
 };
 
 // The logits may be the gradient's own buffer, so these loads are plain ones.
@@ -915,18 +914,18 @@ __device__ __forceinline__ GradRow grad_row(const LogprobGradArgs& a, int64_t ro
     return r;
 }
 
-// A piece of a row for each `team` threads of a block; a team has about a batch
-// or two of vectors per thread. (Blocks that walk over many pieces, with the
+// A piece of a row for each TEAM threads of a block; a team has about a batch or
+// two of vectors per thread. (Blocks that walk over many pieces, with the
 // next piece's row values loaded ahead, measured 5 to 8 % slower.) With
 // y = (x - lse) log2(e), every logit's gradient is
 //   -p (g + h (log p + H)) = 2^y (b + k y),  k = -h ln 2,  b = -(g + h H).
 // y is one fma, x log2(e) - RN(lse log2(e)); what that rounding (and lse_lo)
 // leaves out is the same for all logits of the row, so it goes into b and k.
-template <typename T>
-__global__ void __launch_bounds__(kLbThreads, kLbBlocks)
+template <typename T, int TEAM>
+__global__ void __launch_bounds__(kLbThreads)
     token_logprobs_backward(const __grid_constant__ LogprobGradArgs a) {
-    constexpr int kN = Vec16<T>::kN;
-    const int team = a.team, tid = threadIdx.x & (team - 1);
+    constexpr int kN = Vec16<T>::kN, team = TEAM;
+    const int tid = threadIdx.x % team;
     const int64_t piece = int64_t(blockIdx.x) * (kLbThreads / team) + threadIdx.x / team;
     if (piece >= a.pieces) return;
     const int64_t row = piece / a.parts;
@@ -1012,6 +1011,14 @@ __global__ void __launch_bounds__(kLbThreads, kLbBlocks)
         if (!zeros && r.token == id) y += g;
         store1(out + id, y);
     }
+}
+
+template <typename T>
+const void* backward_kernel(int team) {
+    return team == 32    ? reinterpret_cast<const void*>(token_logprobs_backward<T, 32>)
+           : team == 64  ? reinterpret_cast<const void*>(token_logprobs_backward<T, 64>)
+           : team == 128 ? reinterpret_cast<const void*>(token_logprobs_backward<T, 128>)
+                         : reinterpret_cast<const void*>(token_logprobs_backward<T, kLbThreads>);
 }
 
 int check_logits(const char* fn, int64_t rows, int64_t vocab, const void* logits, int64_t stride,
@@ -1146,13 +1153,12 @@ CAM_API int cam_token_logprobs_backward(int64_t rows, int64_t vocab, const void*
         parts = std::max(parts, std::min((n_vec + team - 1) / team, slots / rows));
     LogprobGradArgs a{logits, grad_logits, stride, grad_stride, tokens, lse, lse_lo, entropy,
                       grad_logp, grad_entropy, rows * parts, static_cast<int32_t>(vocab),
-                      static_cast<int32_t>(parts), team};
+                      static_cast<int32_t>(parts)};
     const int64_t blocks = (a.pieces + kLbThreads / team - 1) / (kLbThreads / team);
     if (blocks > INT32_MAX) return record_error(CAM_E_ARG, "%s: too many logits", fn);
     void* args[] = {&a};
-    const void* kern = dtype == CAM_F32
-                           ? reinterpret_cast<const void*>(token_logprobs_backward<float>)
-                           : reinterpret_cast<const void*>(token_logprobs_backward<uint16_t>);
+    const void* kern =
+        dtype == CAM_F32 ? backward_kernel<float>(team) : backward_kernel<uint16_t>(team);
     ce = cudaLaunchKernel(kern, dim3(static_cast<unsigned>(blocks)),
                           dim3(kLbThreads), args, 0, static_cast<cudaStream_t>(stream));
     if (ce != cudaSuccess)
