@@ -16,14 +16,15 @@
 // first; at a few columns per weight the tensor cores are far from the bound
 // either way.
 //
-// A block holds x (its share of the columns) in shared memory in the order of
-// the operand and walks over units of rows. Its warps split a unit's tiles
-// along the columns (and over rows where there are few columns); each streams
-// its tiles through a private ring of cp.async slots, ahead across units, so
-// the loads never wait for a unit's sums. A cluster of blocks splits the
-// columns further where x would not fit or where there are too few rows to
-// fill the GPU; sums meet in distributed shared memory, in a fixed order.
-#include <cooperative_groups.h>
+// A block has a run of the matrix's 16-row tiles, a like share for every block,
+// and holds x in shared memory in the order of the operand. Its warps share out
+// the run's 128-column records evenly, in the order they lie in memory: each
+// streams its part through a private ring of cp.async slots, as one straight
+// read, and never waits for another until it is done. A tile that is cut
+// between warps belongs to the warp that has its first record; the others leave
+// their sums in shared memory, and after one barrier the owner adds them, in
+// order. Where x's rows are too long for shared memory they are taken in slabs
+// of columns, a tile's sums kept in shared memory from slab to slab.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -39,12 +40,6 @@
 namespace cam {
 namespace {
 
-namespace cg = cooperative_groups;
-
-constexpr int kGvThreads = 256;
-constexpr int kGvWarps = kGvThreads / 32;
-constexpr int kGvMaxCols = 32;  // columns of x in one pass (four 8-column operands)
-
 struct GemvArgs {
     const void* x;
     const uint8_t* packed;
@@ -54,14 +49,10 @@ struct GemvArgs {
     int32_t cols;
     int32_t tokens;       // of the call
     int32_t pass_tokens;  // of one pass (grid.y passes)
-    int32_t n_blk;        // 128-column tiles across
-    int32_t cta_blk;      // of which a block of the cluster takes so many
+    int32_t n_blk;        // 128-column records of a tile
+    int32_t slab_blk;     // of which x has so many in shared memory at once
     int32_t n_tiles;      // 16-row tiles
-    int32_t units;
-    int32_t wk;           // warps along the columns; kGvWarps / wk along the rows
-    int32_t red_bufs;     // 1 or 2 buffers of partial sums
-    int32_t cluster;
-    int32_t x_bf16, y_bf16, x_vec;
+    int32_t y_bf16, x_vec;
 };
 
 __device__ __forceinline__ void cp16(uint32_t smem, const void* gmem) {
@@ -122,19 +113,20 @@ __device__ __forceinline__ void terms(float x, uint32_t (&t)[3]) {
     t[2] = __float_as_uint(r - __uint_as_float(__float_as_uint(r) & 0xFFFF0000u)) >> 16;
 }
 
-// x's columns of this block and pass into shared memory: 16 bytes (8
-// elements) at ((block-local tile * 4 + i) * C + column) * 4 + t, elements
-// 32 i + 8 t .. + 7 of the tile. Elements past the end are 0.
+// A slab of x into shared memory: 16 bytes (8 elements) of a column at
+// ((slab-local record * 4 + i) * C + column) * 4 + t, elements 32 i + 8 t .. + 7 of
+// the record. An fp32 x has three columns for a token, n_tok apart. Elements
+// past the end are 0.
 template <bool F32>
 __device__ __forceinline__ void stage_x(const GemvArgs& a, uint4* xs, int m0, int n_tok, int C,
                                         int blk0, int n_my) {
     const int runs = n_my * 16;
-    for (int idx = threadIdx.x; idx < runs * n_tok; idx += kGvThreads) {
-        const int m = idx / runs, run = idx - m * runs;  // run = (tile, i, t)
+    for (int idx = threadIdx.x; idx < runs * n_tok; idx += blockDim.x) {
+        const int m = idx / runs, run = idx - m * runs;  // run = (record, i, t)
         const int k = blk0 * kP4Cols + run * 8;
         const int left = min(8, a.cols - k);
         const int64_t at = int64_t(m0 + m) * a.x_stride + k;
-        uint4* dst = xs + (run >> 2) * C * 4 + (run & 3);
+        uint4* dst = xs + ((run >> 2) * C + m) * 4 + (run & 3);
         if constexpr (F32) {
             const float* p = static_cast<const float*>(a.x) + at;
             float v[8];
@@ -158,7 +150,7 @@ __device__ __forceinline__ void stage_x(const GemvArgs& a, uint4* xs, int m0, in
             }
 #pragma unroll
             for (int q = 0; q < 3; ++q)
-                dst[(3 * m + q) * 4] = make_uint4(w[q][0], w[q][1], w[q][2], w[q][3]);
+                dst[q * n_tok * 4] = make_uint4(w[q][0], w[q][1], w[q][2], w[q][3]);
         } else {
             const uint16_t* p = static_cast<const uint16_t*>(a.x) + at;
             uint4 v;
@@ -171,7 +163,7 @@ __device__ __forceinline__ void stage_x(const GemvArgs& a, uint4* xs, int m0, in
                 v = make_uint4(e[0] | (e[1] << 16), e[2] | (e[3] << 16), e[4] | (e[5] << 16),
                                e[6] | (e[7] << 16));
             }
-            dst[m * 4] = v;
+            *dst = v;
         }
     }
 }
@@ -180,217 +172,319 @@ __device__ __forceinline__ uint16_t round_bf16(float v) {
     return __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
-// Ring slots per warp: enough that every SM has some 64 KB of weights on their way.
-__host__ __device__ constexpr int gv_depth(int rt) { return rt == 1 ? 6 : 4; }
+// The forms of the kernel by columns of x: NT operands of 8 columns. bf16: up to
+// 8, 16 or 32 tokens (NT 1, 2, 4). fp32: up to 2 tokens packed in one operand
+// (NT 1), else three operands for each 8 tokens (NT 3, 6), so that a token's
+// three sums stand in one lane. Few columns take many small blocks per SM, many
+// columns one large one, whose warps share its x.
+template <bool F32, int NT>
+struct GvForm {
+    static constexpr bool kPacked = F32 && NT == 1;
+    static constexpr int kWarps = NT <= 2 ? 8 : 16;
+    static constexpr int kBlocks = NT == 1 ? 3 : NT == 2 ? 2 : 1;  // per SM
+    static constexpr int kDepth = NT <= 2 ? 6 : 4;                 // ring slots per warp
+    static constexpr int kOut = F32 && NT > 1 ? NT / 3 : NT;       // operands of sums kept
+    static constexpr int kTokens = F32 ? (NT == 1 ? 2 : 8 * NT / 3) : 8 * NT;
+};
 
-template <int RT, int NT, int GROUP>
-__global__ void __launch_bounds__(kGvThreads, RT * NT == 1 ? 3 : NT <= 2 ? 2 : 1)
+template <bool F32, int NT, int GROUP>
+__global__ void __launch_bounds__(GvForm<F32, NT>::kWarps * 32, GvForm<F32, NT>::kBlocks)
     gemv4(const __grid_constant__ GemvArgs a) {
-    constexpr int kTile = p4_tile_bytes(GROUP);
-    constexpr int kGvDepth = gv_depth(RT);
-    constexpr int kPer = kP4Cols / GROUP;    // scales per row of a tile
-    constexpr int kSlot = RT * kTile;
-    constexpr int kRedRow = RT * 16 + 4;     // padded: the lanes' rows and columns miss each other's banks
+    using Form = GvForm<F32, NT>;
+    constexpr int kTile = p4_tile_bytes(GROUP), kPer = kP4Cols / GROUP;
+    constexpr int kWarps = Form::kWarps, kDepth = Form::kDepth, kOut = Form::kOut;
     extern __shared__ __align__(128) uint8_t smem[];
+    int* slot_tile = reinterpret_cast<int*>(smem);  // (128 bytes)
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int rank = a.cluster > 1 ? static_cast<int>(cg::this_cluster().block_rank()) : 0;
-    const int n_clusters = gridDim.x / a.cluster, cluster_id = blockIdx.x / a.cluster;
     const int m0 = blockIdx.y * a.pass_tokens;
     const int n_tok = min(a.pass_tokens, a.tokens - m0);
-    const int planes = a.x_bf16 ? 1 : 3;
-    const int C = n_tok * planes;
-    const int blk0 = rank * a.cta_blk;
-    const int n_my = max(0, min(a.cta_blk, a.n_blk - blk0));  // this block's tiles across
-    const int wr = warp / a.wk, wk = warp - wr * a.wk;
-    const int wpr = kGvWarps / a.wk;                          // warps along the rows
-    const int unit_tiles = wpr * RT;
+    const int C = F32 ? 3 * n_tok : n_tok;
+    const int tile0 = static_cast<int>(int64_t(a.n_tiles) * blockIdx.x / gridDim.x);
+    const int my_tiles = static_cast<int>(int64_t(a.n_tiles) * (blockIdx.x + 1) / gridDim.x) - tile0;
+    const bool slabs = a.slab_blk < a.n_blk;
 
-    uint8_t* ring = smem + warp * (kGvDepth * kSlot);
-    uint4* xs = reinterpret_cast<uint4*>(smem + kGvWarps * kGvDepth * kSlot);
-    float* red = reinterpret_cast<float*>(xs + a.cta_blk * 16 * C);
-    const int red_floats = kGvWarps * C * kRedRow;
+    // the rings, the slots of cut tiles' sums, x, and (slabs) every tile's sums
+    uint8_t* ring = smem + 128 + warp * (kDepth * kTile);
+    float4* slot = reinterpret_cast<float4*>(smem + 128 + kWarps * kDepth * kTile);
+    uint4* xs = reinterpret_cast<uint4*>(slot + kWarps * kOut * 32);
+    float4* kept = reinterpret_cast<float4*>(xs + a.slab_blk * 16 * C);
 
-    // this warp's steps: for each unit, its tiles across wk, wk + a.wk, ...
-    const int per_unit = n_my > wk ? (n_my - wk + a.wk - 1) / a.wk : 0;
-    int l_unit = per_unit > 0 ? cluster_id : a.units, l_b = 0;  // the next step to load
-    const uint8_t* l_src[RT];
+    // this warp's records of the slab that starts at record blk0 of each tile
+    auto range = [&](int blk0, int& begin, int& end) {
+        const int64_t n = int64_t(my_tiles) * min(a.slab_blk, a.n_blk - blk0);
+        begin = static_cast<int>(n * warp / kWarps);
+        end = static_cast<int>(n * (warp + 1) / kWarps);
+    };
+
+    // loads run ahead of the sums, over tiles and slabs
+    int l_blk0 = 0, l_nb = 0, l_at = 0, l_left = 0;
+    bool l_more = a.n_blk > 0;
+    const uint8_t* l_src = nullptr;
+    auto open_slab = [&]() {  // to the first of this warp's records, from slab l_blk0 on
+        for (; l_more; l_blk0 += a.slab_blk) {
+            if (l_blk0 >= a.n_blk) {
+                l_more = false;
+                return;
+            }
+            int begin, end;
+            range(l_blk0, begin, end);
+            l_nb = min(a.slab_blk, a.n_blk - l_blk0);
+            if (begin == end) continue;
+            l_left = end - begin;
+            l_at = begin % l_nb;
+            l_src = a.packed + (int64_t(tile0 + begin / l_nb) * a.n_blk + l_blk0 + l_at) * kTile +
+                    lane * 16;
+            return;
+        }
+    };
+    open_slab();
     uint32_t l_dst = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + lane * 16;
-    const uint32_t ring_end = l_dst + kGvDepth * kSlot;
-    const int l_jump = a.wk * kTile;
+    const uint32_t ring_end = l_dst + kDepth * kTile;
     auto load = [&]() {
-        if (l_unit < a.units) {
-            if (l_b == 0) {
-#pragma unroll
-                for (int r = 0; r < RT; ++r) {
-                    const int tile = min(l_unit * unit_tiles + wr * RT + r, a.n_tiles - 1);
-                    l_src[r] = a.packed + (int64_t(tile) * a.n_blk + blk0 + wk) * kTile + lane * 16;
-                }
+        if (l_more) {
+            cp16(l_dst, l_src);
+            cp16(l_dst + 512, l_src + 512);
+            if (lane < kPer * 2) cp16(l_dst + 1024, l_src + 1024);
+            l_src += kTile;
+            if (++l_at == l_nb) {
+                l_at = 0;
+                if (slabs) l_src += int64_t(a.n_blk - l_nb) * kTile;
             }
-#pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                const uint32_t dst = l_dst + r * kTile;
-                cp16(dst, l_src[r]);
-                cp16(dst + 512, l_src[r] + 512);
-                if (lane < kPer * 2) cp16(dst + 1024, l_src[r] + 1024);
-                l_src[r] += l_jump;
+            if (--l_left == 0) {
+                l_blk0 += a.slab_blk;
+                open_slab();
             }
-            if (++l_b == per_unit) l_b = 0, l_unit += n_clusters;
         }
         cp_commit();
-        l_dst += kSlot;
-        if (l_dst == ring_end) l_dst -= kGvDepth * kSlot;
+        l_dst += kTile;
+        if (l_dst == ring_end) l_dst -= kDepth * kTile;
     };
 #pragma unroll
-    for (int s = 0; s < kGvDepth - 1; ++s) load();
+    for (int s = 0; s < kDepth - 1; ++s) load();
 
-    if (a.x_bf16) stage_x<false>(a, xs, m0, n_tok, C, blk0, n_my);
-    else stage_x<true>(a, xs, m0, n_tok, C, blk0, n_my);
-    __syncthreads();
-
-    // this lane's column of each operand; past the last column any will do, those results are
-    // not kept
+    // this lane's column of each operand; past the last token any will do, its results are not
+    // kept
     int x_lane[NT];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) x_lane[n] = min(8 * n + g, C - 1) * 4 + t;
+    for (int n = 0; n < NT; ++n) {
+        if constexpr (F32 && NT > 1)
+            x_lane[n] = (n / kOut * n_tok + min(8 * (n % kOut) + g, n_tok - 1)) * 4 + t;
+        else
+            x_lane[n] = min(8 * n + g, C - 1) * 4 + t;
+    }
 
-    int slot = 0, buf = 0;
-    for (int unit = cluster_id; unit < a.units; unit += n_clusters) {
-        float acc[RT][NT][4];
-#pragma unroll
-        for (int r = 0; r < RT; ++r)
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[r][n][j] = 0.0f;
-
-        for (int b = 0; b < per_unit; ++b) {
-            cp_wait<kGvDepth - 2>();
-            __syncwarp();  // every lane's copies are in, and every lane is done with the slot before
-            load();
-            const uint8_t* q = ring + slot * kSlot;
-            if (++slot == kGvDepth) slot = 0;
-            const uint4* xb = xs + (wk + b * a.wk) * 16 * C;
-            uint4 w[RT][2];
-            uint32_t sc[RT][2][kPer > 1 ? kPer / 2 : 1];  // bf16 pairs (kPer 1: both rows in one)
-#pragma unroll
-            for (int r = 0; r < RT; ++r) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    w[r][h] = *reinterpret_cast<const uint4*>(q + r * kTile + h * 512 + lane * 16);
-                const uint8_t* s = q + r * kTile + 1024 + g * (4 * kPer);
-                if constexpr (kPer == 4) {
-                    const uint4 v = *reinterpret_cast<const uint4*>(s);
-                    sc[r][0][0] = v.x, sc[r][0][1] = v.y, sc[r][1][0] = v.z, sc[r][1][1] = v.w;
-                } else if constexpr (kPer == 2) {
-                    const uint2 v = *reinterpret_cast<const uint2*>(s);
-                    sc[r][0][0] = v.x, sc[r][1][0] = v.y;
-                } else {
-                    sc[r][0][0] = *reinterpret_cast<const uint32_t*>(s);
-                    sc[r][1][0] = sc[r][0][0] >> 16;
+    // A tile's finished sums. v[n]: rows g (x, y) and g + 8 (z, w), columns 8 n + 2 t and + 1.
+    auto write = [&](int tile, const float4 (&v)[kOut]) {
+        const int64_t row = int64_t(tile) * kP4Rows + g;
+        auto put = [&](int m, int64_t r, float value) {
+            if (m >= n_tok || r >= a.rows) return;
+            const int64_t to = int64_t(m0 + m) * a.y_stride + r;
+            if (a.y_bf16) static_cast<uint16_t*>(a.y)[to] = round_bf16(value);
+            else static_cast<float*>(a.y)[to] = value;
+        };
+        if constexpr (Form::kPacked) {
+            // a token's three columns stand in neighbouring lanes
+            for (int m = 0; m < n_tok; ++m) {
+                float lo = 0.0f, hi = 0.0f;
+                for (int q = 2; q >= 0; --q) {
+                    const int c = q * n_tok + m, from = (lane & ~3) | (c >> 1);
+                    const float x = __shfl_sync(0xFFFFFFFFu, v[0].x, from);
+                    const float y = __shfl_sync(0xFFFFFFFFu, v[0].y, from);
+                    const float z = __shfl_sync(0xFFFFFFFFu, v[0].z, from);
+                    const float w = __shfl_sync(0xFFFFFFFFu, v[0].w, from);
+                    lo += (c & 1) ? y : x;
+                    hi += (c & 1) ? w : z;
                 }
+                if (t == 0) put(m, row, lo);
+                if (t == 1) put(m, row + 8, hi);
             }
-            float part[RT][NT][4];
+        } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                constexpr int kSteps = GROUP / 32;  // steps of 32 columns per group
-                uint4 x[NT];
-#pragma unroll
-                for (int n = 0; n < NT; ++n) x[n] = xb[i * C * 4 + x_lane[n]];
-#pragma unroll
-                for (int r = 0; r < RT; ++r) {
-                    const uint32_t lo = i == 0 ? w[r][0].x : i == 1 ? w[r][0].y : i == 2 ? w[r][0].z : w[r][0].w;
-                    const uint32_t hi = i == 0 ? w[r][1].x : i == 1 ? w[r][1].y : i == 2 ? w[r][1].z : w[r][1].w;
-                    uint32_t al[4], ah[4];
-#pragma unroll
-                    for (int p = 0; p < 4; ++p) al[p] = widen(lo, p), ah[p] = widen(hi, p);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        if (i % kSteps == 0)
-                            mma_first(part[r][n], al[0], ah[0], al[1], ah[1], x[n].x, x[n].y);
-                        else
-                            mma(part[r][n], al[0], ah[0], al[1], ah[1], x[n].x, x[n].y);
-                        mma(part[r][n], al[2], ah[2], al[3], ah[3], x[n].z, x[n].w);
-                    }
-                    if (i % kSteps == kSteps - 1) {
-                        const int j = i / kSteps;
-                        const float s0 = __uint_as_float((j & 1) ? sc[r][0][j >> 1] & 0xFFFF0000u
-                                                                 : sc[r][0][j >> 1] << 16);
-                        const float s1 = __uint_as_float((j & 1) ? sc[r][1][j >> 1] & 0xFFFF0000u
-                                                                 : sc[r][1][j >> 1] << 16);
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            acc[r][n][0] = fmaf(s0, part[r][n][0], acc[r][n][0]);
-                            acc[r][n][1] = fmaf(s0, part[r][n][1], acc[r][n][1]);
-                            acc[r][n][2] = fmaf(s1, part[r][n][2], acc[r][n][2]);
-                            acc[r][n][3] = fmaf(s1, part[r][n][3], acc[r][n][3]);
-                        }
-                    }
-                }
+            for (int n = 0; n < kOut; ++n) {
+                const int m = 8 * n + 2 * t;
+                put(m, row, v[n].x);
+                put(m + 1, row, v[n].y);
+                put(m, row + 8, v[n].z);
+                put(m + 1, row + 8, v[n].w);
             }
         }
+    };
+    auto add = [](float4& s, const float4& v) {
+        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    };
+    // ... of this slab: to the result, or onto what the slabs before left
+    auto finish = [&](int tile, int blk0, float4 (&v)[kOut]) {
+        if (slabs) {
+            float4* k = kept + (tile - tile0) * kOut * 32 + lane;
+            const bool last = blk0 + a.slab_blk >= a.n_blk;
+#pragma unroll
+            for (int n = 0; n < kOut; ++n) {
+                if (blk0 > 0) {
+                    float4 s = k[n * 32];
+                    add(s, v[n]);
+                    v[n] = s;
+                }
+                if (!last) k[n * 32] = v[n];
+            }
+            if (!last) return;
+        }
+        write(tile, v);
+    };
 
-        // the warps' (and blocks') sums meet: [warp][column][row]
-        float* mine = red + buf * red_floats + warp * C * kRedRow;
+    uint32_t at_slot = 0;
+    for (int blk0 = 0; blk0 == 0 || blk0 < a.n_blk; blk0 += a.slab_blk) {
+        const int nb = min(a.slab_blk, a.n_blk - blk0);
+        if (blk0 > 0) __syncthreads();  // every warp is done with the slab of x before
+        stage_x<F32>(a, xs, m0, n_tok, C, blk0, nb);
+        if (lane == 0) slot_tile[warp] = -1;
+        __syncthreads();
+        if (nb == 0) {  // no columns: the sums are 0
+            float4 zero[kOut];
+#pragma unroll
+            for (int n = 0; n < kOut; ++n) zero[n] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int i = warp; i < my_tiles; i += kWarps) write(tile0 + i, zero);
+            return;
+        }
+        int begin, end;
+        range(blk0, begin, end);
+        int tile = tile0 + begin / nb, b = begin % nb;
+        bool owner = b == 0, open = false;  // the tile under way: has its first record; not finished
+        float acc[NT][4];
+        float4 v[kOut];
+        auto gather = [&]() {  // a token's three terms together, the smallest first
+#pragma unroll
+            for (int n = 0; n < kOut; ++n) {
+                v[n] = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
+                if constexpr (F32 && NT > 1) {
+                    v[n].x += acc[kOut + n][0] + acc[2 * kOut + n][0];
+                    v[n].y += acc[kOut + n][1] + acc[2 * kOut + n][1];
+                    v[n].z += acc[kOut + n][2] + acc[2 * kOut + n][2];
+                    v[n].w += acc[kOut + n][3] + acc[2 * kOut + n][3];
+                }
+            }
+        };
+        auto leave = [&]() {  // another warp's tile
+            gather();
+#pragma unroll
+            for (int n = 0; n < kOut; ++n) slot[(warp * kOut + n) * 32 + lane] = v[n];
+            if (lane == 0) slot_tile[warp] = tile;
+        };
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int c = 8 * n + 2 * t + (j & 1);
-                if (c < C) {
+            for (int j = 0; j < 4; ++j) acc[n][j] = 0.0f;
+        for (int pos = begin; pos < end; ++pos) {
+            cp_wait<kDepth - 2>();
+            __syncwarp();  // every lane's copies are in, and every lane is done with the slot before
+            load();
+            const uint8_t* q = ring + at_slot * kTile;
+            if (++at_slot == kDepth) at_slot = 0;
+            const uint4* xb = xs + b * 16 * C;
+            const uint4 wl = *reinterpret_cast<const uint4*>(q + lane * 16);
+            const uint4 wh = *reinterpret_cast<const uint4*>(q + 512 + lane * 16);
+            uint32_t sl[kPer > 1 ? kPer / 2 : 1], sh[kPer > 1 ? kPer / 2 : 1];  // bf16 pairs
+            const uint8_t* sp = q + 1024 + g * (4 * kPer);
+            if constexpr (kPer == 4) {
+                const uint4 s = *reinterpret_cast<const uint4*>(sp);
+                sl[0] = s.x, sl[1] = s.y, sh[0] = s.z, sh[1] = s.w;
+            } else if constexpr (kPer == 2) {
+                const uint2 s = *reinterpret_cast<const uint2*>(sp);
+                sl[0] = s.x, sh[0] = s.y;
+            } else {
+                sl[0] = *reinterpret_cast<const uint32_t*>(sp);
+                sh[0] = sl[0] >> 16;
+            }
+            float part[NT][4];
 #pragma unroll
-                    for (int r = 0; r < RT; ++r)
-                        mine[c * kRedRow + 16 * r + 8 * (j >> 1) + g] = acc[r][n][j];
+            for (int i = 0; i < 4; ++i) {
+                constexpr int kSteps = GROUP / 32;  // steps of 32 columns per group
+                const uint32_t lo = i == 0 ? wl.x : i == 1 ? wl.y : i == 2 ? wl.z : wl.w;
+                const uint32_t hi = i == 0 ? wh.x : i == 1 ? wh.y : i == 2 ? wh.z : wh.w;
+                uint32_t al[4], ah[4];
+#pragma unroll
+                for (int p = 0; p < 4; ++p) al[p] = widen(lo, p), ah[p] = widen(hi, p);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const uint4 x = xb[i * C * 4 + x_lane[n]];
+                    if (i % kSteps == 0) mma_first(part[n], al[0], ah[0], al[1], ah[1], x.x, x.y);
+                    else mma(part[n], al[0], ah[0], al[1], ah[1], x.x, x.y);
+                    mma(part[n], al[2], ah[2], al[3], ah[3], x.z, x.w);
+                }
+                if (i % kSteps == kSteps - 1) {
+                    const int j = i / kSteps;
+                    const float s0 = __uint_as_float((j & 1) ? sl[j >> 1] & 0xFFFF0000u : sl[j >> 1] << 16);
+                    const float s1 = __uint_as_float((j & 1) ? sh[j >> 1] & 0xFFFF0000u : sh[j >> 1] << 16);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        acc[n][0] = fmaf(s0, part[n][0], acc[n][0]);
+                        acc[n][1] = fmaf(s0, part[n][1], acc[n][1]);
+                        acc[n][2] = fmaf(s1, part[n][2], acc[n][2]);
+                        acc[n][3] = fmaf(s1, part[n][3], acc[n][3]);
+                    }
                 }
             }
-        if (a.cluster > 1) cg::this_cluster().sync();
-        else __syncthreads();
-        const int unit_rows = unit_tiles * 16;
-        const int64_t row0 = int64_t(unit) * unit_rows;
-        for (int o = threadIdx.x + kGvThreads * rank; o < unit_rows * n_tok;
-             o += kGvThreads * a.cluster) {
-            const int m = o / unit_rows, row = o - m * unit_rows;
-            const int rw = row / (RT * 16), in = row - rw * (RT * 16);
-            if (row0 + row >= a.rows) continue;
-            float sum = 0.0f;
-            for (int p = planes - 1; p >= 0; --p) {
-                const float* at = red + buf * red_floats +
-                                  (rw * a.wk * C + m * planes + p) * kRedRow + in;
-                for (int c = 0; c < a.cluster; ++c) {
-                    const float* from = a.cluster > 1 ? cg::this_cluster().map_shared_rank(at, c) : at;
-                    for (int k = 0; k < a.wk; ++k) sum += from[k * C * kRedRow];
+            open = true;
+            if (++b == nb) {
+                if (owner) {
+                    gather();
+                    finish(tile, blk0, v);
+                } else {
+                    leave();
                 }
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[n][j] = 0.0f;
+                b = 0, ++tile;
+                owner = true, open = false;
             }
-            const int64_t to = int64_t(m0 + m) * a.y_stride + row0 + row;
-            if (a.y_bf16) static_cast<uint16_t*>(a.y)[to] = round_bf16(sum);
-            else static_cast<float*>(a.y)[to] = sum;
         }
-        if (a.red_bufs == 2) {
-            buf ^= 1;
-        } else {
-            if (a.cluster > 1) cg::this_cluster().sync();
-            else __syncthreads();
+        if (open && !owner) leave();
+        __syncthreads();
+        if (open && owner) {
+            gather();
+            for (int w = warp + 1; w < kWarps; ++w) {
+                if (slot_tile[w] != tile) continue;
+#pragma unroll
+                for (int n = 0; n < kOut; ++n) add(v[n], slot[(w * kOut + n) * 32 + lane]);
+            }
+            finish(tile, blk0, v);
         }
     }
     cp_wait<0>();
-    if (a.cluster > 1) cg::this_cluster().sync();  // no block leaves while another reads its sums
 }
 
-template <int RT, int NT>
+template <bool F32, int NT>
 const void* kernel_for_group(int group) {
-    return group == 32   ? reinterpret_cast<const void*>(gemv4<RT, NT, 32>)
-           : group == 64 ? reinterpret_cast<const void*>(gemv4<RT, NT, 64>)
-                         : reinterpret_cast<const void*>(gemv4<RT, NT, 128>);
+    return group == 32   ? reinterpret_cast<const void*>(gemv4<F32, NT, 32>)
+           : group == 64 ? reinterpret_cast<const void*>(gemv4<F32, NT, 64>)
+                         : reinterpret_cast<const void*>(gemv4<F32, NT, 128>);
 }
 
-const void* kernel_for(int rt, int nt, int group) {
-    if (rt == 1)
-        return nt == 1   ? kernel_for_group<1, 1>(group)
-               : nt == 2 ? kernel_for_group<1, 2>(group)
-                         : kernel_for_group<1, 4>(group);
-    return nt == 1   ? kernel_for_group<2, 1>(group)
-           : nt == 2 ? kernel_for_group<2, 2>(group)
-                     : kernel_for_group<2, 4>(group);
+// A form's launch: its kernel, and what the host needs to know of it.
+struct GvPlan {
+    const void* kernel;
+    int warps, blocks, depth, out, tokens;
+    std::atomic<uint64_t>* shared_ok;
+};
+
+template <bool F32, int NT>
+GvPlan plan_of(int group) {
+    using Form = GvForm<F32, NT>;
+    static std::atomic<uint64_t> shared_ok[3];
+    return {kernel_for_group<F32, NT>(group), Form::kWarps,  Form::kBlocks, Form::kDepth,
+            Form::kOut,                       Form::kTokens, &shared_ok[group == 32 ? 0 : group / 64]};
+}
+
+GvPlan plan_for(bool f32, int tokens, int group) {
+    if (f32)
+        return tokens <= 2 ? plan_of<true, 1>(group)
+               : tokens <= 8 ? plan_of<true, 3>(group)
+                             : plan_of<true, 6>(group);
+    return tokens <= 8    ? plan_of<false, 1>(group)
+           : tokens <= 16 ? plan_of<false, 2>(group)
+                          : plan_of<false, 4>(group);
 }
 
 }  // namespace
@@ -438,75 +532,43 @@ CAM_API int cam_gemv4(int64_t tokens, int64_t rows, int64_t cols, const void* x,
     a.tokens = static_cast<int32_t>(tokens);
     a.n_blk = static_cast<int32_t>((cols + kP4Cols - 1) / kP4Cols);
     a.n_tiles = static_cast<int32_t>((rows + kP4Rows - 1) / kP4Rows);
-    a.x_bf16 = x_dtype == CAM_BF16;
     a.y_bf16 = y_dtype == CAM_BF16;
     a.x_vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && x_stride * x_size % 16 == 0;
-    // tokens in as few passes over the weights as their columns allow, evenly; fewer at a time
-    // where the longest rows of x would not fit even a cluster
-    const int planes = a.x_bf16 ? 1 : 3;
-    int most = kGvMaxCols / planes;
-    int passes, C, nt, red, rt, ring;
-    for (;; most /= 2) {
-        if (most == 0) return record_error(CAM_E_ARG, "%s: cols too large", fn);
-        passes = (a.tokens + most - 1) / most;
-        a.pass_tokens = (a.tokens + passes - 1) / passes;
-        passes = (a.tokens + a.pass_tokens - 1) / a.pass_tokens;
-        C = a.pass_tokens * planes;
-        nt = C <= 8 ? 1 : C <= 16 ? 2 : 4;
-        // two row tiles per step where x's operand is wide and rows are enough: it is read once
-        // for both
-        rt = nt > 1 && a.n_tiles >= 4 * sms ? 2 : 1;
-        ring = kGvWarps * gv_depth(rt) * rt * p4_tile_bytes(group);
-        a.red_bufs = C <= 8 ? 2 : 1;
-        red = a.red_bufs * kGvWarps * C * (rt * 16 + 4) * 4;
-        const int x_room = kMaxSharedBytes - ring - red;
-        // the columns split over a cluster until x fits, and further while blocks are fewer
-        // than SMs
-        a.cluster = 1;
-        while (a.cluster < 8 &&
-               (int64_t((a.n_blk + a.cluster - 1) / a.cluster) * 256 * C > x_room ||
-                (int64_t(a.n_tiles) * passes * 2 * a.cluster <= sms && a.n_blk >= 16 * a.cluster)))
-            a.cluster *= 2;
-        a.cta_blk = (a.n_blk + a.cluster - 1) / a.cluster;
-        if (int64_t(a.cta_blk) * 256 * C <= x_room) break;
-    }
+    // as few passes over the weights as the widest form allows, evenly
+    const bool f32 = x_dtype == CAM_F32;
+    const int most = f32 ? GvForm<true, 6>::kTokens : GvForm<false, 4>::kTokens;
+    int passes = (a.tokens + most - 1) / most;
+    a.pass_tokens = (a.tokens + passes - 1) / passes;
+    passes = (a.tokens + a.pass_tokens - 1) / a.pass_tokens;
     if (passes > 65535) return record_error(CAM_E_ARG, "%s: too many tokens", fn);
-    const int bytes = ring + red + a.cta_blk * 256 * C;
-    const int room = 228 * 1024 / (bytes + 1024);
-    const int per_sm = std::min(room, rt * nt == 1 ? 3 : nt <= 2 ? 2 : 1);
-    const int slots = std::max(1, sms * per_sm / a.cluster / passes);
-    // Warps along the columns: more of them even the work out over the blocks, fewer meet less
-    // often. In units of one step, a meeting costs about two.
-    int64_t best = INT64_MAX;
-    for (int wk = 1; wk <= kGvWarps && (wk == 1 || wk <= a.cta_blk); wk *= 2) {
-        const int unit_tiles = kGvWarps / wk * rt;
-        const int units = (a.n_tiles + unit_tiles - 1) / unit_tiles;
-        const int64_t cost =
-            int64_t((units + slots - 1) / slots) * ((a.cta_blk + wk - 1) / wk + 2);
-        if (cost < best) best = cost, a.wk = wk, a.units = units;
+    const GvPlan p = plan_for(f32, a.pass_tokens, group);
+    // Shared memory: rings and slots, then x, whole if it fits beside the other blocks of the SM
+    // or, alone, in half of what is left, with the rest for the tiles' sums.
+    const int record = 256 * (f32 ? 3 : 1) * a.pass_tokens;  // bytes of x per record of a tile
+    const int fixed = 128 + p.warps * (p.depth * p4_tile_bytes(group) + p.out * 512);
+    int per_sm = p.blocks;
+    while (per_sm > 1 && int64_t(record) * a.n_blk + fixed > 228 * 1024 / per_sm - 1280) --per_sm;
+    const int room = (per_sm > 1 ? 228 * 1024 / per_sm - 1280 : kMaxSharedBytes) - fixed;
+    int64_t blocks = std::min<int64_t>(a.n_tiles, std::max(1, sms * per_sm / passes));
+    int kept = 0;
+    a.slab_blk = a.n_blk;
+    if (int64_t(record) * a.n_blk > room) {
+        const int kept_room = room / 2, per_tile = p.out * 512;
+        const int64_t tiles = kept_room / per_tile;  // a block may have at most
+        blocks = std::max(blocks, (a.n_tiles + tiles - 1) / tiles);
+        kept = static_cast<int>((a.n_tiles + blocks - 1) / blocks) * per_tile;
+        a.slab_blk = std::max(1, (room - kept) / record);
+        const int slabs = (a.n_blk + a.slab_blk - 1) / a.slab_blk;
+        a.slab_blk = (a.n_blk + slabs - 1) / slabs;
     }
-    const int clusters = std::min(a.units, slots);
+    a.slab_blk = std::max(1, a.slab_blk);
+    const int bytes = fixed + kept + a.slab_blk * record;
 
-    const void* kern = kernel_for(rt, nt, group);
-    if (bytes > 48 * 1024) {
-        static std::atomic<uint64_t> shared_ok[2][3][3];
-        ce = allow_shared(kern, dev,
-                          shared_ok[rt - 1][nt == 4 ? 2 : nt - 1][group == 32 ? 0 : group / 64]);
-    }
+    if (bytes > 48 * 1024) ce = allow_shared(p.kernel, dev, *p.shared_ok);
     if (ce == cudaSuccess) {
-        cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3(clusters * a.cluster, passes);
-        cfg.blockDim = dim3(kGvThreads);
-        cfg.dynamicSmemBytes = bytes;
-        cfg.stream = s;
-        cudaLaunchAttribute attr{};
-        attr.id = cudaLaunchAttributeClusterDimension;
-        attr.val.clusterDim.x = a.cluster;
-        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-        cfg.attrs = &attr;
-        cfg.numAttrs = a.cluster > 1 ? 1 : 0;
         void* args[] = {&a};
-        ce = cudaLaunchKernelExC(&cfg, kern, args);
+        ce = cudaLaunchKernel(p.kernel, dim3(static_cast<unsigned>(blocks), passes),
+                              dim3(p.warps * 32), args, bytes, s);
     }
     if (ce != cudaSuccess)
         return record_error(CAM_E_CUDA, "%s: launch: %s", fn, cudaGetErrorString(ce));
