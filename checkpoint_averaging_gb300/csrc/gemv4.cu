@@ -24,7 +24,10 @@
 // between warps belongs to the warp that has its first record; the others leave
 // their sums in shared memory, and after one barrier the owner adds them, in
 // order. Where x's rows are too long for shared memory they are taken in slabs
-// of columns, a tile's sums kept in shared memory from slab to slab.
+// of columns, a tile's sums kept in shared memory from slab to slab; where there
+// are too few rows to fill the GPU, the blocks of a cluster take the slabs of one
+// run of tiles side by side and add up through distributed shared memory.
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -40,6 +43,8 @@
 namespace cam {
 namespace {
 
+namespace cg = cooperative_groups;
+
 struct GemvArgs {
     const void* x;
     const uint8_t* packed;
@@ -52,6 +57,7 @@ struct GemvArgs {
     int32_t n_blk;        // 128-column records of a tile
     int32_t slab_blk;     // of which x has so many in shared memory at once
     int32_t n_tiles;      // 16-row tiles
+    int32_t cluster;      // blocks that share a run of tiles, each with its own slabs
     int32_t y_bf16, x_vec;
 };
 
@@ -200,9 +206,12 @@ __global__ void __launch_bounds__(GvForm<F32, NT>::kWarps * 32, GvForm<F32, NT>:
     const int m0 = blockIdx.y * a.pass_tokens;
     const int n_tok = min(a.pass_tokens, a.tokens - m0);
     const int C = F32 ? 3 * n_tok : n_tok;
-    const int tile0 = static_cast<int>(int64_t(a.n_tiles) * blockIdx.x / gridDim.x);
-    const int my_tiles = static_cast<int>(int64_t(a.n_tiles) * (blockIdx.x + 1) / gridDim.x) - tile0;
+    const int rank = a.cluster > 1 ? static_cast<int>(cg::this_cluster().block_rank()) : 0;
+    const int run = blockIdx.x / a.cluster, runs = gridDim.x / a.cluster;
+    const int tile0 = static_cast<int>(int64_t(a.n_tiles) * run / runs);
+    const int my_tiles = static_cast<int>(int64_t(a.n_tiles) * (run + 1) / runs) - tile0;
     const bool slabs = a.slab_blk < a.n_blk;
+    const int first_blk = rank * a.slab_blk, next_slab = a.cluster * a.slab_blk;
 
     // the rings, the slots of cut tiles' sums, x, and (slabs) every tile's sums
     uint8_t* ring = smem + 128 + warp * (kDepth * kTile);
@@ -218,11 +227,11 @@ __global__ void __launch_bounds__(GvForm<F32, NT>::kWarps * 32, GvForm<F32, NT>:
     };
 
     // loads run ahead of the sums, over tiles and slabs
-    int l_blk0 = 0, l_nb = 0, l_at = 0, l_left = 0;
+    int l_blk0 = first_blk, l_nb = 0, l_at = 0, l_left = 0;
     bool l_more = a.n_blk > 0;
     const uint8_t* l_src = nullptr;
     auto open_slab = [&]() {  // to the first of this warp's records, from slab l_blk0 on
-        for (; l_more; l_blk0 += a.slab_blk) {
+        for (; l_more; l_blk0 += next_slab) {
             if (l_blk0 >= a.n_blk) {
                 l_more = false;
                 return;
@@ -252,7 +261,7 @@ __global__ void __launch_bounds__(GvForm<F32, NT>::kWarps * 32, GvForm<F32, NT>:
                 if (slabs) l_src += int64_t(a.n_blk - l_nb) * kTile;
             }
             if (--l_left == 0) {
-                l_blk0 += a.slab_blk;
+                l_blk0 += next_slab;
                 open_slab();
             }
         }
@@ -317,10 +326,10 @@ __global__ void __launch_bounds__(GvForm<F32, NT>::kWarps * 32, GvForm<F32, NT>:
     auto finish = [&](int tile, int blk0, float4 (&v)[kOut]) {
         if (slabs) {
             float4* k = kept + (tile - tile0) * kOut * 32 + lane;
-            const bool last = blk0 + a.slab_blk >= a.n_blk;
+            const bool last = a.cluster == 1 && blk0 + next_slab >= a.n_blk;
 #pragma unroll
             for (int n = 0; n < kOut; ++n) {
-                if (blk0 > 0) {
+                if (blk0 > first_blk) {
                     float4 s = k[n * 32];
                     add(s, v[n]);
                     v[n] = s;
@@ -333,9 +342,9 @@ __global__ void __launch_bounds__(GvForm<F32, NT>::kWarps * 32, GvForm<F32, NT>:
     };
 
     uint32_t at_slot = 0;
-    for (int blk0 = 0; blk0 == 0 || blk0 < a.n_blk; blk0 += a.slab_blk) {
+    for (int blk0 = first_blk; blk0 == 0 || blk0 < a.n_blk; blk0 += next_slab) {
         const int nb = min(a.slab_blk, a.n_blk - blk0);
-        if (blk0 > 0) __syncthreads();  // every warp is done with the slab of x before
+        if (blk0 > first_blk) __syncthreads();  // every warp is done with the slab of x before
         stage_x<F32>(a, xs, m0, n_tok, C, blk0, nb);
         if (lane == 0) slot_tile[warp] = -1;
         __syncthreads();
@@ -453,6 +462,23 @@ __global__ void __launch_bounds__(GvForm<F32, NT>::kWarps * 32, GvForm<F32, NT>:
         }
     }
     cp_wait<0>();
+    if (a.cluster > 1) {
+        // a tile's sums from all blocks, in the order of their slabs
+        cg::cluster_group cluster = cg::this_cluster();
+        cluster.sync();
+        for (int i = rank * kWarps + warp; i < my_tiles; i += a.cluster * kWarps) {
+            float4 v[kOut];
+#pragma unroll
+            for (int n = 0; n < kOut; ++n) v[n] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int r = 0; r < a.cluster; ++r) {
+                const float4* k = cluster.map_shared_rank(kept, r) + i * kOut * 32 + lane;
+#pragma unroll
+                for (int n = 0; n < kOut; ++n) add(v[n], k[n * 32]);
+            }
+            write(tile0 + i, v);
+        }
+        cluster.sync();  // no block leaves while another reads its sums
+    }
 }
 
 template <bool F32, int NT>
@@ -552,13 +578,19 @@ CAM_API int cam_gemv4(int64_t tokens, int64_t rows, int64_t cols, const void* x,
     int64_t blocks = std::min<int64_t>(a.n_tiles, std::max(1, sms * per_sm / passes));
     int kept = 0;
     a.slab_blk = a.n_blk;
-    if (int64_t(record) * a.n_blk > room) {
+    // few rows: a cluster for each tile or so, as long as a warp has a few records
+    a.cluster = 1;
+    while (a.cluster < 8 && blocks * passes * a.cluster * 2 <= sms &&
+           a.n_blk >= a.cluster * 4 * p.warps)
+        a.cluster *= 2;
+    if (a.cluster > 1 || int64_t(record) * a.n_blk > room) {
         const int kept_room = room / 2, per_tile = p.out * 512;
         const int64_t tiles = kept_room / per_tile;  // a block may have at most
         blocks = std::max(blocks, (a.n_tiles + tiles - 1) / tiles);
         kept = static_cast<int>((a.n_tiles + blocks - 1) / blocks) * per_tile;
         a.slab_blk = std::max(1, (room - kept) / record);
-        const int slabs = (a.n_blk + a.slab_blk - 1) / a.slab_blk;
+        int slabs = (a.n_blk + a.slab_blk - 1) / a.slab_blk;
+        slabs = (slabs + a.cluster - 1) / a.cluster * a.cluster;
         a.slab_blk = (a.n_blk + slabs - 1) / slabs;
     }
     a.slab_blk = std::max(1, a.slab_blk);
@@ -567,8 +599,18 @@ CAM_API int cam_gemv4(int64_t tokens, int64_t rows, int64_t cols, const void* x,
     if (bytes > 48 * 1024) ce = allow_shared(p.kernel, dev, *p.shared_ok);
     if (ce == cudaSuccess) {
         void* args[] = {&a};
-        ce = cudaLaunchKernel(p.kernel, dim3(static_cast<unsigned>(blocks), passes),
-                              dim3(p.warps * 32), args, bytes, s);
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(static_cast<unsigned>(blocks * a.cluster), passes);
+        cfg.blockDim = dim3(p.warps * 32);
+        cfg.dynamicSmemBytes = bytes;
+        cfg.stream = s;
+        cudaLaunchAttribute attr{};
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = a.cluster;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = a.cluster > 1 ? 1 : 0;
+        ce = cudaLaunchKernelExC(&cfg, p.kernel, args);
     }
     if (ce != cudaSuccess)
         return record_error(CAM_E_CUDA, "%s: launch: %s", fn, cudaGetErrorString(ce));
