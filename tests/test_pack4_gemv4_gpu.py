@@ -184,6 +184,16 @@ def test_products(tokens, rows, cols, group, dtype):
     assert torch.equal(B.gemv4(x, pk), y)  # the same bits again
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("tokens,rows,cols", [
+    (1, 14700, 64), (1, 19400, 256), (2, 19456, 1), (5, 19456, 513), (6, 40000, 129),
+    (11, 18999, 130), (16, 19000, 1024), (17, 38000, 640), (32, 19333, 384), (40, 19456, 128)])
+def test_products_of_many_rows(tokens, rows, cols, group, dtype):
+    # rows enough to fill the GPU with units of 128 of them
+    test_products(tokens, rows, cols, group, dtype)
+
+
 @pytest.mark.parametrize("tokens,cols", [(1, 131072), (2, 131072), (32, 131072)])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_the_longest_rows(tokens, cols, dtype):
