@@ -23,8 +23,16 @@ from . import binding as _b
 LOGPROBS_MAX_TOP = _b.LOGPROBS_MAX_TOP
 _CODES = {torch.float32: _b.F32, torch.bfloat16: _b.BF16}
 _empty, _FLOAT, _INT64 = torch.empty, torch.float32, torch.int64
-_current_device = torch.cuda.current_device
 _L = _b.lib()
+
+
+def _initialised_device() -> int:
+    return torch.cuda.current_device()
+
+
+# (current_device() but for its check that CUDA is initialised, which it is wherever a
+# CUDA tensor exists)
+_current_device = getattr(torch._C, "_cuda_getDevice", _initialised_device)
 
 
 def _raw_stream(device: int) -> int:
@@ -34,6 +42,11 @@ def _raw_stream(device: int) -> int:
 # (torch keeps the handle of the current stream without an object for it, which takes a
 # twentieth of the time)
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+
+
+_gemv4, _logprobs, _logprobs_backward = \
+    _L.cam_gemv4, _L.cam_token_logprobs, _L.cam_token_logprobs_backward
+_pack4, _unpack4 = _L.cam_pack4, _L.cam_unpack4
 
 
 def _failed(rc: int):
@@ -53,10 +66,10 @@ def _refuse(t, what: str):
 
 def _matrix(t, what: str):
     """(rows, cols, elements between row starts, dtype code) of a matrix argument."""
-    code = _CODES.get(t.dtype)
-    if code is None or t.dim() != 2 or not t.is_cuda:
+    code, shape = _CODES.get(t.dtype), t.shape
+    if code is None or len(shape) != 2 or not t.is_cuda:
         _refuse(t, what)
-    rows, cols = t.shape
+    rows, cols = shape
     ld, step = t.stride()
     if step != 1 and cols > 1:
         _refuse(t, what)
@@ -92,7 +105,7 @@ class Packed4:
     """A matrix in the 4-bit form (include/cam.h): ``data`` is its bytes (uint8,
     1-D, on the GPU), which may be saved and made a Packed4 of again."""
 
-    __slots__ = ("data", "rows", "cols", "group", "_at", "_device")
+    __slots__ = ("data", "rows", "cols", "group", "_at", "_device", "_place")
 
     def __init__(self, data, rows: int, cols: int, group: int):
         if not data.is_cuda or data.dtype != torch.uint8 or not data.is_contiguous() \
@@ -104,7 +117,7 @@ class Packed4:
 
     def _set(self, data, rows, cols, group, at, device):
         self.data, self.rows, self.cols, self.group = data, rows, cols, group
-        self._at, self._device = at, device
+        self._at, self._device, self._place = at, device, data.device
         return self
 
     @property
@@ -127,7 +140,7 @@ def pack4(weight, group: int = 64, *, stream=None) -> Packed4:
     data = _empty(size, dtype=torch.uint8, device=weight.device)
     at = data.data_ptr()
     handle = _current_stream(device) if stream is None else _on_stream(stream, (weight, data))
-    rc = _L.cam_pack4(rows, cols, weight.data_ptr(), ld, code, group, at, handle)
+    rc = _pack4(rows, cols, weight.data_ptr(), ld, code, group, at, handle)
     if rc:
         _failed(rc)
     return Packed4.__new__(Packed4)._set(data, rows, cols, group, at, device)
@@ -152,7 +165,7 @@ def unpack4(packed: Packed4, dtype=None, *, out=None, stream=None):
         _, _, ld, code = _matrix(out, "out")
         _same_device(device, out)
     handle = _current_stream(device) if stream is None else _on_stream(stream, (packed.data, out))
-    rc = _L.cam_unpack4(rows, cols, packed._at, packed.group, out.data_ptr(), ld, code, handle)
+    rc = _unpack4(rows, cols, packed._at, packed.group, out.data_ptr(), ld, code, handle)
     if rc:
         _failed(rc)
     return out
@@ -162,6 +175,20 @@ def gemv4(x, packed: Packed4, *, out=None, out_dtype=None, stream=None):
     """x W^T for a 4-bit W and a few rows x (cam_gemv4): x is [cols] or
     [tokens, cols]; the result is [rows] or [tokens, rows] in x's dtype (or
     `out_dtype`, or into `out`). For serving: no gradient."""
+    if out is None and out_dtype is None and stream is None:
+        # the call of a decoding step, with every check of the general one below
+        code, shape, device = _CODES.get(x.dtype), x.shape, packed._device
+        if code is not None and len(shape) == 2 and x.get_device() == device == _current_device():
+            tokens, cols = shape
+            ld, step = x.stride()
+            if cols == packed.cols and step == 1 and ld >= cols:
+                rows = packed.rows
+                y = _empty((tokens, rows), dtype=x.dtype, device=packed._place)
+                rc = _gemv4(tokens, rows, cols, x.data_ptr(), ld, code, packed._at, packed.group,
+                            y.data_ptr(), rows, code, _current_stream(device))
+                if rc:
+                    _failed(rc)
+                return y
     if x.dim() == 1:
         if out is not None:
             gemv4(x.unsqueeze(0), packed, out=out.unsqueeze(0) if out.dim() == 1 else out,
@@ -192,8 +219,8 @@ def gemv4(x, packed: Packed4, *, out=None, out_dtype=None, stream=None):
         _same_device(device, y)
     handle = _current_stream(device) if stream is None else \
         _on_stream(stream, (x, packed.data, y))
-    rc = _L.cam_gemv4(tokens, rows, cols, x.data_ptr(), ld, code, packed._at, packed.group,
-                      y.data_ptr(), ld_y, code_y, handle)
+    rc = _gemv4(tokens, rows, cols, x.data_ptr(), ld, code, packed._at, packed.group,
+                y.data_ptr(), ld_y, code_y, handle)
     if rc:
         _failed(rc)
     return y
@@ -204,7 +231,8 @@ class TokenLogprobs:
     logp of the given tokens (None without tokens), entropy, lse, top_logp and
     top_ids ([rows, top], None for top = 0), and lse_lo, what rounding lse to
     fp32 left out (for the gradient). Unpacks in that order. The first three
-    and the last are rows of one tensor, made when they are first asked for."""
+    and the last are rows of one tensor, made when they are first asked for
+    (an allocation for each takes twice the host time where they are not all read)."""
 
     __slots__ = ("_stats", "_rows", "top_logp", "top_ids")
     _fields = ("logp", "entropy", "lse", "top_logp", "top_ids", "lse_lo")
@@ -252,39 +280,34 @@ def token_logprobs(logits, tokens=None, *, top: int = 0, stream=None) -> TokenLo
         with torch.cuda.device(device):
             return token_logprobs(logits, tokens, top=top, stream=stream)
     place = logits.device
-    # one allocation: logp, entropy, lse and lse_lo are its rows
-    stats = _empty((4, rows), dtype=_FLOAT, device=place)
-    top_logp = top_ids = at_logp = at_ids = at_token = None
+    stats = _empty((4, rows), dtype=_FLOAT, device=place)  # logp, entropy, lse, lse_lo
+    at = stats.data_ptr()
+    top_logp = top_ids = at_token = at_top = at_ids = None
+    if tokens is not None:
+        at_token = tokens.data_ptr()
     if top:
         top_logp = _empty((rows, top), dtype=_FLOAT, device=place)
         top_ids = _empty((rows, top), dtype=_INT64, device=place)
-        at_logp, at_ids = top_logp.data_ptr(), top_ids.data_ptr()
-    at = stats.data_ptr()
+        at_top, at_ids = top_logp.data_ptr(), top_ids.data_ptr()
     handle = _current_stream(device) if stream is None else \
         _on_stream(stream, (logits, tokens, stats, top_logp, top_ids))
-    if tokens is not None:
-        at_token = tokens.data_ptr()
-    rc = _L.cam_token_logprobs(rows, vocab, logits.data_ptr(), ld, code, at_token, top,
-                               None if at_token is None else at, at + 4 * rows, at + 8 * rows,
-                               at + 12 * rows, at_logp, at_ids, handle)
+    rc = _logprobs(rows, vocab, logits.data_ptr(), ld, code, at_token, top,
+                   None if at_token is None else at, at + 4 * rows, at + 8 * rows, at + 12 * rows,
+                   at_top, at_ids, handle)
     if rc:
         _failed(rc)
     return TokenLogprobs(stats, tokens is not None, top_logp, top_ids)
 
 
-def _row_values(rows: int, device: int, *tensors):
-    """The pointers of fp32 arrays with one entry per row (None stays None)."""
-    found, shape = [], (rows,)
-    for t in tensors:
-        if t is None:
-            found.append(None)
-            continue
-        if t.dtype != _FLOAT or t.shape != shape or not t.is_contiguous():
-            raise ValueError("lse, entropy and the gradients must be contiguous fp32, one per row")
-        if t.get_device() != device:
-            raise ValueError("tensors must live on one CUDA device")
-        found.append(t.data_ptr())
-    return found
+def _row_value(t, shape, device: int):
+    """The pointer of an fp32 array with one entry per row (None stays None)."""
+    if t is None:
+        return None
+    if t.dtype is not _FLOAT or t.shape != shape or not t.is_contiguous():
+        raise ValueError("lse, entropy and the gradients must be contiguous fp32, one per row")
+    if t.get_device() != device:
+        raise ValueError("tensors must live on one CUDA device")
+    return t.data_ptr()
 
 
 def token_logprobs_backward(logits, tokens, lse, entropy, grad_logp=None, grad_entropy=None, *,
@@ -304,7 +327,10 @@ def token_logprobs_backward(logits, tokens, lse, entropy, grad_logp=None, grad_e
         _check_tokens(tokens, rows)
         _same_device(device, tokens)
         at_token = tokens.data_ptr()
-    values = _row_values(rows, device, lse, lse_lo, entropy, grad_logp, grad_entropy)
+    shape = (rows,)
+    at_lse, at_lo = _row_value(lse, shape, device), _row_value(lse_lo, shape, device)
+    at_entropy = _row_value(entropy, shape, device)
+    at_g, at_h = _row_value(grad_logp, shape, device), _row_value(grad_entropy, shape, device)
     if out is None:
         out = _empty((rows, vocab), dtype=logits.dtype, device=logits.device)
         ld_out = vocab
@@ -315,8 +341,8 @@ def token_logprobs_backward(logits, tokens, lse, entropy, grad_logp=None, grad_e
         _same_device(device, out)
     handle = _current_stream(device) if stream is None else \
         _on_stream(stream, (logits, tokens, lse, lse_lo, entropy, grad_logp, grad_entropy, out))
-    rc = _L.cam_token_logprobs_backward(rows, vocab, logits.data_ptr(), ld, code, at_token, *values,
-                                        out.data_ptr(), ld_out, handle)
+    rc = _logprobs_backward(rows, vocab, logits.data_ptr(), ld, code, at_token, at_lse, at_lo,
+                            at_entropy, at_g, at_h, out.data_ptr(), ld_out, handle)
     if rc:
         _failed(rc)
     return out
