@@ -736,7 +736,7 @@ int cam_unpack4(int64_t rows, int64_t cols, const void* packed, int32_t group, v
  * elements, into y[m] of rows elements. Products are exact and sums are held
  * in binary32, whatever the types of x and y (fp32 or bf16); y is rounded
  * once. Made for the few tokens of a decoding step: the weights are read once
- * for up to 32 bf16 tokens (10 in fp32) and again for each further such set.
+ * for up to 32 bf16 tokens (16 in fp32) and again for each further such set.
  * A group's sum of q * x is formed before its scale, so |x| above about 1e35
  * may overflow where q * s * x would not. cols = 0 writes zeros.
  * Errors: CAM_E_ARG, CAM_E_CUDA.
