@@ -9,7 +9,8 @@
 // exact in bf16 and so is a bf16 x, hence every product is exact and only
 // binary32 sums round. An fp32 x is cut into three bf16 terms of 8 bits each,
 // x = x1 + x2 + x3 exactly, which take three columns and meet again in the
-// output's sum. The group's scale multiplies the group's fp32 sum. The
+// group's sum (for one or two tokens in the output's). The group's scale
+// multiplies the group's fp32 sum. The
 // weights stay in the lane that loaded them: mma.sync takes them from
 // registers, where the 4-bit words are widened (two instructions per two
 // weights), while tcgen05 wants them written to shared or tensor memory first.
@@ -185,8 +186,8 @@ __device__ __forceinline__ uint16_t round_bf16(float v) {
 
 // The forms of the kernel by columns of x: NT operands of 8 columns. bf16: up to
 // 8, 16 or 32 tokens (NT 1, 2, 4). fp32: up to 2 tokens packed in one operand
-// (NT 1), else three operands for each 8 tokens (NT 3, 6), so that a token's
-// three sums stand in one lane. Few columns take many small blocks per SM, many
+// (NT 1), else three operands for each 8 tokens (NT 3, 6) that add up in the
+// same accumulators. Few columns take many small blocks per SM, many
 // columns one large one, whose warps share its x.
 template <bool F32, int NT>
 struct GvForm {
@@ -364,19 +365,12 @@ __global__ void __launch_bounds__(GvForm<F32, NT>::kWarps * 32, GvForm<F32, NT>:
         range(blk0, begin, end);
         int tile = tile0 + begin / nb, b = begin % nb;
         bool owner = b == 0, open = false;  // the tile under way: has its first record; not finished
-        float acc[NT][4];
+        float acc[kOut][4];
         float4 v[kOut];
-        auto gather = [&]() {  // a token's three terms together, the smallest first
+        auto gather = [&]() {
 #pragma unroll
-            for (int n = 0; n < kOut; ++n) {
+            for (int n = 0; n < kOut; ++n)
                 v[n] = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
-                if constexpr (F32 && NT > 1) {
-                    v[n].x += acc[kOut + n][0] + acc[2 * kOut + n][0];
-                    v[n].y += acc[kOut + n][1] + acc[2 * kOut + n][1];
-                    v[n].z += acc[kOut + n][2] + acc[2 * kOut + n][2];
-                    v[n].w += acc[kOut + n][3] + acc[2 * kOut + n][3];
-                }
-            }
         };
         auto leave = [&]() {  // another warp's tile
             gather();
@@ -385,7 +379,7 @@ __global__ void __launch_bounds__(GvForm<F32, NT>::kWarps * 32, GvForm<F32, NT>:
             if (lane == 0) slot_tile[warp] = tile;
         };
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < kOut; ++n)
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[n][j] = 0.0f;
         for (int pos = begin; pos < end; ++pos) {
@@ -409,33 +403,43 @@ __global__ void __launch_bounds__(GvForm<F32, NT>::kWarps * 32, GvForm<F32, NT>:
                 sl[0] = *reinterpret_cast<const uint32_t*>(sp);
                 sh[0] = sl[0] >> 16;
             }
-            float part[NT][4];
+            constexpr int kSteps = GROUP / 32;  // steps of 32 columns per group
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                constexpr int kSteps = GROUP / 32;  // steps of 32 columns per group
-                const uint32_t lo = i == 0 ? wl.x : i == 1 ? wl.y : i == 2 ? wl.z : wl.w;
-                const uint32_t hi = i == 0 ? wh.x : i == 1 ? wh.y : i == 2 ? wh.z : wh.w;
-                uint32_t al[4], ah[4];
+            for (int j = 0; j < kPer; ++j) {
+                uint32_t al[kSteps][4], ah[kSteps][4];
 #pragma unroll
-                for (int p = 0; p < 4; ++p) al[p] = widen(lo, p), ah[p] = widen(hi, p);
+                for (int k = 0; k < kSteps; ++k) {
+                    const int i = j * kSteps + k;
+                    const uint32_t lo = i == 0 ? wl.x : i == 1 ? wl.y : i == 2 ? wl.z : wl.w;
+                    const uint32_t hi = i == 0 ? wh.x : i == 1 ? wh.y : i == 2 ? wh.z : wh.w;
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const uint4 x = xb[i * C * 4 + x_lane[n]];
-                    if (i % kSteps == 0) mma_first(part[n], al[0], ah[0], al[1], ah[1], x.x, x.y);
-                    else mma(part[n], al[0], ah[0], al[1], ah[1], x.x, x.y);
-                    mma(part[n], al[2], ah[2], al[3], ah[3], x.z, x.w);
+                    for (int p = 0; p < 4; ++p) al[k][p] = widen(lo, p), ah[k][p] = widen(hi, p);
                 }
-                if (i % kSteps == kSteps - 1) {
-                    const int j = i / kSteps;
-                    const float s0 = __uint_as_float((j & 1) ? sl[j >> 1] & 0xFFFF0000u : sl[j >> 1] << 16);
-                    const float s1 = __uint_as_float((j & 1) ? sh[j >> 1] & 0xFFFF0000u : sh[j >> 1] << 16);
+                // a token's three terms in one sum, over the whole group the smallest first (step
+                // by step the sum's error is three times as large at group 128; in sums of their
+                // own 32 tokens over 73,760 x 2,048 took 100 us instead of 92)
+                float part[kOut][4];
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        acc[n][0] = fmaf(s0, part[n][0], acc[n][0]);
-                        acc[n][1] = fmaf(s0, part[n][1], acc[n][1]);
-                        acc[n][2] = fmaf(s1, part[n][2], acc[n][2]);
-                        acc[n][3] = fmaf(s1, part[n][3], acc[n][3]);
-                    }
+                for (int q = NT / kOut - 1; q >= 0; --q)
+#pragma unroll
+                    for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+                        for (int n = 0; n < kOut; ++n) {
+                            const uint4 x = xb[(j * kSteps + k) * C * 4 + x_lane[q * kOut + n]];
+                            if (q == NT / kOut - 1 && k == 0)
+                                mma_first(part[n], al[k][0], ah[k][0], al[k][1], ah[k][1], x.x, x.y);
+                            else
+                                mma(part[n], al[k][0], ah[k][0], al[k][1], ah[k][1], x.x, x.y);
+                            mma(part[n], al[k][2], ah[k][2], al[k][3], ah[k][3], x.z, x.w);
+                        }
+                const float s0 = __uint_as_float((j & 1) ? sl[j >> 1] & 0xFFFF0000u : sl[j >> 1] << 16);
+                const float s1 = __uint_as_float((j & 1) ? sh[j >> 1] & 0xFFFF0000u : sh[j >> 1] << 16);
+#pragma unroll
+                for (int n = 0; n < kOut; ++n) {
+                    acc[n][0] = fmaf(s0, part[n][0], acc[n][0]);
+                    acc[n][1] = fmaf(s0, part[n][1], acc[n][1]);
+                    acc[n][2] = fmaf(s1, part[n][2], acc[n][2]);
+                    acc[n][3] = fmaf(s1, part[n][3], acc[n][3]);
                 }
             }
             open = true;
@@ -447,7 +451,7 @@ __global__ void __launch_bounds__(GvForm<F32, NT>::kWarps * 32, GvForm<F32, NT>:
                     leave();
                 }
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                for (int n = 0; n < kOut; ++n)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) acc[n][j] = 0.0f;
                 b = 0, ++tile;
