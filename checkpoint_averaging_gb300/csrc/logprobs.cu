@@ -135,6 +135,9 @@ struct Vec16<float> {
     __device__ __forceinline__ float get(int j) const {
         return __uint_as_float(j == 0 ? u.x : j == 1 ? u.y : j == 2 ? u.z : u.w);
     }
+    static __device__ __forceinline__ uint4 nothing() {  // -inf
+        return make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u);
+    }
     __device__ __forceinline__ float largest() const {  // NaN apart
         return fmaxf(fmaxf(get(0), get(1)), fmaxf(get(2), get(3)));
     }
@@ -165,6 +168,9 @@ struct Vec16<uint16_t> {
     __device__ __forceinline__ float get(int j) const {
         const uint32_t w = j < 2 ? u.x : j < 4 ? u.y : j < 6 ? u.z : u.w;
         return __uint_as_float((j & 1) ? w & 0xFFFF0000u : w << 16);
+    }
+    static __device__ __forceinline__ uint4 nothing() {
+        return make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);
     }
     __device__ __forceinline__ float largest() const {
         const __nv_bfloat162 m =
@@ -281,6 +287,49 @@ struct Share {
     float r;  // sum of exp(x - m) over the others
     float t;  // sum of exp(x - m) (x - m)
 };
+
+// What a row's share says of the row. (No distribution: c and r are 0; a NaN or
+// +inf: r is NaN.)
+struct RowResult {
+    Share s;
+    float log_s;
+    bool dead;
+    __device__ __forceinline__ explicit RowResult(const Share& share) : s(share) {
+        if (s.m == kInf) s.r = NAN;
+        dead = s.m == -kInf && s.r == 0.0f;
+        log_s = dead ? 0.0f : log1pf((s.c - 1.0f) + s.r);
+    }
+    __device__ __forceinline__ float logp_of(float v) const {
+        return dead ? -kInf : (v - s.m) - log_s;
+    }
+    __device__ __forceinline__ void write(const LogprobArgs& a, int64_t row, int64_t token,
+                                          float x_token) const {
+        const float lse = dead ? -kInf : s.m + log_s;
+        if (a.lse) a.lse[row] = lse;
+        if (a.lse_lo) {  // what the sum's rounding left out, exactly (the order of the two is free)
+            const float b = __fsub_rn(lse, s.m);
+            const float lo = __fadd_rn(__fsub_rn(s.m, __fsub_rn(lse, b)), __fsub_rn(log_s, b));
+            a.lse_lo[row] = isfinite(lse) ? lo : 0.0f;
+        }
+        if (a.entropy) a.entropy[row] = dead ? 0.0f : log_s - __fdividef(s.t, s.c + s.r);
+        if (a.logp)
+            a.logp[row] = token >= a.vocab ? NAN : token >= 0 ? logp_of(x_token) : 0.0f;
+    }
+    __device__ __forceinline__ void write_top(const LogprobArgs& a, int64_t row, int place,
+                                              Key key) const {
+        if (a.top_ids) a.top_ids[row * a.top + place] = key_id(key);
+        if (a.top_logp) a.top_logp[row * a.top + place] = logp_of(key_logit(key));
+    }
+};
+
+// How many of a descending list's n <= 32 keys are above a key.
+__device__ __forceinline__ int count_above(const Key* list, int n, Key key) {
+    int at = 0;
+#pragma unroll
+    for (int step = 32; step > 0; step /= 2)
+        if (at + step <= n && list[at + step - 1] > key) at += step;
+    return at;
+}
 
 // What a streaming warp hands over of its vectors of a row. Sums are of
 // 2^(x log2(e) - m log2(e)) and of that times its exponent; those of the lane
@@ -650,35 +699,19 @@ __device__ __noinline__ void select_rows(const LogprobArgs& a, LogprobShared& sh
             }
             s = all;
         }
-        if (s.m == kInf) s.r = NAN;
-        // no distribution: c and r are 0; a NaN or +inf: r is NaN
-        const bool dead = s.m == -kInf && s.r == 0.0f;
-        const float log_s = dead ? 0.0f : log1pf((s.c - 1.0f) + s.r);
-        auto logp_of = [&](float v) { return dead ? -kInf : (v - s.m) - log_s; };
-        if (lane == 0) {
-            const float lse = dead ? -kInf : s.m + log_s;
-            if (a.lse) a.lse[r_at] = lse;
-            if (a.lse_lo) {  // what the sum's rounding left out, exactly (the order of the two is free)
-                const float b = __fsub_rn(lse, s.m);
-                const float lo = __fadd_rn(__fsub_rn(s.m, __fsub_rn(lse, b)), __fsub_rn(log_s, b));
-                a.lse_lo[r_at] = isfinite(lse) ? lo : 0.0f;
-            }
-            if (a.entropy) a.entropy[r_at] = dead ? 0.0f : log_s - __fdividef(s.t, s.c + s.r);
-            if (a.logp)
-                a.logp[r_at] = token >= a.vocab ? NAN : token >= 0 ? logp_of(x_token) : 0.0f;
-        }
+        const RowResult result(s);
+        if (lane == 0) result.write(a, r_at, token, x_token);
         for (int i = lane; i < a.cluster * a.top; i += 32) {
             const Key key = clustered ? sh.all_best[i / a.top][i % a.top] : best[i];
             if (key == 0) continue;
             int place = i;
-            if (clustered) {
+            if (clustered) {  // each block's list is in order
                 place = 0;
-                for (int j = 0; j < a.cluster; ++j)
-                    for (int q = 0; q < a.top; ++q) place += sh.all_best[j][q] > key;
-                if (place >= a.top) continue;
+#pragma unroll
+                for (int j = 0; j < kLpMaxCluster; ++j)
+                    if (j < a.cluster) place += count_above(sh.all_best[j], a.top, key);
             }
-            if (a.top_ids) a.top_ids[r_at * a.top + place] = key_id(key);
-            if (a.top_logp) a.top_logp[r_at * a.top + place] = logp_of(key_logit(key));
+            if (place < a.top) result.write_top(a, r_at, place, key);
         }
         __syncwarp();
     }
@@ -860,6 +893,235 @@ __global__ void __launch_bounds__(kLpMaxBlock, 2)
     select_rows<T>(a, sh, warp - n_warps, rank, first, step, n_rows);
 }
 
+// ---- rows that fit the registers of a few warps ----------------------------------
+
+constexpr int kLhMaxWarps = 8;  // of a block, which has one row
+constexpr int kLhMost = 16;     // vectors per thread
+constexpr int kLhFill = 16;     // warps per SM that rows are cut for (8 to 32 measure alike)
+constexpr int kLhList = 256;    // candidates a row may have, and vectors with one
+
+struct HeldShared {
+    float thread_max[32 * kLhMaxWarps];
+    float warp_max[kLhMaxWarps];
+    float c[kLhMaxWarps], r[kLhMaxWarps], t[kLhMaxWarps];
+    Key key[kLhMaxWarps];
+    int n, n_vectors;
+    Key list[kLhList];
+    uint16_t vectors[kLhList];
+};
+
+// NV vectors of a row per thread, loaded at once and kept: the largest logit,
+// then the sums relative to it, then the few candidates, which are read once
+// more. Other blocks of the SM load meanwhile; what bounds many rows are the
+// instructions (8,192 x 4,000 bf16 22 us, 3.1 TB/s; fp32 27 us, 4.9 TB/s).
+template <typename T, int NV>
+__global__ void __launch_bounds__(32 * kLhMaxWarps, NV <= 4 ? 4 : NV <= 8 ? 3 : 2)
+    token_logprobs_held(const __grid_constant__ LogprobArgs a) {
+    constexpr int kN = Vec16<T>::kN;
+    constexpr uint32_t kAll = 0xFFFFFFFFu;
+    __shared__ HeldShared sh;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int threads = blockDim.x, warps = threads >> 5;
+    const int64_t r_at = blockIdx.x;
+    const RowPlan<T> row(static_cast<const T*>(a.logits) + r_at * a.stride, a.vocab);
+    const int singles = warp == 0 ? row.head + row.tail : 0;
+    auto meet = [&]() {
+        if (warps == 1) __syncwarp();
+        else __syncthreads();
+    };
+
+    const int64_t token = a.logp ? a.tokens[r_at] : -1;
+    Vec16<T> v[NV];  // past the end: -inf
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int w = i * threads + tid;
+        v[i].u = Vec16<T>::nothing();
+        if (w < row.n_vec) v[i] = load16(row.x + row.head + w * kN);
+    }
+    const int single_id = lane < singles ? row.single_id(lane, a.vocab) : 0;
+    const float single = lane < singles ? widen1(row.x[single_id]) : -kInf;
+    const float x_token = token >= 0 && token < a.vocab ? widen1(row.x[token]) : 0.0f;
+
+    float m = fmaxf(single, -kInf);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) m = fmaxf(m, v[i].largest());
+    m = fmaxf(m, -kInf);
+    float M = warp_max(m);
+    if (warps > 1) {
+        sh.thread_max[tid] = m;
+        if (lane == 0) sh.warp_max[warp] = M;
+    }
+    if (tid == 0) sh.n = sh.n_vectors = 0;
+    meet();
+    if (warps > 1) {
+        M = sh.warp_max[0];
+        for (int w = 1; w < warps; ++w) M = fmaxf(M, sh.warp_max[w]);
+    }
+
+    // the sums of all warps, in their order
+    auto join = [&](Share& s) {
+        s.c = warp_sum(s.c), s.r = warp_sum(s.r), s.t = warp_sum(s.t);
+        if (warps == 1) {
+            __syncwarp();
+            return;
+        }
+        if (lane == 0) sh.c[warp] = s.c, sh.r[warp] = s.r, sh.t[warp] = s.t;
+        __syncthreads();
+        s.c = s.r = s.t = 0.0f;
+        for (int w = 0; w < warps; ++w) s.c += sh.c[w], s.r += sh.r[w], s.t += sh.t[w];
+    };
+    Share s{M, 0.0f, 0.0f, 0.0f};
+    const float from = M == -kInf ? 0.0f : M;
+    {
+        const Pair less = pair(-from, -from), log2e = pair(kLog2e, kLog2e);
+        Pair r2 = pair(0.0f, 0.0f), t2 = r2;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            // a mask held finite: its exponent times its term is then 0 and not NaN
+            const Vec16<T> u = v[i].held_finite();
+#pragma unroll
+            for (int j = 0; j < kN; j += 2) {
+                const Pair d = add2(pair(u.get(j), u.get(j + 1)), less);
+                float y0, y1;
+                split(mul2(d, log2e), y0, y1);
+                const Pair e = pair(ex2(y0), ex2(y1));
+                r2 = add2(r2, e);
+                t2 = fma2(e, d, t2);
+            }
+        }
+        const float d = max_nan(single - from, -200.0f), e = lane < singles ? ex2(d * kLog2e) : 0.0f;
+        float lo, hi;
+        split(r2, lo, hi);
+        s.r = lo + hi + e;
+        split(t2, lo, hi);
+        s.t = lo + hi + e * d;
+    }
+
+    // a bound that at least `top` logits reach, and the vectors with one that does
+    float bound = M;
+    if (a.top > 1) {
+        float set = m;
+        if (warps > 1) {
+            set = sh.thread_max[lane];
+            for (int w = 1; w < warps; ++w) set = fmaxf(set, sh.thread_max[32 * w + lane]);
+        }
+        bound = nth_of_warp(set, a.top);
+    }
+    const bool list = a.top > 0 && bound > -kInf;
+    auto put = [&](float x, int id) {
+        const int at = atomicAdd(&sh.n, 1);
+        if (at < kLhList) sh.list[at] = make_key(x, static_cast<uint32_t>(id));
+    };
+    if (list && m >= bound) {
+        if (single >= bound) put(single, single_id);
+        uint32_t hits = 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) hits |= v[i].largest() >= bound ? 1u << i : 0u;
+        int at = atomicAdd(&sh.n_vectors, __popc(hits));
+        for (; hits != 0; hits &= hits - 1, ++at)
+            if (at < kLhList)
+                sh.vectors[at] = static_cast<uint16_t>((__ffs(hits) - 1) * threads + tid);
+    }
+    join(s);
+    const int n_vectors = sh.n_vectors;
+    if (list && n_vectors <= kLhList) {  // a thread to a logit (from the caches)
+        for (int i = tid; i < n_vectors * kN; i += threads) {
+            const int id = row.head + sh.vectors[i / kN] * kN + i % kN;
+            const float x = widen1(row.x[id]);
+            if (x >= bound) put(x, id);
+        }
+    }
+
+    bool bad = false;
+    if (s.r != s.r || fabsf(M) >= kHuge) {
+        // a NaN, no logit, or logits too large for differences to stay finite
+        s = Share{M, 0.0f, 0.0f, 0.0f};
+        auto add = [&](float x) {
+            if (x != x || x == kInf) s.r = NAN;
+            if (x == M) {
+                if (M != -kInf) s.c += 1.0f;
+            } else {
+                const float d = max_nan(x - from, -200.0f), e = ex2(d * kLog2e);
+                s.r += e;
+                s.t += e * d;
+            }
+        };
+        if (lane < singles) add(single);
+#pragma unroll 1
+        for (int i = 0; i < NV; ++i) {
+            const int w = i * threads + tid;
+            if (w >= row.n_vec) break;
+            const Vec16<T> u = load16(row.x + row.head + w * kN);
+#pragma unroll
+            for (int j = 0; j < kN; ++j) add(u.get(j));
+        }
+        meet();  // (the sums before have been read)
+        join(s);
+        bad = s.r != s.r;
+    } else if (s.r < 1.5f) {
+        // One logit has most of the probability, and what the others add to it would drown in
+        // the sum: again without it.
+        s = Share{M, 0.0f, 0.0f, 0.0f};
+        auto add = [&](float x) {
+            if (x == M) return;
+            const float d = fmaxf(x - M, -200.0f), e = ex2(d * kLog2e);
+            s.r += e;
+            s.t += e * d;
+        };
+        if (lane < singles) add(single);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < kN; ++j) add(v[i].get(j));
+        meet();
+        join(s);
+        s.c = 1.0f;
+    }
+    const RowResult result(s);
+    if (tid == 0) result.write(a, r_at, token, x_token);
+    if (a.top == 0) return;
+    meet();
+    const int n = sh.n;
+    if (!bad && list && n_vectors <= kLhList && n <= kLhList) {
+        // a candidate's place is the number before it
+        for (int i = tid; i < n; i += threads) {
+            const Key key = sh.list[i];
+            int place = 0;
+#pragma unroll 4
+            for (int k = 0; k < n; ++k) place += sh.list[k] > key;
+            if (place < a.top) result.write_top(a, r_at, place, key);
+        }
+        return;
+    }
+    // a NaN, masks, or more candidates than the list holds: one maximum at a time
+    Key last = ~0ull;
+    for (int p = 0; p < a.top; ++p) {
+        Key key = 0;
+        auto look = [&](float x, int id) {
+            const Key u = make_key(x, static_cast<uint32_t>(id));
+            if (u < last) key = max(key, u);
+        };
+        if (lane < singles) look(single, single_id);
+#pragma unroll 1
+        for (int i = 0; i < NV; ++i) {
+            const int w = i * threads + tid;
+            if (w >= row.n_vec) break;
+            const Vec16<T> u = load16(row.x + row.head + w * kN);
+#pragma unroll
+            for (int j = 0; j < kN; ++j) look(u.get(j), row.head + w * kN + j);
+        }
+        key = warp_max_key(key);
+        if (warps > 1) {
+            if (lane == 0) sh.key[warp] = key;
+            __syncthreads();
+            for (int w = 0; w < warps; ++w) key = max(key, sh.key[w]);
+            __syncthreads();
+        }
+        last = key;
+        if (tid == 0) result.write_top(a, r_at, p, key);
+    }
+}
+
 // ---- backward ----------------------------------------------------------------
 
 constexpr int kLbThreads = 256;
@@ -1029,6 +1291,13 @@ __global__ void __launch_bounds__(kLbThreads)
 }
 
 template <typename T>
+const void* held_kernel(int nv) {
+    return nv <= 4   ? reinterpret_cast<const void*>(token_logprobs_held<T, 4>)
+           : nv <= 8 ? reinterpret_cast<const void*>(token_logprobs_held<T, 8>)
+                     : reinterpret_cast<const void*>(token_logprobs_held<T, kLhMost>);
+}
+
+template <typename T>
 const void* backward_kernel(int team) {
     return team == 32    ? reinterpret_cast<const void*>(token_logprobs_backward<T, 32>)
            : team == 64  ? reinterpret_cast<const void*>(token_logprobs_backward<T, 64>)
@@ -1079,9 +1348,31 @@ CAM_API int cam_token_logprobs(int64_t rows, int64_t vocab, const void* logits, 
     LogprobArgs a{logits, stride, tokens, logp, entropy, lse, lse_lo, top_logp, top_ids,
                   static_cast<int32_t>(rows), static_cast<int32_t>(vocab),
                   top_logp || top_ids ? top : 0, 1, 0, 0, 0};
+    // Rows that fit the registers of a block are held there. Up to 2,048 vectors that is faster
+    // for any number of rows, in us against the streaming form's, without alternatives and with
+    // 20: 8,192 x 2,000 fp32 17 and 29 (29 and 66), 8,192 x 16,000 bf16 57 and 84 (70 and 117).
+    // Up to 4,096 it is where rows are few: 512 x 32,000 bf16 13 and 17 (14 and 23); with many
+    // the two are alike: 8,192 x 16,000 fp32 93 to 131 (98 to 133).
+    const int64_t n_vec = std::max<int64_t>(1, vocab / (dtype == CAM_F32 ? 4 : 8));
+    const int64_t held = 32 * kLhMaxWarps * kLhMost;
+    if (n_vec <= held / 2 || (n_vec <= held && rows <= int64_t(sms) * 8)) {
+        // as few warps as hold the row where rows are many, as many as still have four
+        // vectors per thread where they are few
+        int64_t warps = (n_vec + 32 * kLhMost - 1) / (32 * kLhMost);
+        const int64_t most = std::min<int64_t>(kLhMaxWarps, (n_vec + 32 * 4 - 1) / (32 * 4));
+        while (warps < most && rows * (warps + 1) <= int64_t(sms) * kLhFill) ++warps;
+        const int nv = static_cast<int>((n_vec + 32 * warps - 1) / (32 * warps));
+        void* held_args[] = {&a};
+        ce = cudaLaunchKernel(dtype == CAM_F32 ? held_kernel<float>(nv) : held_kernel<uint16_t>(nv),
+                              dim3(static_cast<unsigned>(rows)),
+                              dim3(static_cast<unsigned>(32 * warps)), held_args, 0,
+                              static_cast<cudaStream_t>(stream));
+        if (ce != cudaSuccess)
+            return record_error(CAM_E_CUDA, "%s: launch: %s", fn, cudaGetErrorString(ce));
+        return CAM_OK;
+    }
     // Streaming threads per block: about 16 vectors each. Where rows are few, a cluster of
     // blocks shares each of them.
-    const int64_t n_vec = std::max<int64_t>(1, vocab / (dtype == CAM_F32 ? 4 : 8));
     auto threads_for = [&](int64_t share) {
         return static_cast<int32_t>(
             std::min<int64_t>(kLpMaxStream, std::max<int64_t>(64, (share / 16 + 31) / 32 * 32)));
