@@ -918,7 +918,6 @@ template <typename T, int NV>
 __global__ void __launch_bounds__(32 * kLhMaxWarps, NV <= 4 ? 4 : NV <= 8 ? 3 : 2)
     token_logprobs_held(const __grid_constant__ LogprobArgs a) {
     constexpr int kN = Vec16<T>::kN;
-    constexpr uint32_t kAll = 0xFFFFFFFFu;
     __shared__ HeldShared sh;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int threads = blockDim.x, warps = threads >> 5;

@@ -4,11 +4,12 @@
 //
 // Both are streaming, HBM-bound: 4 B (fp32) or 2 B (bf16) per weight on one
 // side, 1/2 + 2 / group B on the other. One warp takes one tile of 16 rows x
-// 128 columns, its loads in flight before their first use. Measured with
-// 20,000 rows, group 64: 6,160 fp32 columns 89 us to pack and 88 us to unpack
-// (6.3 TB/s), bf16 68 us (4.6 TB/s: the scales' and roundings' instructions) and
-// 50 us (6.3 TB/s); rows without alignment (6,159 columns) 103 and 123 us in
-// fp32, 168 and 125 us in bf16.
+// 128 columns, its loads in flight before their first use; four blocks of
+// eight warps per SM (with two or three the bf16 pass takes 82 and 68 us, not
+// 64). Measured with 20,000 rows, group 32: 6,160 fp32 columns 89 us to pack
+// and 87 us to unpack (6.3 and 6.4 TB/s), bf16 64 us (4.9 TB/s: the scales' and
+// roundings' instructions) and 50 us (6.4 TB/s); rows without alignment (6,159
+// columns) 97 and 94 us in fp32, 114 and 84 us in bf16.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -27,11 +28,20 @@ constexpr int kPkThreads = 256;
 __device__ __forceinline__ float widen(uint32_t bits) { return __uint_as_float(bits << 16); }
 __device__ __forceinline__ float load1(const uint16_t* p) { return widen(__ldg(p)); }
 
+__device__ __forceinline__ uint4 load_word(const uint16_t* p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
 // Eight columns of a row as loaded. `fetch` reads them from a row aligned to 16
 // bytes (`eight`: to eight elements), columns past the end as 0. Rows without
 // that alignment, as every odd number of columns gives, are read four bytes to
 // a lane, so that a load is still one run of memory (`gather`, of the row's 128
-// columns), and turned in shared memory (`put`, then `take`).
+// columns), and turned in shared memory (`put`, then `take`). (That alone takes
+// 168 us for the 20,000 x 6,159 bf16; see pack4 for tiles inside the rows.)
 template <typename T>
 struct Eight;
 
@@ -141,6 +151,25 @@ struct Eight<uint16_t> {
     }
 };
 
+// The 16 bytes that start `by` (0, 2, .. 14) bytes into a and b.
+__device__ __forceinline__ uint4 cut(const uint4& a, const uint4& b, int by) {
+    const bool two = by & 8, one = by & 4;
+    const uint32_t c0 = two ? a.z : a.x, c1 = two ? a.w : a.y, c2 = two ? b.x : a.z;
+    const uint32_t c3 = two ? b.y : a.w, c4 = two ? b.z : b.x, c5 = two ? b.w : b.y;
+    const uint32_t d0 = one ? c1 : c0, d1 = one ? c2 : c1, d2 = one ? c3 : c2;
+    const uint32_t d3 = one ? c4 : c3, d4 = one ? c5 : c4;
+    const int half = 8 * (by & 2);
+    return make_uint4(__funnelshift_r(d0, d1, half), __funnelshift_r(d1, d2, half),
+                      __funnelshift_r(d2, d3, half), __funnelshift_r(d3, d4, half));
+}
+
+// A 16-byte word of lane `from` of each W lanes.
+template <int W>
+__device__ __forceinline__ uint4 word_from(const uint4& v, int from) {
+    return make_uint4(__shfl_sync(0xFFFFFFFFu, v.x, from, W), __shfl_sync(0xFFFFFFFFu, v.y, from, W),
+                      __shfl_sync(0xFFFFFFFFu, v.z, from, W), __shfl_sync(0xFFFFFFFFu, v.w, from, W));
+}
+
 // big / 7 rounded to nearest: the product with 1/7 and one correction by the
 // remainder, which an fma gives exactly (Markstein's step); tiny dividends, whose
 // remainder may not be exact, divide.
@@ -198,12 +227,12 @@ __device__ __forceinline__ void store16(uint16_t* p, int n, const float (&v)[8])
 // high bits add up to, are the word. |w| (1 / s) is at most 7.06, so q never
 // needs holding to [-7, 7].
 template <typename T, int GROUP, bool ALIGNED>
-__global__ void __launch_bounds__(kPkThreads)
+__global__ void __launch_bounds__(kPkThreads, 4)
     pack4(int64_t rows, int64_t cols, const T* __restrict__ w, int64_t stride, bool eight,
           uint8_t* __restrict__ packed, int64_t n_tiles, int32_t tiles_across) {
     constexpr int kPer = kP4Cols / GROUP;
     constexpr float kRound = 12582912.0f + 8.0f;
-    constexpr int kBatch = Eight<T>::kBatch;
+    constexpr int kBatch = ALIGNED ? Eight<T>::kBatch : 4;
     constexpr int kTurn = 128 / (4 / sizeof(T)) + 4;  // words of a row, and one more
     __shared__ __align__(16) uint32_t turn[ALIGNED ? 1 : kPkThreads / 32][8][ALIGNED ? 4 : kTurn];
     const int lane = threadIdx.x & 31, run = lane & 15, odd = lane >> 4, warp = threadIdx.x >> 5;
@@ -228,22 +257,53 @@ __global__ void __launch_bounds__(kPkThreads)
                 const int64_t base = tile / tiles_across * kP4Rows;
                 const int64_t col0 = tile % tiles_across * kP4Cols;
                 const int in_cols = static_cast<int>(min(int64_t(kP4Cols), cols - col0));
+                bool done = false;
+                if constexpr (sizeof(T) == 2) {
+                    // Tiles inside the rows: the 17 aligned words that hold a row's 16 are read whole, and
+                    // each lane cuts its eight columns from its word and the next lane's.
+                    done = col0 >= 8 && col0 + kP4Cols + 8 <= cols;
+                    if (done) {
+                        uint4 own[kBatch], end[kBatch];
 #pragma unroll
-                for (int q = 0; q < kBatch / 4; ++q) {  // eight rows at a time
-                    typename Eight<T>::Row got[8];
-                    const int64_t first = base + 2 * b * kBatch + 8 * q;
+                        for (int r = 0; r < kBatch; ++r) {
+                            const int64_t row = row0 + 2 * (b * kBatch + r);
+                            const T* at = w + row * stride + col0;
+                            at -= reinterpret_cast<uintptr_t>(at) / 2 % 8;
+                            own[r] = end[r] = make_uint4(0u, 0u, 0u, 0u);
+                            if (row < rows) {
+                                own[r] = load_word(at + 8 * run);
+                                if (run == 15) end[r] = load_word(at + kP4Cols);
+                            }
+                        }
 #pragma unroll
-                    for (int r = 0; r < 8; ++r)
-                        Eight<T>::gather(got[r], w + (first + r) * stride + col0,
-                                         first + r < rows ? in_cols : 0, lane);
-                    __syncwarp();
+                        for (int r = 0; r < kBatch; ++r) {
+                            const T* at = w + (row0 + 2 * (b * kBatch + r)) * stride + col0;
+                            uint4 next = word_from<16>(own[r], (run + 1) & 15);
+                            if (run == 15) next = end[r];
+                            const uint4 c =
+                                cut(own[r], next, static_cast<int>(reinterpret_cast<uintptr_t>(at) & 15));
+                            v[r].u[0] = c.x, v[r].u[1] = c.y, v[r].u[2] = c.z, v[r].u[3] = c.w;
+                        }
+                    }
+                }
+                if (!done) {
 #pragma unroll
-                    for (int r = 0; r < 8; ++r) Eight<T>::put(got[r], turn[warp][r], lane);
-                    __syncwarp();
+                    for (int q = 0; q < kBatch / 4; ++q) {  // eight rows at a time
+                        typename Eight<T>::Row got[8];
+                        const int64_t first = base + 2 * b * kBatch + 8 * q;
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        v[4 * q + r].take(turn[warp][2 * r + odd], run,
-                                          w + (first + 2 * r + odd) * stride + col0);
+                        for (int r = 0; r < 8; ++r)
+                            Eight<T>::gather(got[r], w + (first + r) * stride + col0,
+                                             first + r < rows ? in_cols : 0, lane);
+                        __syncwarp();
+#pragma unroll
+                        for (int r = 0; r < 8; ++r) Eight<T>::put(got[r], turn[warp][r], lane);
+                        __syncwarp();
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            v[4 * q + r].take(turn[warp][2 * r + odd], run,
+                                              w + (first + 2 * r + odd) * stride + col0);
+                    }
                 }
             }
 #pragma unroll
@@ -289,11 +349,11 @@ __device__ __forceinline__ float value(uint32_t word, int column, float s) {
     return __fmul_rn(__fsub_rn(__uint_as_float(u), 8388608.0f + 8.0f), s);
 }
 
-// One warp takes one tile. Aligned rows are written 16 bytes to a lane, others
-// an element (fp32) or an aligned pair of them (bf16) to a lane, so that a store
-// is still one run of memory.
+// One warp takes one tile. Rows are written 16 bytes to a lane, of tiles at the
+// right edge without alignment an element (fp32) or an aligned pair of them
+// (bf16) to a lane, so that a store is still one run of memory.
 template <typename T, int GROUP, bool ALIGNED>
-__global__ void __launch_bounds__(kPkThreads)
+__global__ void __launch_bounds__(kPkThreads, ALIGNED ? 4 : 5)
     unpack4(int64_t rows, int64_t cols, const uint8_t* __restrict__ packed, T* __restrict__ values,
             int64_t stride, int64_t n_tiles, int32_t tiles_across) {
     constexpr int kPer = kP4Cols / GROUP;
@@ -333,6 +393,64 @@ __global__ void __launch_bounds__(kPkThreads)
 #pragma unroll
                 for (int j = 0; j < kC; ++j) v[j] = value(word[r], (col & 7) + j, s[r]);
                 store16(out + row * stride + col, in_cols - col, v);
+            }
+        } else if (in_cols == kP4Cols) {
+            // Whole rows of 128 columns: a lane has the columns of a 16-byte word and takes what
+            // it lacks of an aligned one from the lane before. The first lane's word is the ends
+            // of two: `a` columns that are the tile's last and kC - a that are its first.
+            constexpr int kLanes = 128 / kC;
+            const int run = lane % kLanes, sub = lane / kLanes;
+#pragma unroll
+            for (int r0 = 0; r0 < kP4Rows; r0 += 8 * kRows) {
+                uint32_t word[8];
+                float s[8];
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {
+                    word[r] = word_of(r0 + kRows * r + sub, kC * run);
+                    s[r] = scale_of(r0 + kRows * r + sub, kC * run);
+                }
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {
+                    const int row = r0 + kRows * r + sub;
+                    uint4 own;
+                    if constexpr (sizeof(T) == 4) {
+                        const uint32_t half = (run & 1) ? word[r] >> 8 : word[r];
+                        own = make_uint4(__float_as_uint(value(half, 0, s[r])),
+                                         __float_as_uint(value(half, 1, s[r])),
+                                         __float_as_uint(value(half, 2, s[r])),
+                                         __float_as_uint(value(half, 3, s[r])));
+                    } else {
+                        uint32_t u[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            u[j] = to_bf16x2(value(word[r], 2 * j, s[r]),
+                                             value(word[r], 2 * j + 1, s[r]));
+                        own = make_uint4(u[0], u[1], u[2], u[3]);
+                    }
+                    T* at = out + row * stride;
+                    const int a = static_cast<int>(reinterpret_cast<uintptr_t>(at) / sizeof(T) % kC);
+                    uint4 before = word_from<kLanes>(own, (run + kLanes - 1) % kLanes);
+                    if (a == 0) before = own;
+                    const uint4 c = cut(before, own, (16 - static_cast<int>(sizeof(T)) * a) & 15);
+                    if (row >= in_rows) continue;
+                    T* to = at - a + kC * run;
+                    if (run > 0 || a == 0) {
+                        __stcs(reinterpret_cast<uint4*>(to), c);
+                        continue;
+                    }
+                    const uint32_t part[4] = {c.x, c.y, c.z, c.w};
+                    constexpr int kE = 4 / sizeof(T);  // columns of a part
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (sizeof(T) == 2 && kE * k + 1 == a) {
+                            to[kP4Cols + kE * k] = static_cast<T>(part[k] & 0xFFFFu);
+                            to[kE * k + 1] = static_cast<T>(part[k] >> 16);
+                        } else {
+                            *reinterpret_cast<uint32_t*>(to + kE * k + (kE * k < a ? kP4Cols : 0)) =
+                                part[k];
+                        }
+                    }
+                }
             }
         } else if constexpr (sizeof(T) == 4) {
 #pragma unroll 4

@@ -111,6 +111,41 @@ def test_log_probabilities(rows, vocab, top, dtype):
         assert u is None or torch.equal(u, v)  # the same bits again
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows,vocab,top", [
+    (3000, 1001, 20), (2700, 4003, 5), (1300, 9001, 32), (1300, 16385, 1), (700, 33001, 10)])
+def test_many_rows_of_every_kind(rows, vocab, top, dtype):
+    # rows enough that a block takes several, or that each is held by as few threads as can
+    x, tokens = logits(rows, vocab, vocab, dtype)
+    k = torch.arange(rows, device=DEV) % 16
+    x[k == 1, vocab // 2] = 60.0                 # confident
+    x[k == 2, vocab - 1] = 90.0
+    x[k == 3, 1:] = -INF                         # one token left
+    x[k == 4] = -INF
+    x[k == 5, vocab // 3] = math.nan
+    x[k == 6, 0] = INF
+    x[k == 7] = 1.25                             # all equal
+    x[k == 8] = torch.floor(x[k == 8])           # many equal
+    x[k == 9, ::3] = torch.finfo(dtype).min
+    x[k == 10] *= 1e37
+    x[k == 11] = torch.finfo(dtype).min
+    x[k == 12, 40:] = -INF
+    tokens[k == 13] = -1
+    tokens[k == 14] = vocab
+    r = B.token_logprobs(x, tokens, top=top)
+    at = torch.cat([torch.arange(48), torch.arange(48, rows, 61), torch.arange(rows - 16, rows)])
+    mine, H, lse, best, ids = definition(x[at.to(DEV)], tokens[at.to(DEV)], top)
+    finite = x[at.to(DEV)].float().cpu().masked_fill(~torch.isfinite(x[at.to(DEV)].float().cpu()), 0.0)
+    L = torch.maximum(finite.abs().amax(1).double(), lse.abs().nan_to_num(0.0, 0.0, 0.0))
+    base = 2e-5 + 2.0 ** -22 * L
+    got = [v.cpu()[at] for v in (r.logp, r.entropy, r.lse, r.top_logp, r.top_ids)]
+    close(got[0], mine, base)
+    close(got[1], H, base + 2e-5 * H.nan_to_num(0.0))
+    close(got[2], lse, base)
+    assert torch.equal(got[4], ids)
+    close(got[3], best, base[:, None])
+
+
 def test_without_tokens_and_with_strides():
     x, tokens = logits(6, 5000, 1)
     check(x, None, 4)

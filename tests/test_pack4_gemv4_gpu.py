@@ -113,6 +113,24 @@ def test_strided_and_unaligned_matrices(dtype):
         assert int((out == 9.0).sum()) == out.numel() - rows * cols  # nothing else written
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("cols,ld", [(519, 519), (520, 523), (392, 400), (647, 649)])
+def test_every_alignment_of_a_row(cols, ld, group, dtype):
+    rows = 37
+    flat = matrix(1, rows * ld + 9, cols, dtype).to(DEV)[0]
+    for at in range(9):
+        w = flat[at:at + rows * ld].as_strided((rows, cols), (ld, 1))
+        q, s = form(w.float().cpu().numpy(), group)
+        pk = B.pack4(w, group)
+        assert torch.equal(pk.data, B.pack4(w.float(), group).data)
+        out = torch.full((rows * ld + at,), 9.0, dtype=dtype, device=DEV)
+        view = out[at:].as_strided((rows, cols), (ld, 1))
+        B.unpack4(pk, out=view)
+        assert torch.equal(view.cpu(), torch.from_numpy(values(q, s, cols)).to(dtype))
+        assert int((out == 9.0).sum()) == out.numel() - rows * cols  # nothing else written
+
+
 def test_zero_tiny_huge_and_broken_groups():
     w = torch.zeros(8, 128)
     w[1, 5] = 1e-45          # the scale underflows: the group stands for 0
