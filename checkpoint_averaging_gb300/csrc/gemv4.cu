@@ -39,6 +39,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "cam_internal.h"
 #include "op_launch.h"
@@ -129,53 +130,56 @@ __device__ __forceinline__ void terms(float x, uint32_t (&t)[3]) {
 // ((slab-local record * 4 + i) * C + column) * 4 + t, elements 32 i + 8 t .. + 7 of
 // the record. An fp32 x has three columns for a token, n_tok apart. Elements
 // past the end are 0.
-template <bool F32>
+template <bool F32, int kAhead>
 __device__ __forceinline__ void stage_x(const GemvArgs& a, uint4* xs, int m0, int n_tok, int C,
                                         int blk0, int n_my) {
-    const int runs = n_my * 16;
-    for (int idx = threadIdx.x; idx < runs * n_tok; idx += blockDim.x) {
-        const int m = idx / runs, run = idx - m * runs;  // run = (record, i, t)
-        const int k = blk0 * kP4Cols + run * 8;
-        const int left = min(8, a.cols - k);
-        const int64_t at = int64_t(m0 + m) * a.x_stride + k;
-        uint4* dst = xs + ((run >> 2) * C + m) * 4 + (run & 3);
-        if constexpr (F32) {
-            const float* p = static_cast<const float*>(a.x) + at;
-            float v[8];
+    using Raw = std::conditional_t<F32, float, uint16_t>;
+    const Raw* x = static_cast<const Raw*>(a.x);
+    const int runs = n_my * 16, n = runs * n_tok;
+    for (int i0 = threadIdx.x; i0 < n; i0 += kAhead * blockDim.x) {
+        Raw v[kAhead][8];
+        uint4* dst[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int idx = i0 + u * blockDim.x;
+            if (idx >= n) break;
+            const int m = idx / runs, run = idx - m * runs;  // run = (record, i, t)
+            const int k = blk0 * kP4Cols + run * 8;
+            const int left = min(8, a.cols - k);
+            const Raw* p = x + int64_t(m0 + m) * a.x_stride + k;
+            dst[u] = xs + ((run >> 2) * C + m) * 4 + (run & 3);
             if (a.x_vec && left == 8) {
-                const float4 lo = __ldg(reinterpret_cast<const float4*>(p));
-                const float4 hi = __ldg(reinterpret_cast<const float4*>(p) + 1);
-                v[0] = lo.x, v[1] = lo.y, v[2] = lo.z, v[3] = lo.w;
-                v[4] = hi.x, v[5] = hi.y, v[6] = hi.z, v[7] = hi.w;
+#pragma unroll
+                for (int h = 0; h < (F32 ? 2 : 1); ++h)
+                    reinterpret_cast<uint4*>(v[u])[h] = __ldg(reinterpret_cast<const uint4*>(p) + h);
             } else {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = j < left ? __ldg(p + j) : 0.0f;
+                for (int j = 0; j < 8; ++j) v[u][j] = j < left ? __ldg(p + j) : Raw(0);
             }
-            uint32_t w[3][4];
+        }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint32_t lo[3], hi[3];
-                terms(v[2 * j], lo);
-                terms(v[2 * j + 1], hi);
+        for (int u = 0; u < kAhead; ++u) {
+            if (i0 + u * static_cast<int>(blockDim.x) >= n) break;
+            if constexpr (F32) {
+                uint32_t w[3][4];
 #pragma unroll
-                for (int q = 0; q < 3; ++q) w[q][j] = lo[q] | (hi[q] << 16);
-            }
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t lo[3], hi[3];
+                    terms(v[u][2 * j], lo);
+                    terms(v[u][2 * j + 1], hi);
 #pragma unroll
-            for (int q = 0; q < 3; ++q)
-                dst[q * n_tok * 4] = make_uint4(w[q][0], w[q][1], w[q][2], w[q][3]);
-        } else {
-            const uint16_t* p = static_cast<const uint16_t*>(a.x) + at;
-            uint4 v;
-            if (a.x_vec && left == 8) {
-                v = __ldg(reinterpret_cast<const uint4*>(p));
+                    for (int q = 0; q < 3; ++q) w[q][j] = lo[q] | (hi[q] << 16);
+                }
+#pragma unroll
+                for (int q = 0; q < 3; ++q)
+                    dst[u][q * n_tok * 4] = make_uint4(w[q][0], w[q][1], w[q][2], w[q][3]);
             } else {
-                uint32_t e[8];
+                uint32_t w[4];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) e[j] = j < left ? __ldg(p + j) : 0u;
-                v = make_uint4(e[0] | (e[1] << 16), e[2] | (e[3] << 16), e[4] | (e[5] << 16),
-                               e[6] | (e[7] << 16));
+                for (int j = 0; j < 4; ++j)
+                    w[j] = v[u][2 * j] | (static_cast<uint32_t>(v[u][2 * j + 1]) << 16);
+                *dst[u] = make_uint4(w[0], w[1], w[2], w[3]);
             }
-            *dst = v;
         }
     }
 }
@@ -195,6 +199,8 @@ struct GvForm {
     static constexpr int kWarps = NT <= 2 ? 8 : 16;
     static constexpr int kBlocks = NT == 1 ? 3 : NT == 2 ? 2 : 1;  // per SM
     static constexpr int kDepth = NT <= 2 ? 6 : 4;                 // ring slots per warp
+    // runs of x that a thread stages at once: more of them cost the fp32 forms their registers
+    static constexpr int kAhead = F32 ? (NT == 3 ? 2 : 1) : NT == 4 ? 4 : NT == 2 ? 8 : 2;
     static constexpr int kOut = F32 && NT > 1 ? NT / 3 : NT;       // operands of sums kept
     static constexpr int kTokens = F32 ? (NT == 1 ? 2 : 8 * NT / 3) : 8 * NT;
 };
@@ -351,7 +357,7 @@ __global__ void __launch_bounds__(GvForm<F32, NT>::kWarps * 32, GvForm<F32, NT>:
     for (int blk0 = first_blk; blk0 == 0 || blk0 < a.n_blk; blk0 += next_slab) {
         const int nb = min(a.slab_blk, a.n_blk - blk0);
         if (blk0 > first_blk) __syncthreads();  // every warp is done with the slab of x before
-        stage_x<F32>(a, xs, m0, n_tok, C, blk0, nb);
+        stage_x<F32, Form::kAhead>(a, xs, m0, n_tok, C, blk0, nb);
         if (lane == 0) slot_tile[warp] = -1;
         __syncthreads();
         if (nb == 0) {  // no columns: the sums are 0

@@ -895,7 +895,7 @@ __global__ void __launch_bounds__(kLpMaxBlock, 2)
 
 // ---- rows that fit the registers of a few warps ----------------------------------
 
-constexpr int kLhMaxWarps = 8;  // of a block, which has one row
+constexpr int kLhMaxWarps = 16;  // of a block, which has one row
 constexpr int kLhMost = 16;     // vectors per thread
 constexpr int kLhFill = 16;     // warps per SM that rows are cut for (8 to 32 measure alike)
 constexpr int kLhList = 256;    // candidates a row may have, and vectors with one
@@ -915,7 +915,7 @@ struct HeldShared {
 // more. Other blocks of the SM load meanwhile; what bounds many rows are the
 // instructions (8,192 x 4,000 bf16 22 us, 3.1 TB/s; fp32 27 us, 4.9 TB/s).
 template <typename T, int NV>
-__global__ void __launch_bounds__(32 * kLhMaxWarps, NV <= 4 ? 4 : NV <= 8 ? 3 : 2)
+__global__ void __launch_bounds__(32 * kLhMaxWarps, NV <= 4 ? 2 : 1)
     token_logprobs_held(const __grid_constant__ LogprobArgs a) {
     constexpr int kN = Vec16<T>::kN;
     __shared__ HeldShared sh;
@@ -1350,11 +1350,13 @@ CAM_API int cam_token_logprobs(int64_t rows, int64_t vocab, const void* logits, 
     // Rows that fit the registers of a block are held there. Up to 2,048 vectors that is faster
     // for any number of rows, in us against the streaming form's, without alternatives and with
     // 20: 8,192 x 2,000 fp32 17 and 29 (29 and 66), 8,192 x 16,000 bf16 57 and 84 (70 and 117).
-    // Up to 4,096 it is where rows are few: 512 x 32,000 bf16 13 and 17 (14 and 23); with many
-    // the two are alike: 8,192 x 16,000 fp32 93 to 131 (98 to 133).
+    // Up to 4,096 it is where rows are fewer: 512 x 32,000 bf16 13 and 17 (14 and 23); with many
+    // the two are alike: 8,192 x 16,000 fp32 93 to 131 (98 to 133). Up to 8,192 it is where each
+    // row has an SM: 1 x 52,000 bf16 8 and 8 (8 and 25), but 512 x 52,000 27 and 33 (19 and 29).
     const int64_t n_vec = std::max<int64_t>(1, vocab / (dtype == CAM_F32 ? 4 : 8));
     const int64_t held = 32 * kLhMaxWarps * kLhMost;
-    if (n_vec <= held / 2 || (n_vec <= held && rows <= int64_t(sms) * 8)) {
+    if (n_vec <= held / 4 || (n_vec <= held / 2 && rows <= int64_t(sms) * 8) ||
+        (n_vec <= held && rows <= sms)) {
         // as few warps as hold the row where rows are many, as many as still have four
         // vectors per thread where they are few
         int64_t warps = (n_vec + 32 * kLhMost - 1) / (32 * kLhMost);
