@@ -896,9 +896,9 @@ __global__ void __launch_bounds__(kLpMaxBlock, 2)
 // ---- rows that fit the registers of a few warps ----------------------------------
 
 constexpr int kLhMaxWarps = 16;  // of a block, which has one row
-constexpr int kLhMost = 16;     // vectors per thread
-constexpr int kLhFill = 16;     // warps per SM that rows are cut for (8 to 32 measure alike)
-constexpr int kLhList = 256;    // candidates a row may have, and vectors with one
+constexpr int kLhMost = 16;      // vectors per thread
+constexpr int kLhFill = 16;      // warps per SM that rows are cut for (8 to 32 measure alike)
+constexpr int kLhList = 256;     // candidates a row may have, and vectors with one
 
 struct HeldShared {
     float thread_max[32 * kLhMaxWarps];
@@ -913,9 +913,11 @@ struct HeldShared {
 // NV vectors of a row per thread, loaded at once and kept: the largest logit,
 // then the sums relative to it, then the few candidates, which are read once
 // more. Other blocks of the SM load meanwhile; what bounds many rows are the
-// instructions (8,192 x 4,000 bf16 22 us, 3.1 TB/s; fp32 27 us, 4.9 TB/s).
+// instructions (8,192 x 4,000 bf16 21 us, 3.1 TB/s; fp32 28 us, 4.8 TB/s).
+// Registers for the blocks that are to be resident: 102 of them at NV = 8 cost
+// 8,192 x 1,000 fp32 a tenth.
 template <typename T, int NV>
-__global__ void __launch_bounds__(32 * kLhMaxWarps, NV <= 4 ? 2 : 1)
+__global__ void __maxnreg__(NV <= 4 ? 64 : NV <= 8 ? 80 : 128)
     token_logprobs_held(const __grid_constant__ LogprobArgs a) {
     constexpr int kN = Vec16<T>::kN;
     __shared__ HeldShared sh;
@@ -1006,30 +1008,39 @@ __global__ void __launch_bounds__(32 * kLhMaxWarps, NV <= 4 ? 2 : 1)
         }
         bound = nth_of_warp(set, a.top);
     }
-    const bool list = a.top > 0 && bound > -kInf;
     auto put = [&](float x, int id) {
         const int at = atomicAdd(&sh.n, 1);
         if (at < kLhList) sh.list[at] = make_key(x, static_cast<uint32_t>(id));
     };
-    if (list && m >= bound) {
-        if (single >= bound) put(single, single_id);
+    auto mark = [&](auto&& wanted) {
+        if (!wanted(m)) return;
+        if (wanted(single) && lane < singles) put(single, single_id);
         uint32_t hits = 0;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) hits |= v[i].largest() >= bound ? 1u << i : 0u;
+        for (int i = 0; i < NV; ++i) hits |= wanted(v[i].largest()) ? 1u << i : 0u;
         int at = atomicAdd(&sh.n_vectors, __popc(hits));
         for (; hits != 0; hits &= hits - 1, ++at)
             if (at < kLhList)
                 sh.vectors[at] = static_cast<uint16_t>((__ffs(hits) - 1) * threads + tid);
-    }
-    join(s);
-    const int n_vectors = sh.n_vectors;
-    if (list && n_vectors <= kLhList) {  // a thread to a logit (from the caches)
-        for (int i = tid; i < n_vectors * kN; i += threads) {
-            const int id = row.head + sh.vectors[i / kN] * kN + i % kN;
-            const float x = widen1(row.x[id]);
-            if (x >= bound) put(x, id);
+    };
+    auto look_through = [&](auto&& wanted) {  // a thread to a logit, from the caches
+        const int n_vectors = sh.n_vectors;
+        if (n_vectors <= kLhList) {
+            for (int i = tid; i < n_vectors * kN; i += threads) {
+                const int id = row.head + sh.vectors[i / kN] * kN + i % kN;
+                const float x = widen1(row.x[id]);
+                if (wanted(x)) put(x, id);
+            }
         }
-    }
+        meet();
+        return n_vectors <= kLhList && sh.n <= kLhList;
+    };
+    const auto reaches = [&](float x) { return x >= bound; };
+    const auto passes = [&](float x) { return x > bound; };
+    const bool list = a.top > 0 && bound > -kInf;
+    if (list) mark(reaches);
+    join(s);
+    bool found = list && look_through(reaches);
 
     bool bad = false;
     if (s.r != s.r || fabsf(M) >= kHuge) {
@@ -1079,10 +1090,39 @@ __global__ void __launch_bounds__(32 * kLhMaxWarps, NV <= 4 ? 2 : 1)
     const RowResult result(s);
     if (tid == 0) result.write(a, r_at, token, x_token);
     if (a.top == 0) return;
-    meet();
-    const int n = sh.n;
-    if (!bad && list && n_vectors <= kLhList && n <= kLhList) {
+    if (!bad && !found) {
+        // many logits equal to the bound, or masks where there are too few others: those above
+        // it, and of the equal ones the first `top` in the order of ids
+        meet();
+        if (tid == 0) sh.n = sh.n_vectors = 0;
+        meet();
+        mark(passes);
+        meet();
+        found = look_through(passes) && sh.n <= kLhList - 32;
+        meet();
+        if (found && warp == 0) {
+            int left = a.top - sh.n;
+            for (int id0 = 0; id0 < a.vocab && left > 0; id0 += 32 * 8) {
+                float x[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int id = id0 + 32 * j + lane;
+                    x[j] = id < a.vocab ? widen1(row.x[id]) : kInf;
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const uint32_t who = __ballot_sync(0xFFFFFFFFu, x[j] == bound);
+                    if (x[j] == bound && __popc(who & ((1u << lane) - 1u)) < left)
+                        put(x[j], id0 + 32 * j + lane);
+                    left -= __popc(who);
+                }
+            }
+        }
+        meet();
+    }
+    if (found && !bad) {
         // a candidate's place is the number before it
+        const int n = sh.n;
         for (int i = tid; i < n; i += threads) {
             const Key key = sh.list[i];
             int place = 0;
@@ -1092,7 +1132,7 @@ __global__ void __launch_bounds__(32 * kLhMaxWarps, NV <= 4 ? 2 : 1)
         }
         return;
     }
-    // a NaN, masks, or more candidates than the list holds: one maximum at a time
+    // a NaN, or more candidates than the list holds: one maximum at a time
     Key last = ~0ull;
     for (int p = 0; p < a.top; ++p) {
         Key key = 0;
