@@ -17,7 +17,7 @@
 // A tcgen05 form (weights widened into tensor memory as the first operand, a
 // group's sums read back and scaled by warps of their own) was built and
 // measured over 73,760 x 2,048: 34.5 us for one bf16 token, 36 for 16, 45 for
-// 32 and 108 for 32 fp32 tokens, against 25, 39, 50 and 95 us of this form. Both
+// 32 and 108 for 32 fp32 tokens, against 25, 33, 47 and 92 us of this form. Both
 // are bound by the instructions that widen the weights (206 executed per 2,048
 // of them here; the tensor cores 20 % busy at one token), which tcgen05 does
 // not save. One token's 25 us are 3.2 TB/s, 47 % of the copy rate.

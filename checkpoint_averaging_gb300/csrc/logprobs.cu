@@ -27,6 +27,8 @@
 //
 // Blocks take rows in turn, two blocks of 352 + 96 threads per SM for a long
 // row; where rows are fewer than blocks, the blocks of a cluster share a row.
+// Rows short enough for the registers of one block take a form of their own
+// (token_logprobs_held), with M known before the sums.
 // Measured, 10 alternatives: 2,048 x 73,760 bf16 70 us (4.3 TB/s; 5.7 once
 // every block has 16 rows, the instructions of the exponentials and the
 // widening being the bound then), 4,096 x 50,257 fp32 139 us (5.9 TB/s, 6.7
@@ -1231,7 +1233,7 @@ __device__ __forceinline__ GradRow grad_row(const LogprobGradArgs& a, int64_t ro
 
 // A piece of a row for each TEAM threads of a block; a team has about a batch or
 // two of vectors per thread: 256 threads for a long row, 32 for the shortest
-// (8,192 x 2,001 bf16 19 us against 29 us with 256). Blocks that walk over many pieces, with the
+// (8,192 x 2,001 bf16 18 us). Blocks that walk over many pieces, with the
 // next piece's row values loaded ahead, measured 5 to 8 % slower. With
 // y = (x - lse) log2(e), every logit's gradient is
 //   -p (g + h (log p + H)) = 2^y (b + k y),  k = -h ln 2,  b = -(g + h H).
