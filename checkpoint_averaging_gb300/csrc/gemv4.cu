@@ -137,7 +137,7 @@ __device__ __forceinline__ void stage_x(const GemvArgs& a, uint4* xs, int m0, in
     const Raw* x = static_cast<const Raw*>(a.x);
     const int runs = n_my * 16, n = runs * n_tok;
     for (int i0 = threadIdx.x; i0 < n; i0 += kAhead * blockDim.x) {
-        Raw v[kAhead][8];
+        alignas(16) Raw v[kAhead][8];
         uint4* dst[kAhead];
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {

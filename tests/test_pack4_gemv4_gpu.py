@@ -212,6 +212,15 @@ def test_products_of_many_rows(tokens, rows, cols, group, dtype):
     test_products(tokens, rows, cols, group, dtype)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("tokens,rows,cols", [
+    (3, 5000, 9001), (8, 2433, 16000), (12, 2600, 9000), (17, 4000, 3700), (32, 2500, 5000),
+    (40, 1300, 8200)])
+def test_products_of_long_rows_that_are_many(tokens, rows, cols, dtype):
+    # x in slabs, taken by one block or by two side by side
+    test_products(tokens, rows, cols, 64, dtype)
+
+
 @pytest.mark.parametrize("tokens,cols", [(1, 131072), (2, 131072), (32, 131072)])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_the_longest_rows(tokens, cols, dtype):
