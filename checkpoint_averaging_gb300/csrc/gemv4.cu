@@ -587,9 +587,16 @@ CAM_API int cam_gemv4(int64_t tokens, int64_t rows, int64_t cols, const void* x,
     // or, alone, in what the tiles' sums leave.
     const int record = 256 * (f32 ? 3 : 1) * a.pass_tokens;  // bytes of x per record of a tile
     const int fixed = 128 + p.warps * (p.depth * p4_tile_bytes(group) + p.out * 512);
+    const int64_t all_x = int64_t(record) * a.n_blk;
     int per_sm = p.blocks;
-    while (per_sm > 1 && int64_t(record) * a.n_blk + fixed > 228 * 1024 / per_sm - 1280) --per_sm;
-    const int room = (per_sm > 1 ? 228 * 1024 / per_sm - 1280 : kMaxSharedBytes) - fixed;
+    auto room_of = [&](int k) { return (k > 1 ? 228 * 1024 / k - 1280 : kMaxSharedBytes) - fixed; };
+    while (per_sm > 1 && all_x > room_of(per_sm)) {
+        // (two blocks whose slabs are two at most, in pairs, do better than one: 8 bf16 tokens over
+        // 16,384 x 9,000 33 us against 38; with three slabs 3,000 x 16,000 takes 26 against 21)
+        if (per_sm == 2 && 2 * all_x <= 7 * int64_t(room_of(2))) break;
+        --per_sm;
+    }
+    const int room = room_of(per_sm);
     const int64_t blocks_most = std::max(1, sms * per_sm / passes);
     int64_t blocks = std::min<int64_t>(a.n_tiles, blocks_most);
     int kept = 0;
@@ -602,7 +609,7 @@ CAM_API int cam_gemv4(int64_t tokens, int64_t rows, int64_t cols, const void* x,
     // x in slabs: where the tiles' sums leave room, the blocks of a pair take them side by side
     // and stage half as many each (32 tokens over 16,384 x 9,000: bf16 66 -> 54 us, fp32 120 ->
     // 100; larger clusters leave SMs out and take 90 and 180)
-    if (a.cluster == 1 && int64_t(record) * a.n_blk > room && blocks > 1) {
+    if (a.cluster == 1 && all_x > room && blocks > 1) {
         auto slabs = [&](int c) {  // of a block
             const int64_t runs = std::min<int64_t>(a.n_tiles, blocks_most / c);
             const int64_t sums = (a.n_tiles + runs - 1) / runs * p.out * 512;
@@ -614,7 +621,7 @@ CAM_API int cam_gemv4(int64_t tokens, int64_t rows, int64_t cols, const void* x,
             blocks = std::min<int64_t>(a.n_tiles, blocks_most / 2);
         }
     }
-    if (a.cluster > 1 || int64_t(record) * a.n_blk > room) {
+    if (a.cluster > 1 || all_x > room) {
         const int kept_room = room - record, per_tile = p.out * 512;
         const int64_t tiles = kept_room / per_tile;  // a block may have at most
         blocks = std::max(blocks, (a.n_tiles + tiles - 1) / tiles);
