@@ -63,7 +63,7 @@ struct GemvArgs {
     int32_t pass_tokens;  // of one pass (grid.y passes)
     int32_t n_blk;        // 128-column records of a tile
     int32_t slab_blk;     // of which x has so many in shared memory at once
-    int32_t n_tiles;      // 16-row tiles
+    int32_t tiles, more;  // 16-row tiles of a run, and the first runs that have one more
     int32_t cluster;      // blocks that share a run of tiles, each with its own slabs
     int32_t y_bf16, x_vec;
 };
@@ -219,9 +219,10 @@ __global__ void __launch_bounds__(GvForm<F32, NT>::kWarps * 32, GvForm<F32, NT>:
     const int n_tok = min(a.pass_tokens, a.tokens - m0);
     const int C = F32 ? 3 * n_tok : n_tok;
     const int rank = a.cluster > 1 ? static_cast<int>(cg::this_cluster().block_rank()) : 0;
-    const int run = blockIdx.x / a.cluster, runs = gridDim.x / a.cluster;
-    const int tile0 = static_cast<int>(int64_t(a.n_tiles) * run / runs);
-    const int my_tiles = static_cast<int>(int64_t(a.n_tiles) * (run + 1) / runs) - tile0;
+    const int run = a.cluster > 1 ? blockIdx.x / a.cluster : blockIdx.x;
+    int tile0 = run * a.tiles + min(run, a.more);
+    int my_tiles = a.tiles + (run < a.more ? 1 : 0);
+    asm volatile("" : "+r"(tile0), "+r"(my_tiles));  // (kept, not worked out again at each use)
     const bool slabs = a.slab_blk < a.n_blk;
     const int first_blk = rank * a.slab_blk, next_slab = a.cluster * a.slab_blk;
 
@@ -572,7 +573,7 @@ CAM_API int cam_gemv4(int64_t tokens, int64_t rows, int64_t cols, const void* x,
     a.cols = static_cast<int32_t>(cols);
     a.tokens = static_cast<int32_t>(tokens);
     a.n_blk = static_cast<int32_t>((cols + kP4Cols - 1) / kP4Cols);
-    a.n_tiles = static_cast<int32_t>((rows + kP4Rows - 1) / kP4Rows);
+    const auto n_tiles = static_cast<int32_t>((rows + kP4Rows - 1) / kP4Rows);
     a.y_bf16 = y_dtype == CAM_BF16;
     a.x_vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && x_stride * x_size % 16 == 0;
     // as few passes over the weights as the widest form allows, evenly
@@ -598,7 +599,7 @@ CAM_API int cam_gemv4(int64_t tokens, int64_t rows, int64_t cols, const void* x,
     }
     const int room = room_of(per_sm);
     const int64_t blocks_most = std::max(1, sms * per_sm / passes);
-    int64_t blocks = std::min<int64_t>(a.n_tiles, blocks_most);
+    int64_t blocks = std::min<int64_t>(n_tiles, blocks_most);
     int kept = 0;
     a.slab_blk = a.n_blk;
     // few rows: a cluster for each tile or so, as long as a warp has a few records
@@ -611,27 +612,29 @@ CAM_API int cam_gemv4(int64_t tokens, int64_t rows, int64_t cols, const void* x,
     // 100; larger clusters leave SMs out and take 90 and 180)
     if (a.cluster == 1 && all_x > room && blocks > 1) {
         auto slabs = [&](int c) {  // of a block
-            const int64_t runs = std::min<int64_t>(a.n_tiles, blocks_most / c);
-            const int64_t sums = (a.n_tiles + runs - 1) / runs * p.out * 512;
+            const int64_t runs = std::min<int64_t>(n_tiles, blocks_most / c);
+            const int64_t sums = (n_tiles + runs - 1) / runs * p.out * 512;
             const int64_t slab = (room - sums) / record;
             return slab < 1 ? INT64_MAX : (a.n_blk + c * slab - 1) / (c * slab);
         };
         if (slabs(2) < slabs(1)) {
             a.cluster = 2;
-            blocks = std::min<int64_t>(a.n_tiles, blocks_most / 2);
+            blocks = std::min<int64_t>(n_tiles, blocks_most / 2);
         }
     }
     if (a.cluster > 1 || all_x > room) {
         const int kept_room = room - record, per_tile = p.out * 512;
         const int64_t tiles = kept_room / per_tile;  // a block may have at most
-        blocks = std::max(blocks, (a.n_tiles + tiles - 1) / tiles);
-        kept = static_cast<int>((a.n_tiles + blocks - 1) / blocks) * per_tile;
+        blocks = std::max(blocks, (n_tiles + tiles - 1) / tiles);
+        kept = static_cast<int>((n_tiles + blocks - 1) / blocks) * per_tile;
         a.slab_blk = std::max(1, (room - kept) / record);
         int slabs = (a.n_blk + a.slab_blk - 1) / a.slab_blk;
         slabs = (slabs + a.cluster - 1) / a.cluster * a.cluster;
         a.slab_blk = (a.n_blk + slabs - 1) / slabs;
     }
     a.slab_blk = std::max(1, a.slab_blk);
+    a.tiles = static_cast<int32_t>(n_tiles / blocks);
+    a.more = static_cast<int32_t>(n_tiles % blocks);
     const int bytes = fixed + kept + a.slab_blk * record;
 
     if (bytes > 48 * 1024) ce = allow_shared(p.kernel, dev, *p.shared_ok);
