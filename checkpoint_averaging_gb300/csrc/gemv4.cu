@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(GvForm<F32, NT>::kWarps * 32, GvForm<F32, NT>:
     };
 
     // loads run ahead of the sums, over tiles and slabs
-    int l_blk0 = first_blk, l_nb = 0, l_at = 0, l_left = 0;
+    int l_blk0 = first_blk, l_nb = 0, l_run = 0, l_left = 0;  // l_run: records in one piece
     bool l_more = a.n_blk > 0;
     const uint8_t* l_src = nullptr;
     auto open_slab = [&]() {  // to the first of this warp's records, from slab l_blk0 on
@@ -253,10 +253,11 @@ __global__ void __launch_bounds__(GvForm<F32, NT>::kWarps * 32, GvForm<F32, NT>:
             range(l_blk0, begin, end);
             l_nb = min(a.slab_blk, a.n_blk - l_blk0);
             if (begin == end) continue;
+            const int tile = begin / l_nb, at = begin - tile * l_nb;
             l_left = end - begin;
-            l_at = begin % l_nb;
-            l_src = a.packed + (int64_t(tile0 + begin / l_nb) * a.n_blk + l_blk0 + l_at) * kTile +
-                    lane * 16;
+            l_run = slabs ? min(l_nb - at, l_left) : l_left;
+            l_left -= l_run;
+            l_src = a.packed + (int64_t(tile0 + tile) * a.n_blk + l_blk0 + at) * kTile + lane * 16;
             return;
         }
     };
@@ -269,13 +270,15 @@ __global__ void __launch_bounds__(GvForm<F32, NT>::kWarps * 32, GvForm<F32, NT>:
             cp16(l_dst + 512, l_src + 512);
             if (lane < kPer * 2) cp16(l_dst + 1024, l_src + 1024);
             l_src += kTile;
-            if (++l_at == l_nb) {
-                l_at = 0;
-                if (slabs) l_src += int64_t(a.n_blk - l_nb) * kTile;
-            }
-            if (--l_left == 0) {
-                l_blk0 += next_slab;
-                open_slab();
+            if (--l_run == 0) {
+                if (l_left > 0) {  // (of a slab: on to the next tile's)
+                    l_src += int64_t(a.n_blk - l_nb) * kTile;
+                    l_run = min(l_nb, l_left);
+                    l_left -= l_run;
+                } else {
+                    l_blk0 += next_slab;
+                    open_slab();
+                }
             }
         }
         cp_commit();
@@ -370,7 +373,8 @@ __global__ void __launch_bounds__(GvForm<F32, NT>::kWarps * 32, GvForm<F32, NT>:
         }
         int begin, end;
         range(blk0, begin, end);
-        int tile = tile0 + begin / nb, b = begin % nb;
+        int tile = begin / nb, b = begin - tile * nb;
+        tile += tile0;
         bool owner = b == 0, open = false;  // the tile under way: has its first record; not finished
         float acc[kOut][4];
         float4 v[kOut];
