@@ -126,11 +126,17 @@ __device__ __forceinline__ void terms(float x, uint32_t (&t)[3]) {
     t[2] = __float_as_uint(r - __uint_as_float(__float_as_uint(r) & 0xFFFF0000u)) >> 16;
 }
 
-// A slab of x into shared memory: 16 bytes (8 elements) of a column at
-// ((slab-local record * 4 + i) * C + column) * 4 + t, elements 32 i + 8 t .. + 7 of
-// the record. An fp32 x has three columns for a token, n_tok apart. Elements
-// past the end are 0.
-template <bool F32, int kAhead>
+// Where x stands in shared memory: the 16 runs (of 8 elements, 16 bytes) of a
+// record's column together, run 4 i + t (elements 32 i + 8 t .. + 7) in place
+// (4 i + t) ^ (odd << 2), so that the lanes of two neighbouring columns, one of
+// them odd, read different banks. An fp32 x has three columns for a token, n_tok
+// apart; `odd` goes by the token, or by the column where one operand has all.
+__device__ __forceinline__ int x_place(int record, int C, int column, int run, int odd) {
+    return (record * C + column) * 16 + (run ^ (odd << 2));
+}
+
+// A slab of x into shared memory. Elements past the end are 0.
+template <bool F32, bool kPacked, int kAhead>
 __device__ __forceinline__ void stage_x(const GemvArgs& a, uint4* xs, int m0, int n_tok, int C,
                                         int blk0, int n_my) {
     using Raw = std::conditional_t<F32, float, uint16_t>;
@@ -138,7 +144,8 @@ __device__ __forceinline__ void stage_x(const GemvArgs& a, uint4* xs, int m0, in
     const int runs = n_my * 16, n = runs * n_tok;
     for (int i0 = threadIdx.x; i0 < n; i0 += kAhead * blockDim.x) {
         alignas(16) Raw v[kAhead][8];
-        uint4* dst[kAhead];
+        uint4* dst[kAhead];  // (the first column's)
+        int token[kAhead];
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             const int idx = i0 + u * blockDim.x;
@@ -147,7 +154,8 @@ __device__ __forceinline__ void stage_x(const GemvArgs& a, uint4* xs, int m0, in
             const int k = blk0 * kP4Cols + run * 8;
             const int left = min(8, a.cols - k);
             const Raw* p = x + int64_t(m0 + m) * a.x_stride + k;
-            dst[u] = xs + ((run >> 2) * C + m) * 4 + (run & 3);
+            dst[u] = xs + x_place(run >> 4, C, m, run & 15, kPacked ? 0 : m & 1);
+            token[u] = m;
             if (a.x_vec && left == 8) {
 #pragma unroll
                 for (int h = 0; h < (F32 ? 2 : 1); ++h)
@@ -171,8 +179,13 @@ __device__ __forceinline__ void stage_x(const GemvArgs& a, uint4* xs, int m0, in
                     for (int q = 0; q < 3; ++q) w[q][j] = lo[q] | (hi[q] << 16);
                 }
 #pragma unroll
-                for (int q = 0; q < 3; ++q)
-                    dst[u][q * n_tok * 4] = make_uint4(w[q][0], w[q][1], w[q][2], w[q][3]);
+                for (int q = 0; q < 3; ++q) {
+                    const int column = q * n_tok + token[u];
+                    uint4* to = dst[u] + q * n_tok * 16;
+                    if (kPacked && (column & 1))  // (the run's place in a pair of fours)
+                        to = xs + (static_cast<int>(to - xs) ^ 4);
+                    *to = make_uint4(w[q][0], w[q][1], w[q][2], w[q][3]);
+                }
             } else {
                 uint32_t w[4];
 #pragma unroll
@@ -291,12 +304,13 @@ __global__ void __launch_bounds__(GvForm<F32, NT>::kWarps * 32, GvForm<F32, NT>:
     // this lane's column of each operand; past the last token any will do, its results are not
     // kept
     int x_lane[NT];
+    const int x_odd = -8 * (g & 1);  // (steps change places in pairs)
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         if constexpr (F32 && NT > 1)
-            x_lane[n] = (n / kOut * n_tok + min(8 * (n % kOut) + g, n_tok - 1)) * 4 + t;
+            x_lane[n] = x_place(0, C, n / kOut * n_tok + min(8 * (n % kOut) + g, n_tok - 1), t, g & 1);
         else
-            x_lane[n] = min(8 * n + g, C - 1) * 4 + t;
+            x_lane[n] = x_place(0, C, min(8 * n + g, C - 1), t, g & 1);
     }
 
     // A tile's finished sums. v[n]: rows g (x, y) and g + 8 (z, w), columns 8 n + 2 t and + 1.
@@ -357,11 +371,11 @@ __global__ void __launch_bounds__(GvForm<F32, NT>::kWarps * 32, GvForm<F32, NT>:
         write(tile, v);
     };
 
-    uint32_t at_slot = 0;
+    int at = 0;  // the ring's slot under way
     for (int blk0 = first_blk; blk0 == 0 || blk0 < a.n_blk; blk0 += next_slab) {
         const int nb = min(a.slab_blk, a.n_blk - blk0);
         if (blk0 > first_blk) __syncthreads();  // every warp is done with the slab of x before
-        stage_x<F32, Form::kAhead>(a, xs, m0, n_tok, C, blk0, nb);
+        stage_x<F32, Form::kPacked, Form::kAhead>(a, xs, m0, n_tok, C, blk0, nb);
         if (lane == 0) slot_tile[warp] = -1;
         __syncthreads();
         if (nb == 0) {  // no columns: the sums are 0
@@ -393,68 +407,75 @@ __global__ void __launch_bounds__(GvForm<F32, NT>::kWarps * 32, GvForm<F32, NT>:
         for (int n = 0; n < kOut; ++n)
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[n][j] = 0.0f;
-        for (int pos = begin; pos < end; ++pos) {
-            cp_wait<kDepth - 2>();
-            __syncwarp();  // every lane's copies are in, and every lane is done with the slot before
-            load();
-            const uint8_t* q = ring + at_slot * kTile;
-            if (++at_slot == kDepth) at_slot = 0;
+        for (int left = end - begin; left > 0;) {  // a tile's records at a time
+            int here = min(left, nb - b);
+            left -= here;
+            open = b + here < nb;
             const uint4* xb = xs + b * 16 * C;
-            const uint4 wl = *reinterpret_cast<const uint4*>(q + lane * 16);
-            const uint4 wh = *reinterpret_cast<const uint4*>(q + 512 + lane * 16);
-            uint32_t sl[kPer > 1 ? kPer / 2 : 1], sh[kPer > 1 ? kPer / 2 : 1];  // bf16 pairs
-            const uint8_t* sp = q + 1024 + g * (4 * kPer);
-            if constexpr (kPer == 4) {
-                const uint4 s = *reinterpret_cast<const uint4*>(sp);
-                sl[0] = s.x, sl[1] = s.y, sh[0] = s.z, sh[1] = s.w;
-            } else if constexpr (kPer == 2) {
-                const uint2 s = *reinterpret_cast<const uint2*>(sp);
-                sl[0] = s.x, sh[0] = s.y;
-            } else {
-                sl[0] = *reinterpret_cast<const uint32_t*>(sp);
-                sh[0] = sl[0] >> 16;
-            }
-            constexpr int kSteps = GROUP / 32;  // steps of 32 columns per group
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) {
-                uint32_t al[kSteps][4], ah[kSteps][4];
-#pragma unroll
-                for (int k = 0; k < kSteps; ++k) {
-                    const int i = j * kSteps + k;
-                    const uint32_t lo = i == 0 ? wl.x : i == 1 ? wl.y : i == 2 ? wl.z : wl.w;
-                    const uint32_t hi = i == 0 ? wh.x : i == 1 ? wh.y : i == 2 ? wh.z : wh.w;
-#pragma unroll
-                    for (int p = 0; p < 4; ++p) al[k][p] = widen(lo, p), ah[k][p] = widen(hi, p);
+#pragma unroll 1
+            for (; here > 0; --here, xb += 16 * C) {
+                cp_wait<kDepth - 2>();
+                __syncwarp();  // every lane's copies are in, and every lane is done with the slot before
+                load();
+                const uint8_t* q = ring + at;
+                at += kTile;
+                if (at == kDepth * kTile) at = 0;
+                const uint4 wl = *reinterpret_cast<const uint4*>(q + lane * 16);
+                const uint4 wh = *reinterpret_cast<const uint4*>(q + 512 + lane * 16);
+                uint32_t sl[kPer > 1 ? kPer / 2 : 1], sh[kPer > 1 ? kPer / 2 : 1];  // bf16 pairs
+                const uint8_t* sp = q + 1024 + g * (4 * kPer);
+                if constexpr (kPer == 4) {
+                    const uint4 s = *reinterpret_cast<const uint4*>(sp);
+                    sl[0] = s.x, sl[1] = s.y, sh[0] = s.z, sh[1] = s.w;
+                } else if constexpr (kPer == 2) {
+                    const uint2 s = *reinterpret_cast<const uint2*>(sp);
+                    sl[0] = s.x, sh[0] = s.y;
+                } else {
+                    sl[0] = *reinterpret_cast<const uint32_t*>(sp);
+                    sh[0] = sl[0] >> 16;
                 }
-                // a token's three terms in one sum, over the whole group the smallest first (step
-                // by step the sum's error is three times as large at group 128; in sums of their
-                // own 32 tokens over 73,760 x 2,048 took 100 us instead of 92)
-                float part[kOut][4];
+                constexpr int kSteps = GROUP / 32;  // steps of 32 columns per group
 #pragma unroll
-                for (int q = NT / kOut - 1; q >= 0; --q)
+                for (int j = 0; j < kPer; ++j) {
+                    uint32_t al[kSteps][4], ah[kSteps][4];
 #pragma unroll
-                    for (int k = 0; k < kSteps; ++k)
+                    for (int k = 0; k < kSteps; ++k) {
+                        const int i = j * kSteps + k;
+                        const uint32_t lo = i == 0 ? wl.x : i == 1 ? wl.y : i == 2 ? wl.z : wl.w;
+                        const uint32_t hi = i == 0 ? wh.x : i == 1 ? wh.y : i == 2 ? wh.z : wh.w;
 #pragma unroll
-                        for (int n = 0; n < kOut; ++n) {
-                            const uint4 x = xb[(j * kSteps + k) * C * 4 + x_lane[q * kOut + n]];
-                            if (q == NT / kOut - 1 && k == 0)
-                                mma_first(part[n], al[k][0], ah[k][0], al[k][1], ah[k][1], x.x, x.y);
-                            else
-                                mma(part[n], al[k][0], ah[k][0], al[k][1], ah[k][1], x.x, x.y);
-                            mma(part[n], al[k][2], ah[k][2], al[k][3], ah[k][3], x.z, x.w);
-                        }
-                const float s0 = __uint_as_float((j & 1) ? sl[j >> 1] & 0xFFFF0000u : sl[j >> 1] << 16);
-                const float s1 = __uint_as_float((j & 1) ? sh[j >> 1] & 0xFFFF0000u : sh[j >> 1] << 16);
+                        for (int p = 0; p < 4; ++p) al[k][p] = widen(lo, p), ah[k][p] = widen(hi, p);
+                    }
+                    // a token's three terms in one sum, over the whole group the smallest first (step
+                    // by step the sum's error is three times as large at group 128; in sums of their
+                    // own 32 tokens over 73,760 x 2,048 took 100 us instead of 92)
+                    float part[kOut][4];
 #pragma unroll
-                for (int n = 0; n < kOut; ++n) {
-                    acc[n][0] = fmaf(s0, part[n][0], acc[n][0]);
-                    acc[n][1] = fmaf(s0, part[n][1], acc[n][1]);
-                    acc[n][2] = fmaf(s1, part[n][2], acc[n][2]);
-                    acc[n][3] = fmaf(s1, part[n][3], acc[n][3]);
+                    for (int q = NT / kOut - 1; q >= 0; --q)
+#pragma unroll
+                        for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+                            for (int n = 0; n < kOut; ++n) {
+                                const int i = j * kSteps + k;
+                                const uint4 x = xb[x_lane[q * kOut + n] + 4 * i + ((i & 1) ? x_odd : 0)];
+                                if (q == NT / kOut - 1 && k == 0)
+                                    mma_first(part[n], al[k][0], ah[k][0], al[k][1], ah[k][1], x.x, x.y);
+                                else
+                                    mma(part[n], al[k][0], ah[k][0], al[k][1], ah[k][1], x.x, x.y);
+                                mma(part[n], al[k][2], ah[k][2], al[k][3], ah[k][3], x.z, x.w);
+                            }
+                    const float s0 = __uint_as_float((j & 1) ? sl[j >> 1] & 0xFFFF0000u : sl[j >> 1] << 16);
+                    const float s1 = __uint_as_float((j & 1) ? sh[j >> 1] & 0xFFFF0000u : sh[j >> 1] << 16);
+#pragma unroll
+                    for (int n = 0; n < kOut; ++n) {
+                        acc[n][0] = fmaf(s0, part[n][0], acc[n][0]);
+                        acc[n][1] = fmaf(s0, part[n][1], acc[n][1]);
+                        acc[n][2] = fmaf(s1, part[n][2], acc[n][2]);
+                        acc[n][3] = fmaf(s1, part[n][3], acc[n][3]);
+                    }
                 }
             }
-            open = true;
-            if (++b == nb) {
+            if (!open) {
                 if (owner) {
                     gather();
                     finish(tile, blk0, v);
@@ -466,7 +487,7 @@ __global__ void __launch_bounds__(GvForm<F32, NT>::kWarps * 32, GvForm<F32, NT>:
 #pragma unroll
                     for (int j = 0; j < 4; ++j) acc[n][j] = 0.0f;
                 b = 0, ++tile;
-                owner = true, open = false;
+                owner = true;
             }
         }
         if (open && !owner) leave();
