@@ -213,7 +213,7 @@ struct GvForm {
     static constexpr int kBlocks = NT == 1 ? 3 : NT == 2 ? 2 : 1;  // per SM
     static constexpr int kDepth = NT <= 2 ? 6 : 4;                 // ring slots per warp
     // runs of x that a thread stages at once: more of them cost the fp32 forms their registers
-    static constexpr int kAhead = F32 ? (NT == 3 ? 2 : 1) : NT == 4 ? 4 : NT == 2 ? 8 : 2;
+    static constexpr int kAhead = F32 ? (NT == 3 ? 2 : 1) : NT == 4 ? 4 : NT == 2 ? 6 : 2;
     static constexpr int kOut = F32 && NT > 1 ? NT / 3 : NT;       // operands of sums kept
     static constexpr int kTokens = F32 ? (NT == 1 ? 2 : 8 * NT / 3) : 8 * NT;
 };
