@@ -17,10 +17,10 @@
 // A tcgen05 form (weights widened into tensor memory as the first operand, a
 // group's sums read back and scaled by warps of their own) was built and
 // measured over 73,760 x 2,048: 34.5 us for one bf16 token, 36 for 16, 45 for
-// 32 and 108 for 32 fp32 tokens, against 25, 33, 47 and 92 us of this form. Both
-// are bound by the instructions that widen the weights (206 executed per 2,048
+// 32 and 108 for 32 fp32 tokens, against 23, 31, 43 and 86 us of this form. Both
+// are bound by the instructions that widen the weights (188 executed per 2,048
 // of them here; the tensor cores 20 % busy at one token), which tcgen05 does
-// not save. One token's 25 us are 3.2 TB/s, 47 % of the copy rate.
+// not save. One token's 22.6 us are 3.6 TB/s, 52 % of the copy rate.
 //
 // A block has a run of the matrix's 16-row tiles, a like share for every block,
 // and holds x in shared memory in the order of the operand. Its warps share out
@@ -448,7 +448,7 @@ __global__ void __launch_bounds__(GvForm<F32, NT>::kWarps * 32, GvForm<F32, NT>:
                     }
                     // a token's three terms in one sum, over the whole group the smallest first (step
                     // by step the sum's error is three times as large at group 128; in sums of their
-                    // own 32 tokens over 73,760 x 2,048 took 100 us instead of 92)
+                    // own 32 tokens over 73,760 x 2,048 took 100 us where this took 92)
                     float part[kOut][4];
 #pragma unroll
                     for (int q = NT / kOut - 1; q >= 0; --q)
