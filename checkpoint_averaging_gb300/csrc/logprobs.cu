@@ -153,13 +153,16 @@ struct Vec16<float> {
             for (int j = 0; j < 4; ++j) m = max_nan(m, v[i].get(j));
         return m;
     }
-    __device__ __forceinline__ Vec16 held_finite() const {  // NaN stays
+    using Floor = float;
+    static __device__ __forceinline__ Floor floor_at(float low) { return low; }
+    __device__ __forceinline__ Vec16 held_at(Floor low) const {  // NaN stays
         Vec16 v;
-        v.u = make_uint4(low(u.x), low(u.y), low(u.z), low(u.w));
+        v.u = make_uint4(hold(u.x, low), hold(u.y, low), hold(u.z, low), hold(u.w, low));
         return v;
     }
-    static __device__ __forceinline__ uint32_t low(uint32_t w) {
-        return __float_as_uint(max_nan(__uint_as_float(w), -2e38f));
+    __device__ __forceinline__ Vec16 held_finite() const { return held_at(-2e38f); }
+    static __device__ __forceinline__ uint32_t hold(uint32_t w, Floor low) {
+        return __float_as_uint(max_nan(__uint_as_float(w), low));
     }
 };
 
@@ -188,13 +191,18 @@ struct Vec16<uint16_t> {
                             __hmax2_nan(as2(v[i].u.z), as2(v[i].u.w)));
         return max_nan(__low2float(m), __high2float(m));
     }
-    __device__ __forceinline__ Vec16 held_finite() const {  // NaN stays
+    using Floor = __nv_bfloat162;
+    static __device__ __forceinline__ Floor floor_at(float low) {  // the next bf16 below, twice
+        return __bfloat162bfloat162(__float2bfloat16_rd(low));
+    }
+    __device__ __forceinline__ Vec16 held_at(Floor low) const {  // NaN stays
         Vec16 v;
-        v.u = make_uint4(low(u.x), low(u.y), low(u.z), low(u.w));
+        v.u = make_uint4(hold(u.x, low), hold(u.y, low), hold(u.z, low), hold(u.w, low));
         return v;
     }
-    static __device__ __forceinline__ uint32_t low(uint32_t w) {
-        const __nv_bfloat162 m = __hmax2_nan(as2(w), as2(0xFF16FF16u));
+    __device__ __forceinline__ Vec16 held_finite() const { return held_at(as2(0xFF16FF16u)); }
+    static __device__ __forceinline__ uint32_t hold(uint32_t w, Floor low) {
+        const __nv_bfloat162 m = __hmax2_nan(as2(w), low);
         return *reinterpret_cast<const uint32_t*>(&m);
     }
     static __device__ __forceinline__ __nv_bfloat162 as2(uint32_t w) {
@@ -1190,6 +1198,7 @@ __global__ void __maxnreg__(NV <= 4 ? 64 : NV <= 8 ? 80 : 128)
 constexpr int kLbThreads = 256;
 constexpr int kLbBatch = 4;   // vectors per thread in flight
 constexpr int kLbBlocks = 5;  // blocks per SM that rows are cut for
+constexpr float kOutOfReach = 200.0f;  // (exp(-200) < 2^-149)
 
 struct LogprobGradArgs {
     const void* logits;
@@ -1261,6 +1270,9 @@ __device__ __forceinline__ GradRow grad_row(const LogprobGradArgs& a, int64_t ro
 //   -p (g + h (log p + H)) = 2^y (b + k y),  k = -h ln 2,  b = -(g + h H).
 // y is one fma, x log2(e) - RN(lse log2(e)); what that rounding (and lse_lo)
 // leaves out is the same for all logits of the row, so it goes into b and k.
+// Logits more than kOutOfReach below lse, masks among them, have p = 0 in
+// binary32; they are held there, because b + k y has to stay finite under any h
+// for 0 times it to be 0.
 template <typename T, int TEAM>
 __global__ void __launch_bounds__(kLbThreads)
     token_logprobs_backward(const __grid_constant__ LogprobGradArgs a) {
@@ -1291,7 +1303,7 @@ __global__ void __launch_bounds__(kLbThreads)
     auto single = [&](float v) {
         if (zeros) return 0.0f;
         if (nans) return NAN;
-        const float d = fmaxf((v - r.lse) - r.lse_lo, -1e30f);
+        const float d = fmaxf((v - r.lse) - r.lse_lo, -kOutOfReach);
         return -ex2(d * kLog2e) * fmaf(r.h, d + r.H, g);
     };
     if (!zeros && !nans && fabsf(r.lse) < kHuge) {
@@ -1302,6 +1314,7 @@ __global__ void __launch_bounds__(kLbThreads)
         const float b = fmaf(k, off, -f * fmaf(r.h, r.H, g));
         const Pair log2e = pair(kLog2e, kLog2e), base2 = pair(base, base);
         const Pair k2 = pair(k, k), b2 = pair(b, b);
+        const auto low = Vec16<T>::floor_at(r.lse - kOutOfReach);
         const int hit =  // the token among the vectors' logits
             r.token >= head ? static_cast<int>(min(r.token, int64_t(a.vocab))) - head : -kN;
         for (int v0 = begin + tid; v0 < end; v0 += team * kLbBatch) {
@@ -1314,7 +1327,7 @@ __global__ void __launch_bounds__(kLbThreads)
             for (int i = 0; i < kLbBatch; ++i) {
                 const int v = v0 + i * team;
                 if (v >= end) break;
-                const Vec16<T> u = in[i].held_finite();
+                const Vec16<T> u = in[i].held_at(low);
                 float y[kN];
 #pragma unroll
                 for (int j = 0; j < kN; j += 2) {

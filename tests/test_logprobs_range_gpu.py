@@ -1,0 +1,87 @@
+"""Log probabilities and their gradient where the arithmetic's range decides:
+masked logits under large gradients, and logits far from 0, on the GPU against
+the definitions in 64 bits with the largest logit subtracted first.
+
+Tolerances, absolute, from the derivations in test_logprobs_gpu.py with the
+magnitude of the logits taken out: x - M is exact where it matters, so log p
+keeps 2e-5 + 2^-22 |log p| however large M is.
+"""
+import math
+
+import pytest
+import torch
+
+from checkpoint_averaging_gb300 import binding as B
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+INF = math.inf
+
+
+@pytest.fixture(autouse=True)
+def _needs_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA GPU")
+    yield
+    torch.cuda.synchronize()
+
+
+def distribution(x):
+    """In 64 bits: M, log s (lse = M + log s), log p, p and the entropy."""
+    x = x.double()
+    M = x.amax(1, keepdim=True)
+    d = x - M
+    e = d.exp()
+    s = e.sum(1, keepdim=True)
+    log_s = s.log()
+    H = log_s - (e * d.masked_fill(e == 0, 0.0)).sum(1, keepdim=True) / s
+    return M, log_s, d - log_s, e / s, H
+
+
+def gradient(x, tokens, g, h):
+    """The formula, and what rounding may add: 1e-4 p (|g| + |h| (|log p| + H)) + 2^-22 |g|,
+    and 2^-8 of a bf16 result."""
+    _, _, logp, p, H = distribution(x)
+    g, h = g.double()[:, None], h.double()[:, None]
+    known = (tokens >= 0)[:, None]
+    one = torch.zeros_like(p).scatter_(1, tokens.clamp(min=0)[:, None], 1.0)
+    lp = logp.masked_fill(p == 0, 0.0)
+    want = g * known * (one - p) - h * p * (lp + H)
+    tol = 1e-4 * p * (g.abs() + h.abs() * (lp.abs() + H)) + 2.0 ** -22 * g.abs()
+    if x.dtype == torch.bfloat16:
+        tol = tol + 2.0 ** -8 * want.abs()
+    return want, tol
+
+
+def statistics(x):
+    """(lse, what its rounding left out, entropy) as the forward call would give them, from 64 bits."""
+    M, log_s, _, _, H = distribution(x)
+    lse = (M + log_s).float()
+    return lse[:, 0], ((M - lse.double()) + log_s).float()[:, 0], H.float()[:, 0]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("vocab", [40, 3001, 50304])
+@pytest.mark.parametrize("at", [0, 1, 3])
+def test_masked_logits_under_large_entropy_gradients(vocab, at, dtype):
+    # a masked logit's gradient is 0 whatever h is: p is 0 there, and its factor has to stay finite
+    hs = [2.0, -5.0, 1e3, 65536.0, 1e6, -1e10, 1e20, 0.3]
+    gen = torch.Generator().manual_seed(vocab + at)
+    wide = torch.randn(2 * len(hs), vocab + 8, generator=gen) * 2.5
+    x = wide.to(dtype).to(DEV)[:, at:at + vocab]
+    for r in range(len(x)):
+        mask = -INF if r % 2 else torch.finfo(dtype).min
+        x[r, r % 3::3] = mask
+        x[r, vocab // 4:vocab // 2] = mask
+        if r in (4, 5):
+            x[r, 9:] = mask
+    h = torch.tensor([v for v in hs for _ in range(2)], device=DEV)
+    g = torch.full((len(x),), -0.5, device=DEV)
+    tokens = (torch.arange(len(x), device=DEV) * 5 + 1) % vocab
+    tokens[3] = -1
+    lse, lo, H = statistics(x)
+    out = torch.empty_like(wide, dtype=dtype, device=DEV)[:, at:at + vocab]
+    B.token_logprobs_backward(x, tokens, lse, H, g, h, lse_lo=lo, out=out)
+    want, tol = gradient(x, tokens, g, h)
+    assert ((out.double() - want).abs() <= tol).all()
+    assert torch.equal(out, B.token_logprobs_backward(x, tokens, lse, H, g, h, lse_lo=lo, out=x))
