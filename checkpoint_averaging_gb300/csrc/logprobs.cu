@@ -1199,6 +1199,9 @@ constexpr int kLbThreads = 256;
 constexpr int kLbBatch = 4;   // vectors per thread in flight
 constexpr int kLbBlocks = 5;  // blocks per SM that rows are cut for
 constexpr float kOutOfReach = 200.0f;  // (exp(-200) < 2^-149)
+// Rows whose |lse| is less go by the fma below: what rounding lse log2(e) leaves out is at most 1,
+// and so is lse_lo. 2^it is a factor of their gradients, out of range from |lse| of about 2^31 on.
+constexpr float kLbNear = 16777216.0f;
 
 struct LogprobGradArgs {
     const void* logits;
@@ -1306,7 +1309,7 @@ __global__ void __launch_bounds__(kLbThreads)
         const float d = fmaxf((v - r.lse) - r.lse_lo, -kOutOfReach);
         return -ex2(d * kLog2e) * fmaf(r.h, d + r.H, g);
     };
-    if (!zeros && !nans && fabsf(r.lse) < kHuge) {
+    if (!zeros && !nans && fabsf(r.lse) < kLbNear) {
         const float base = -r.lse * kLog2e;
         const float off = fmaf(-r.lse, kLog2e, -base) - r.lse_lo * kLog2e;
         const float f = ex2(off);

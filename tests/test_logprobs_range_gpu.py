@@ -85,3 +85,33 @@ def test_masked_logits_under_large_entropy_gradients(vocab, at, dtype):
     want, tol = gradient(x, tokens, g, h)
     assert ((out.double() - want).abs() <= tol).all()
     assert torch.equal(out, B.token_logprobs_backward(x, tokens, lse, H, g, h, lse_lo=lo, out=x))
+
+
+FAR = [1e6, 1.6e7, 2e7, 1e9, 3e9, 1e10, 1e11, 1e12, 1e15, 1e25, 1e30, 9e35, 1e37]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("vocab", [300, 9000, 50304])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_gradient_of_rows_far_from_0(vocab, sign, dtype):
+    # a row of equal logits (a mask of a finite value left nothing else), two tied logits above the
+    # rest, masks beside them, and rows where such a value masks all but a few
+    gen = torch.Generator().manual_seed(vocab)
+    x = (torch.randn(5 * len(FAR), vocab, generator=gen) * 2.5).to(dtype).to(DEV)
+    for i, c in enumerate(FAR):
+        c = torch.tensor(sign * c).to(dtype).item()
+        x[5 * i] = c
+        x[5 * i + 1] = min(2 * c, c / 2)
+        x[5 * i + 1, 5::vocab // 2] = c
+        x[5 * i + 2] = c
+        x[5 * i + 2, 1::2] = -INF
+        x[5 * i + 3, 20:] = -abs(c)
+        x[5 * i + 4, ::2] = -abs(c)
+    g = torch.linspace(-1, 1, len(x)).to(DEV)
+    h = torch.linspace(0.5, -3, len(x)).to(DEV)
+    tokens = (torch.arange(len(x), device=DEV) * 7 + 5) % vocab
+    tokens[::6] = -1
+    lse, lo, H = statistics(x)
+    got = B.token_logprobs_backward(x, tokens, lse, H, g, h, lse_lo=lo)
+    want, tol = gradient(x, tokens, g, h)
+    assert ((got.double() - want).abs() <= tol).all()
