@@ -66,8 +66,13 @@ constexpr int kLpMaxCluster = 8;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kInf = INFINITY;
-// Logits beyond this are summed with care, by one warp; below its negative they are masks.
+// Rows with logits beyond this are summed with care, relative to their largest.
 constexpr float kHuge = 1e36f;
+// The streaming form's: a term's exponent is x log2(e) less the reference's rounded product, so
+// even of x = reference it is what that rounding left out, up to 64 here and 2^7 from 2^31 on.
+// Rows whose largest logit lies beyond are summed by one warp; below its negative logits are masks,
+// which need no reference (exp of their distance from any other row's largest is 0).
+constexpr float kFar = 1073741824.0f;
 
 struct LogprobArgs {
     const void* logits;
@@ -592,7 +597,7 @@ __device__ __noinline__ void select(const LogprobArgs& a, LogprobShared& sh, con
 }
 
 // A share summed by one warp, its largest logit first: for rows with a NaN or
-// logits beyond kHuge.
+// logits beyond kFar.
 template <typename T>
 __device__ __noinline__ Share careful(const LogprobArgs& a, const RowPlan<T>& row, int rank) {
     constexpr int kN = Vec16<T>::kN;
@@ -664,11 +669,11 @@ __device__ __noinline__ void select_rows(const LogprobArgs& a, LogprobShared& sh
         s.t = warp_sum(f * (ws.t + ws.top_t + d * (ws.s + ws.top_s)) + one * one_y) * kLn2;
         bool bad = false;
         if (!(s.r < 1.5f) || s.m == -kInf) {
-            // (a sum that lost its row: a NaN, logits beyond kHuge either way)
-            bad = s.r != s.r || fabsf(s.m) >= kHuge;
+            // (a sum that lost its row: a NaN, logits beyond kFar either way)
+            bad = s.r != s.r || fabsf(s.m) >= kFar;
             if (bad && !(s.m == -kInf && s.r == 0.0f)) s = careful<T>(a, row, rank);
             bad = s.r != s.r;
-        } else if (fabsf(s.m) >= kHuge) {
+        } else if (fabsf(s.m) >= kFar) {
             s = careful<T>(a, row, rank);
             bad = s.r != s.r;
         } else {
@@ -812,8 +817,8 @@ __global__ void __launch_bounds__(kLpMaxBlock, 2)
         };
 
         const Pair log2e = pair(kLog2e, kLog2e);
-        float m = -kInf, limit = -kHuge, ref = 0.0f;  // ref: minus the reference times log2(e)
-        float unit_m = -kInf;                         // the largest of the unit under way
+        float m = -kInf, limit = -kFar, ref = 0.0f;  // ref: minus the reference times log2(e)
+        float unit_m = -kInf;                        // the largest of the unit under way
         const int unit_batches = a.unit / kLpBatch;
         int unit_left = unit_batches;
         float* unit_max = reinterpret_cast<float*>(&sh + 1) + tid * kLpUnits;
@@ -822,11 +827,11 @@ __global__ void __launch_bounds__(kLpMaxBlock, 2)
         auto add = [&](const Batch& v, int w, int n_vec) {
             const float big = Vec16<T>::largest_nan(v);
             if (!(big <= limit)) {
-                if (big < kHuge) {
+                if (big < kFar) {
                     const float up = -big * kLog2e, by = up - ref;
-                    const float f = limit == -kHuge ? 0.0f : ex2(by);
+                    const float f = limit == -kFar ? 0.0f : ex2(by);
                     s2 = mul2(s2, pair(f, f));
-                    t2 = limit == -kHuge ? t2 : fma2(t2, pair(f, f), mul2(s2, pair(by, by)));
+                    t2 = limit == -kFar ? t2 : fma2(t2, pair(f, f), mul2(s2, pair(by, by)));
                     ref = up;
                     limit = big + 16.0f;
                 } else {  // NaN, or too large
@@ -888,7 +893,7 @@ __global__ void __launch_bounds__(kLpMaxBlock, 2)
             if (lane == top_lane)
                 sh.warps[buf][warp] = WarpSums{wm, rest_s, rest_t, top_s, top_t, top_lane};
             bar_arrive(kBarFull + buf, both);
-            m = -kInf, limit = -kHuge, ref = 0.0f;
+            m = -kInf, limit = -kFar, ref = 0.0f;
             s2 = t2 = pair(0.0f, 0.0f);
             // the next row's buffer
             unit_m = -kInf, unit_left = unit_batches;

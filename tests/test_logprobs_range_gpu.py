@@ -115,3 +115,65 @@ def test_gradient_of_rows_far_from_0(vocab, sign, dtype):
     got = B.token_logprobs_backward(x, tokens, lse, H, g, h, lse_lo=lo)
     want, tol = gradient(x, tokens, g, h)
     assert ((got.double() - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows,vocab,top", [
+    (170, 40000, 3), (1300, 33001, 0), (8, 73760, 12), (2, 300001, 5), (400, 9000, 4)])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_log_probabilities_far_from_0(rows, vocab, top, sign, dtype):
+    # rows of equal logits, a few tied ones above the rest, masks beside them, rows where such a
+    # value masks all but a few or a run of the vocabulary, and one logit far above ordinary ones;
+    # in sizes that stream, that a cluster shares and that a block holds
+    gen = torch.Generator().manual_seed(vocab)
+    for first in range(0, 7 * len(FAR), rows):
+        x = (torch.randn(min(rows, 200), vocab, generator=gen) * 2.5).to(dtype).to(DEV)
+        if rows > 200:
+            x = x.repeat(-(-rows // 200), 1)[:rows]
+        for r in range(rows):
+            c, kind = FAR[(first + r) // 7 % len(FAR)], (first + r) % 7
+            c = torch.tensor(sign * c).to(dtype).item()
+            if kind == 0:
+                x[r] = c
+            elif kind == 1:
+                x[r] = min(2 * c, c / 2)
+                x[r, 5::vocab // 3] = c
+            elif kind == 2:
+                x[r] = c
+                x[r, 1::2] = -INF
+            elif kind == 3:
+                x[r, 20:] = -abs(c)
+            elif kind == 4:
+                x[r, vocab // 3:] = -abs(c)
+            elif kind == 5:
+                x[r] = c
+                x[r, vocab // 2] = c / 2 if c < 0 else c * 2
+            else:
+                x[r, vocab - 7] = abs(c)
+        tokens = (torch.arange(rows, device=DEV) * 7 + 5) % vocab
+        got = B.token_logprobs(x, tokens, top=top)
+        for at in range(0, rows, 100):
+            s = slice(at, min(rows, at + 100))
+            M, log_s, logp, p, H = distribution(x[s])
+            mine = logp.gather(1, tokens[s, None])[:, 0]
+            tol = 2e-5 + 2.0 ** -22 * mine.abs()
+            assert torch.equal(torch.isinf(got.logp[s]), torch.isinf(mine))
+            fine = torch.isfinite(mine)
+            assert ((got.logp[s].double() - mine).abs() <= tol)[fine].all()
+            lse = (M + log_s)[:, 0]
+            assert ((got.lse[s].double() - lse).abs() <= 2e-5 + 2.0 ** -23 * lse.abs()).all()
+            # lse and what it left out, together
+            both = (got.lse[s].double() - M[:, 0]) + got.lse_lo[s].double()
+            assert ((both - log_s[:, 0]).abs() <= 2e-5 + 2.0 ** -22 * log_s[:, 0]).all()
+            # a streamed row's terms have exponents of up to 64 in common, in sums of at most 200
+            # additions in a row: 64 * 200 * 2^-24 < 8e-4 on the entropy
+            assert ((got.entropy[s].double() - H[:, 0]).abs() <= 8e-4 + 2e-5 * H[:, 0]).all()
+            if top:
+                ids = torch.sort(x[s].double(), dim=1, descending=True, stable=True).indices[:, :top]
+                assert torch.equal(got.top_ids[s], ids)
+                best = logp.gather(1, ids)
+                ok = torch.isfinite(best)
+                off = (got.top_logp[s].double() - best).abs() - (2e-5 + 2.0 ** -22 * best.abs())
+                assert torch.equal(ok, torch.isfinite(got.top_logp[s])) and (off[ok] <= 0).all()
+        if rows >= 7 * len(FAR):
+            break
