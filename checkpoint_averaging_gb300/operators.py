@@ -86,12 +86,26 @@ def _same_device(device: int, *tensors):
             raise ValueError("tensors must live on one CUDA device")
 
 
-def _on_stream(stream, tensors) -> int:
-    """The handle of a stream given explicitly; the tensors are recorded on it."""
-    if not _b._capturing(stream):
-        _b._record_streams([t for t in tensors if t is not None], stream,
-                           int(stream.cuda_stream))
-    return int(stream.cuda_stream)
+def _on_stream(stream, device: int, call, args, results=lambda result: (result,)):
+    """What `call` returns, called with `stream` as the current stream: a block of the
+    caller's stream may still be in use by work queued there, which `stream` does not wait
+    for, so results are allocated under the stream that writes them. `args` are recorded
+    on `stream`, the tensors of `results(call's result)` that are not among them on the
+    caller's stream, where they are used and let go of."""
+    if stream.device.index != device:
+        raise ValueError("stream must be one of the tensors' device")
+    args = [t for t in args if t is not None]
+    caller = torch.cuda.current_stream(device)
+    recorded = not _b._capturing(stream)
+    if recorded:
+        _b._record_streams(args, stream, int(stream.cuda_stream))
+    with torch.cuda.stream(stream):
+        result = call()
+    if recorded and caller.cuda_stream != stream.cuda_stream:
+        _b._record_streams([t for t in results(result)
+                            if t is not None and not any(t is u for u in args)],
+                           caller, int(caller.cuda_stream))
+    return result
 
 
 def pack4_bytes(rows: int, cols: int, group: int = 64) -> int:
@@ -130,17 +144,19 @@ def pack4(weight, group: int = 64, *, stream=None) -> Packed4:
     published. `group` columns (32, 64 or 128) share a scale."""
     rows, cols, ld, code = _matrix(weight, "weight")
     device = weight.get_device()
+    if stream is not None:
+        return _on_stream(stream, device, lambda: pack4(weight, group), (weight,),
+                          lambda packed: (packed.data,))
     if device != _current_device():
         with torch.cuda.device(device):
-            return pack4(weight, group, stream=stream)
+            return pack4(weight, group)
     if group in (32, 64, 128):
         size = -(-rows // 16) * -(-cols // 128) * (1024 + 4096 // group)  # (cam_pack4_bytes)
     else:
         size = pack4_bytes(rows, cols, group)  # (refuses it)
     data = _empty(size, dtype=torch.uint8, device=weight.device)
     at = data.data_ptr()
-    handle = _current_stream(device) if stream is None else _on_stream(stream, (weight, data))
-    rc = _pack4(rows, cols, weight.data_ptr(), ld, code, group, at, handle)
+    rc = _pack4(rows, cols, weight.data_ptr(), ld, code, group, at, _current_stream(device))
     if rc:
         _failed(rc)
     return Packed4.__new__(Packed4)._set(data, rows, cols, group, at, device)
@@ -150,9 +166,12 @@ def unpack4(packed: Packed4, dtype=None, *, out=None, stream=None):
     """The values a 4-bit matrix stands for (cam_unpack4), as a new tensor of
     `dtype` (fp32 by default, or bf16) or into `out`."""
     device = packed._device
+    if stream is not None:
+        return _on_stream(stream, device, lambda: unpack4(packed, dtype, out=out),
+                          (packed.data, out))
     if device != _current_device():
         with torch.cuda.device(device):
-            return unpack4(packed, dtype, out=out, stream=stream)
+            return unpack4(packed, dtype, out=out)
     rows, cols = packed.rows, packed.cols
     if out is None:
         out = _empty((rows, cols), dtype=dtype or torch.float32, device=packed.data.device)
@@ -164,8 +183,8 @@ def unpack4(packed: Packed4, dtype=None, *, out=None, stream=None):
             raise ValueError("out must match the packed matrix")
         _, _, ld, code = _matrix(out, "out")
         _same_device(device, out)
-    handle = _current_stream(device) if stream is None else _on_stream(stream, (packed.data, out))
-    rc = _unpack4(rows, cols, packed._at, packed.group, out.data_ptr(), ld, code, handle)
+    rc = _unpack4(rows, cols, packed._at, packed.group, out.data_ptr(), ld, code,
+                  _current_stream(device))
     if rc:
         _failed(rc)
     return out
@@ -201,9 +220,13 @@ def gemv4(x, packed: Packed4, *, out=None, out_dtype=None, stream=None):
     device = x.get_device()
     if device != packed._device:
         raise ValueError("tensors must live on one CUDA device")
+    if stream is not None:
+        return _on_stream(stream, device,
+                          lambda: gemv4(x, packed, out=out, out_dtype=out_dtype),
+                          (x, packed.data, out))
     if device != _current_device():
         with torch.cuda.device(device):
-            return gemv4(x, packed, out=out, out_dtype=out_dtype, stream=stream)
+            return gemv4(x, packed, out=out, out_dtype=out_dtype)
     rows = packed.rows
     if out is None:
         y = _empty((tokens, rows), dtype=out_dtype or x.dtype, device=x.device)
@@ -217,10 +240,8 @@ def gemv4(x, packed: Packed4, *, out=None, out_dtype=None, stream=None):
             raise ValueError("out must match x and the matrix")
         _, _, ld_y, code_y = _matrix(y, "out")
         _same_device(device, y)
-    handle = _current_stream(device) if stream is None else \
-        _on_stream(stream, (x, packed.data, y))
     rc = _gemv4(tokens, rows, cols, x.data_ptr(), ld, code, packed._at, packed.group,
-                y.data_ptr(), ld_y, code_y, handle)
+                y.data_ptr(), ld_y, code_y, _current_stream(device))
     if rc:
         _failed(rc)
     return y
@@ -276,9 +297,12 @@ def token_logprobs(logits, tokens=None, *, top: int = 0, stream=None) -> TokenLo
         _same_device(device, tokens)
     if not 0 <= top <= LOGPROBS_MAX_TOP:
         raise ValueError(f"top must be in [0, {LOGPROBS_MAX_TOP}]")
+    if stream is not None:
+        return _on_stream(stream, device, lambda: token_logprobs(logits, tokens, top=top),
+                          (logits, tokens), lambda r: (r._stats, r.top_logp, r.top_ids))
     if device != _current_device():
         with torch.cuda.device(device):
-            return token_logprobs(logits, tokens, top=top, stream=stream)
+            return token_logprobs(logits, tokens, top=top)
     place = logits.device
     stats = _empty((4, rows), dtype=_FLOAT, device=place)  # logp, entropy, lse, lse_lo
     at = stats.data_ptr()
@@ -289,11 +313,9 @@ def token_logprobs(logits, tokens=None, *, top: int = 0, stream=None) -> TokenLo
         top_logp = _empty((rows, top), dtype=_FLOAT, device=place)
         top_ids = _empty((rows, top), dtype=_INT64, device=place)
         at_top, at_ids = top_logp.data_ptr(), top_ids.data_ptr()
-    handle = _current_stream(device) if stream is None else \
-        _on_stream(stream, (logits, tokens, stats, top_logp, top_ids))
     rc = _logprobs(rows, vocab, logits.data_ptr(), ld, code, at_token, top,
                    None if at_token is None else at, at + 4 * rows, at + 8 * rows, at + 12 * rows,
-                   at_top, at_ids, handle)
+                   at_top, at_ids, _current_stream(device))
     if rc:
         _failed(rc)
     return TokenLogprobs(stats, tokens is not None, top_logp, top_ids)
@@ -318,10 +340,16 @@ def token_logprobs_backward(logits, tokens, lse, entropy, grad_logp=None, grad_e
     are as token_logprobs returned them; either gradient may be None, not both."""
     rows, vocab, ld, code = _matrix(logits, "logits")
     device = logits.get_device()
+    if stream is not None:
+        return _on_stream(
+            stream, device,
+            lambda: token_logprobs_backward(logits, tokens, lse, entropy, grad_logp, grad_entropy,
+                                            lse_lo=lse_lo, out=out),
+            (logits, tokens, lse, lse_lo, entropy, grad_logp, grad_entropy, out))
     if device != _current_device():
         with torch.cuda.device(device):
             return token_logprobs_backward(logits, tokens, lse, entropy, grad_logp, grad_entropy,
-                                           lse_lo=lse_lo, out=out, stream=stream)
+                                           lse_lo=lse_lo, out=out)
     at_token = None
     if tokens is not None:
         _check_tokens(tokens, rows)
@@ -339,10 +367,9 @@ def token_logprobs_backward(logits, tokens, lse, entropy, grad_logp=None, grad_e
             raise ValueError("out must match logits")
         ld_out = _matrix(out, "out")[2]
         _same_device(device, out)
-    handle = _current_stream(device) if stream is None else \
-        _on_stream(stream, (logits, tokens, lse, lse_lo, entropy, grad_logp, grad_entropy, out))
     rc = _logprobs_backward(rows, vocab, logits.data_ptr(), ld, code, at_token, at_lse, at_lo,
-                            at_entropy, at_g, at_h, out.data_ptr(), ld_out, handle)
+                            at_entropy, at_g, at_h, out.data_ptr(), ld_out,
+                            _current_stream(device))
     if rc:
         _failed(rc)
     return out
