@@ -117,9 +117,11 @@ def pack4_bytes(rows: int, cols: int, group: int = 64) -> int:
 
 class Packed4:
     """A matrix in the 4-bit form (include/cam.h): ``data`` is its bytes (uint8,
-    1-D, on the GPU), which may be saved and made a Packed4 of again."""
+    1-D, on the GPU), which may be saved and made a Packed4 of again, as may the
+    Packed4 itself. The fields are read-only: the calls read as many bytes as
+    they say."""
 
-    __slots__ = ("data", "rows", "cols", "group", "_at", "_device", "_place")
+    __slots__ = ("_data", "_rows", "_cols", "_group", "_device", "_place")
 
     def __init__(self, data, rows: int, cols: int, group: int):
         if not data.is_cuda or data.dtype != torch.uint8 or not data.is_contiguous() \
@@ -127,16 +129,21 @@ class Packed4:
             raise ValueError("data must be a contiguous 16-byte aligned uint8 CUDA tensor")
         if data.numel() != pack4_bytes(rows, cols, group):
             raise ValueError(f"data must hold {pack4_bytes(rows, cols, group)} bytes")
-        self._set(data, rows, cols, group, data.data_ptr(), data.get_device())
+        self._set(data, rows, cols, group, data.get_device())
 
-    def _set(self, data, rows, cols, group, at, device):
-        self.data, self.rows, self.cols, self.group = data, rows, cols, group
-        self._at, self._device, self._place = at, device, data.device
+    def _set(self, data, rows, cols, group, device):
+        self._data, self._rows, self._cols, self._group = data, rows, cols, group
+        self._device, self._place = device, data.device
         return self
 
-    @property
-    def shape(self):
-        return (self.rows, self.cols)
+    data = property(lambda self: self._data)
+    rows = property(lambda self: self._rows)
+    cols = property(lambda self: self._cols)
+    group = property(lambda self: self._group)
+    shape = property(lambda self: (self._rows, self._cols))
+
+    def __reduce__(self):  # (copies and saved files: of the bytes they come with)
+        return Packed4, (self._data, self._rows, self._cols, self._group)
 
 
 def pack4(weight, group: int = 64, *, stream=None) -> Packed4:
@@ -155,11 +162,11 @@ def pack4(weight, group: int = 64, *, stream=None) -> Packed4:
     else:
         size = pack4_bytes(rows, cols, group)  # (refuses it)
     data = _empty(size, dtype=torch.uint8, device=weight.device)
-    at = data.data_ptr()
-    rc = _pack4(rows, cols, weight.data_ptr(), ld, code, group, at, _current_stream(device))
+    rc = _pack4(rows, cols, weight.data_ptr(), ld, code, group, data.data_ptr(),
+                _current_stream(device))
     if rc:
         _failed(rc)
-    return Packed4.__new__(Packed4)._set(data, rows, cols, group, at, device)
+    return Packed4.__new__(Packed4)._set(data, rows, cols, group, device)
 
 
 def unpack4(packed: Packed4, dtype=None, *, out=None, stream=None):
@@ -172,9 +179,9 @@ def unpack4(packed: Packed4, dtype=None, *, out=None, stream=None):
     if device != _current_device():
         with torch.cuda.device(device):
             return unpack4(packed, dtype, out=out)
-    rows, cols = packed.rows, packed.cols
+    rows, cols = packed._rows, packed._cols
     if out is None:
-        out = _empty((rows, cols), dtype=dtype or torch.float32, device=packed.data.device)
+        out = _empty((rows, cols), dtype=dtype or torch.float32, device=packed._place)
         ld, code = cols, _CODES.get(out.dtype)
         if code is None:
             _refuse(out, "values")
@@ -183,7 +190,7 @@ def unpack4(packed: Packed4, dtype=None, *, out=None, stream=None):
             raise ValueError("out must match the packed matrix")
         _, _, ld, code = _matrix(out, "out")
         _same_device(device, out)
-    rc = _unpack4(rows, cols, packed._at, packed.group, out.data_ptr(), ld, code,
+    rc = _unpack4(rows, cols, packed._data.data_ptr(), packed._group, out.data_ptr(), ld, code,
                   _current_stream(device))
     if rc:
         _failed(rc)
@@ -200,11 +207,11 @@ def gemv4(x, packed: Packed4, *, out=None, out_dtype=None, stream=None):
         if code is not None and len(shape) == 2 and x.get_device() == device == _current_device():
             tokens, cols = shape
             ld, step = x.stride()
-            if cols == packed.cols and step == 1 and ld >= cols:
-                rows = packed.rows
+            if cols == packed._cols and step == 1 and ld >= cols:
+                rows = packed._rows
                 y = _empty((tokens, rows), dtype=x.dtype, device=packed._place)
-                rc = _gemv4(tokens, rows, cols, x.data_ptr(), ld, code, packed._at, packed.group,
-                            y.data_ptr(), rows, code, _current_stream(device))
+                rc = _gemv4(tokens, rows, cols, x.data_ptr(), ld, code, packed._data.data_ptr(),
+                            packed._group, y.data_ptr(), rows, code, _current_stream(device))
                 if rc:
                     _failed(rc)
                 return y
@@ -215,8 +222,8 @@ def gemv4(x, packed: Packed4, *, out=None, out_dtype=None, stream=None):
             return out
         return gemv4(x.unsqueeze(0), packed, out_dtype=out_dtype, stream=stream)[0]
     tokens, cols, ld, code = _matrix(x, "x")
-    if cols != packed.cols:
-        raise ValueError(f"x has {cols} columns, the matrix {packed.cols}")
+    if cols != packed._cols:
+        raise ValueError(f"x has {cols} columns, the matrix {packed._cols}")
     device = x.get_device()
     if device != packed._device:
         raise ValueError("tensors must live on one CUDA device")
@@ -227,7 +234,7 @@ def gemv4(x, packed: Packed4, *, out=None, out_dtype=None, stream=None):
     if device != _current_device():
         with torch.cuda.device(device):
             return gemv4(x, packed, out=out, out_dtype=out_dtype)
-    rows = packed.rows
+    rows = packed._rows
     if out is None:
         y = _empty((tokens, rows), dtype=out_dtype or x.dtype, device=x.device)
         code_y = code if out_dtype is None else _CODES.get(out_dtype)
@@ -240,8 +247,8 @@ def gemv4(x, packed: Packed4, *, out=None, out_dtype=None, stream=None):
             raise ValueError("out must match x and the matrix")
         _, _, ld_y, code_y = _matrix(y, "out")
         _same_device(device, y)
-    rc = _gemv4(tokens, rows, cols, x.data_ptr(), ld, code, packed._at, packed.group,
-                y.data_ptr(), ld_y, code_y, _current_stream(device))
+    rc = _gemv4(tokens, rows, cols, x.data_ptr(), ld, code, packed._data.data_ptr(),
+                packed._group, y.data_ptr(), ld_y, code_y, _current_stream(device))
     if rc:
         _failed(rc)
     return y
