@@ -200,7 +200,11 @@ def unpack4(packed: Packed4, dtype=None, *, out=None, stream=None):
 def gemv4(x, packed: Packed4, *, out=None, out_dtype=None, stream=None):
     """x W^T for a 4-bit W and a few rows x (cam_gemv4): x is [cols] or
     [tokens, cols]; the result is [rows] or [tokens, rows] in x's dtype (or
-    `out_dtype`, or into `out`). For serving: no gradient."""
+    `out_dtype`, or into `out`). For serving: there is no gradient, and an x that
+    requires one is refused while gradients are recorded."""
+    if x.requires_grad and torch.is_grad_enabled():
+        raise ValueError("gemv4 has no gradient, and x requires one: detach it, or call under "
+                         "torch.no_grad()")
     if out is None and out_dtype is None and stream is None:
         # the call of a decoding step, with every check of the general one below
         code, shape, device = _CODES.get(x.dtype), x.shape, packed._device

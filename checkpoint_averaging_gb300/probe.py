@@ -59,7 +59,8 @@ class Probe(NamedTuple):
 
 def head_logits(hidden, head):
     """The logits of hidden states [rows, width]: `head` is a [vocab, width]
-    matrix, or its 4-bit form (Packed4) for the few rows of a decoding step."""
+    matrix, or its 4-bit form (Packed4) for the few rows of a decoding step,
+    through which no gradient flows (hidden states that require one are refused)."""
     if isinstance(head, B.Packed4):
         return B.gemv4(hidden, head)
     return hidden @ head.to(hidden.dtype).t()
