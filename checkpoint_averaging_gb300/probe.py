@@ -23,6 +23,20 @@ import torch
 from . import binding as B
 
 
+class _TokenLogprobsGrad(torch.autograd.Function):
+    """The gradient, as a step of the graph under create_graph=True, so that a second
+    derivative is refused. (once_differentiable would refuse it only where the gradients
+    that arrive require one: a loss linear in its log probabilities lost this term.)"""
+
+    @staticmethod
+    def forward(ctx, logits, tokens, lse, lse_lo, entropy, g, h):
+        return B.token_logprobs_backward(logits, tokens, lse, entropy, g, h, lse_lo=lse_lo)
+
+    @staticmethod
+    def backward(ctx, grad):
+        raise RuntimeError("token log probabilities have no second derivative")
+
+
 class _TokenLogprobs(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, tokens):
@@ -39,12 +53,13 @@ class _TokenLogprobs(torch.autograd.Function):
         # (the gradient of a sum or mean is one value expanded over the rows)
         g = None if grad_logp is None else grad_logp.contiguous()
         h = None if grad_entropy is None else grad_entropy.contiguous()
-        return B.token_logprobs_backward(logits, tokens, lse, entropy, g, h, lse_lo=lse_lo), None
+        return _TokenLogprobsGrad.apply(logits, tokens, lse, lse_lo, entropy, g, h), None
 
 
 def differentiable_logprobs(logits, tokens):
     """(log probabilities of the tokens, entropies) of rows of logits, for a loss:
-    gradients reach the logits through cam_token_logprobs_backward."""
+    gradients reach the logits through cam_token_logprobs_backward. A second
+    derivative is refused."""
     return _TokenLogprobs.apply(logits, tokens)
 
 

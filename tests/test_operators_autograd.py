@@ -79,3 +79,68 @@ def test_a_4_bit_head_refuses_hidden_states_that_require_a_gradient():
         got = P.probe(x, w4, tokens, top=3)
     assert torch.equal(got.logp, want.logp) and torch.equal(got.top_ids, want.top_ids)
     assert P.head_logits(x, w).requires_grad
+
+
+@pytest.fixture
+def plain_kernels(monkeypatch):
+    """The probe on the host: log probabilities and their gradient by torch, without a graph."""
+    from types import SimpleNamespace
+
+    from checkpoint_averaging_gb300 import probe as P
+
+    def forward(logits, tokens):
+        logp = torch.log_softmax(logits.detach(), 1)
+        lse = torch.logsumexp(logits.detach(), 1)
+        entropy = -(logp.exp() * logp).sum(1)
+        return SimpleNamespace(logp=logp.gather(1, tokens[:, None])[:, 0], entropy=entropy, lse=lse,
+                               lse_lo=torch.zeros_like(lse))
+
+    def backward(logits, tokens, lse, entropy, g, h, *, lse_lo):
+        with torch.no_grad():
+            logp = logits - lse[:, None]
+            p = logp.exp()
+            out = torch.zeros_like(p)
+            if g is not None:
+                out -= g[:, None] * p
+                out.scatter_add_(1, tokens[:, None], g[:, None])
+            if h is not None:
+                out -= h[:, None] * p * (logp + entropy[:, None])
+            return out
+
+    monkeypatch.setattr(P, "B", SimpleNamespace(token_logprobs=forward,
+                                                token_logprobs_backward=backward))
+
+
+def losses(logits, tokens, which):
+    from checkpoint_averaging_gb300 import probe as P
+
+    logp, entropy = P.differentiable_logprobs(logits, tokens)
+    return {"logp": -logp.mean(), "entropy": entropy.sum(), "both": -logp.mean() + 0.1 * entropy.sum(),
+            "square": (logp * logp).sum(), "other": -logp.mean() + (logits ** 3).sum()}[which]
+
+
+def second_derivatives_are_refused(which, device):
+    gen = torch.Generator().manual_seed(3)
+    logits = torch.randn(4, 11, generator=gen).to(device).requires_grad_(True)
+    tokens = torch.tensor([1, 5, 2, 9], device=device)
+    once, = torch.autograd.grad(losses(logits, tokens, which), logits)
+    assert not once.requires_grad
+    first, = torch.autograd.grad(losses(logits, tokens, which), logits, create_graph=True)
+    assert torch.equal(first.detach(), once)
+    with pytest.raises(RuntimeError, match="second derivative"):
+        torch.autograd.grad((first * first).sum(), logits)
+    with pytest.raises(RuntimeError, match="second derivative"):
+        (losses(logits, tokens, which) + torch.autograd.grad(
+            losses(logits, tokens, which), logits, create_graph=True)[0].norm()).backward()
+
+
+@pytest.mark.parametrize("which", ["logp", "entropy", "both", "square", "other"])
+def test_second_derivatives_are_refused(plain_kernels, which):
+    second_derivatives_are_refused(which, "cpu")
+
+
+@gpu
+@needs_gpu
+@pytest.mark.parametrize("which", ["logp", "entropy", "both", "square", "other"])
+def test_second_derivatives_are_refused_on_the_gpu(which):
+    second_derivatives_are_refused(which, "cuda")
