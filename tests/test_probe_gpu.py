@@ -70,3 +70,35 @@ def test_probe_takes_either_head():
     b = P.probe(x, packed, tokens, top=3)
     assert torch.equal(a.top_ids, b.top_ids)
     assert abs(float(a.loss) - float(b.loss)) < 1e-3
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows,vocab,width", [(9, 2000, 320), (1, 8192, 512), (40, 3001, 130)])
+def test_a_published_head_is_probed_as_its_values(rows, vocab, width, dtype):
+    gen = torch.Generator().manual_seed(vocab)
+    w = torch.randn(vocab, width, generator=gen) * 0.05
+    x = (torch.randn(rows, width, generator=gen) * 2).to(dtype).cuda()
+    tokens = torch.randint(0, vocab, (rows,), generator=gen).cuda()
+    tokens[-1] = -1 if rows > 1 else tokens[-1]
+    packed = B.pack4(w.cuda(), 64)
+    got = P.probe(x, packed, tokens, top=5)
+    value = B.unpack4(packed).double()
+    logits = x.double() @ value.t()
+    logp = torch.log_softmax(logits, 1)
+    entropy = -(logp.exp() * logp).sum(1)
+    # a product is off by (width / 32 + 96) 2^-22 sum |s q x| and 2^-8 of itself in bf16
+    # (test_pack4_gemv4_gpu.py), a log probability by twice its row's largest and by
+    # 2e-5 + 2^-22 of the largest logit (test_logprobs_gpu.py)
+    mag = x.double().abs() @ value.abs().t()
+    off = ((width / 32 + 96) * 2.0 ** -22 * mag).amax(1)
+    if dtype == torch.bfloat16:
+        off += 2.0 ** -8 * logits.abs().amax(1)
+    tol = 2 * off + 2e-5 + 2.0 ** -22 * logits.abs().amax(1)
+    known = tokens >= 0
+    mine = logp.gather(1, tokens.clamp(min=0)[:, None])[:, 0] * known
+    assert ((got.logp.double() - mine).abs() <= tol).all()
+    assert abs(float(got.loss) + float(mine.sum() / known.sum())) <= float(tol.max()) * 1.01
+    assert ((got.top_logp.double() - logp.gather(1, got.top_ids)).abs() <= tol[:, None]).all()
+    assert ((got.top_logp.double() - logp.topk(5, 1).values).abs() <= tol[:, None]).all()
+    # |dH| <= sum |dp| (|log p| + H) with |dp| <= 2 off p: at most 4 off H
+    assert (got.entropy.double() - entropy.mean()).abs() <= (tol + 4 * off * entropy + 2e-5 * entropy).max()
