@@ -486,8 +486,6 @@ __global__ void __launch_bounds__(kPkThreads, ALIGNED ? 4 : 5)
                     else if (c == -1)
                         at[0] = static_cast<uint16_t>(both);
                     before = __shfl_sync(0xFFFFFFFFu, both, 31);
-                    if (odd && i == 1 && lane == 31 && in_cols == kP4Cols)
-                        at[kP4Cols - 1] = static_cast<uint16_t>(both >> 16);
                 }
             }
         }
