@@ -17,10 +17,12 @@
 // A tcgen05 form (weights widened into tensor memory as the first operand, a
 // group's sums read back and scaled by warps of their own) was built and
 // measured over 73,760 x 2,048: 34.5 us for one bf16 token, 36 for 16, 45 for
-// 32 and 108 for 32 fp32 tokens, against 23, 31, 43 and 86 us of this form. Both
-// are bound by the instructions that widen the weights (188 executed per 2,048
-// of them here; the tensor cores 20 % busy at one token), which tcgen05 does
-// not save. One token's 22.6 us are 3.6 TB/s, 52 % of the copy rate.
+// 32 and 108 for 32 fp32 tokens, against 23, 31, 43 and 86 us of this form then.
+// One token's 22.5 us are 3.6 TB/s, 52 % of the copy rate. No unit is full: 61 %
+// of the issue slots are taken (188 instructions per 2,048 weights, 88 of them
+// to widen), the ALU pipe 52 %, the tensor cores 21 %, HBM 47 %, with 24 warps
+// per SM. What is left is latency that so many warps do not cover. 32 fp32
+// tokens take 84 us, the tensor cores 58 % busy.
 //
 // A block has a run of the matrix's 16-row tiles, a like share for every block,
 // and holds x in shared memory in the order of the operand. Its warps share out
@@ -212,7 +214,14 @@ struct GvForm {
     static constexpr int kWarps = NT <= 2 ? 8 : 16;
     static constexpr int kBlocks = NT == 1 ? 3 : NT == 2 ? 2 : 1;  // per SM
     static constexpr int kDepth = NT <= 2 ? 6 : 4;                 // ring slots per warp
-    // runs of x that a thread stages at once: more of them cost the fp32 forms their registers
+    // Runs of x that a thread stages at once. More loads in flight help long rows, more registers
+    // cost the loop. In us with 1 / 2 / 4 / 6 of them:
+    //   bf16  8 tokens  16,384 x 9,000 26.7 25.8 25.8 26.2  73,760 x 2,048 21.4 20.5 20.7 21.4
+    //        10         16,384 x 9,000 32.4 31.4 29.9 29.5  3,000 x 16,000 22.2 20.7 18.6 18.2
+    //        32         16,384 x 9,000 52.2 50.0 47.5 52.0  3,000 x 16,000 42.9 41.2 38.5 46.9
+    //   fp32  1         16,384 x 9,000 21.6 23.0 23.2 27.2  73,760 x 2,048 21.1 22.3 22.5 25.0
+    //         8         16,384 x 9,000 34.7 34.5 34.4 35.4  40,000 x 3,700 29.9 29.5 29.5 30.7
+    //        32         16,384 x 9,000 91.5 92.5 95.7 98.7  73,760 x 2,048 84.1 84.9 88.1 93.3
     static constexpr int kAhead = F32 ? (NT == 3 ? 2 : 1) : NT == 4 ? 4 : NT == 2 ? 6 : 2;
     static constexpr int kOut = F32 && NT > 1 ? NT / 3 : NT;       // operands of sums kept
     static constexpr int kTokens = F32 ? (NT == 1 ? 2 : 8 * NT / 3) : 8 * NT;

@@ -29,10 +29,11 @@
 // row; where rows are fewer than blocks, the blocks of a cluster share a row.
 // Rows short enough for the registers of one block take a form of their own
 // (token_logprobs_held), with M known before the sums.
-// Measured, 10 alternatives: 2,048 x 73,760 bf16 70 us (4.3 TB/s; 5.7 once
-// every block has 16 rows, the instructions of the exponentials and the
-// widening being the bound then), 4,096 x 50,257 fp32 139 us (5.9 TB/s, 6.7
-// in steady state: HBM).
+// Measured: 2,048 x 73,760 bf16 with 10 alternatives 69 us (4.4 TB/s, 5.7 for
+// each further row: 4,864 rows 140 us), 4,096 x 50,257 fp32 with one 138 us
+// (5.9 TB/s). In bf16 no unit is full even at 16 rows per block (55 % of the
+// issue slots, HBM 66 %, exponentials 27 %, ALU 35 %): the streaming warps, 22
+// per SM, wait for their loads; a launch's ramp and last selection are 9 us.
 //
 // Backward. One elementwise pass, read and written once, HBM-bound: 4,096 x
 // 73,760 bf16 with the entropy's term 182 us (6.6 TB/s).
@@ -1272,7 +1273,7 @@ __device__ __forceinline__ GradRow grad_row(const LogprobGradArgs& a, int64_t ro
 
 // A piece of a row for each TEAM threads of a block; a team has about a batch or
 // two of vectors per thread: 256 threads for a long row, 32 for the shortest
-// (8,192 x 2,001 bf16 18 us). Blocks that walk over many pieces, with the
+// (8,192 x 2,001 bf16 11 us). Blocks that walk over many pieces, with the
 // next piece's row values loaded ahead, measured 5 to 8 % slower. With
 // y = (x - lse) log2(e), every logit's gradient is
 //   -p (g + h (log p + H)) = 2^y (b + k y),  k = -h ln 2,  b = -(g + h H).

@@ -5,11 +5,11 @@
 // Both are streaming, HBM-bound: 4 B (fp32) or 2 B (bf16) per weight on one
 // side, 1/2 + 2 / group B on the other. One warp takes one tile of 16 rows x
 // 128 columns, its loads in flight before their first use; four blocks of
-// eight warps per SM (with two or three the bf16 pass takes 82 and 68 us, not
-// 64). Measured with 20,000 rows, group 32: 6,160 fp32 columns 89 us to pack
-// and 87 us to unpack (6.3 and 6.4 TB/s), bf16 64 us (4.9 TB/s: the scales' and
-// roundings' instructions) and 50 us (6.4 TB/s); rows without alignment (6,159
-// columns) 97 and 94 us in fp32, 114 and 84 us in bf16.
+// eight warps per SM (with two or three the bf16 pass took 82 and 68 us where
+// four took 64). Measured with 20,000 rows, group 32: 6,160 fp32 columns 85 us to
+// pack and to unpack (6.6 TB/s), bf16 61 us (5.1 TB/s: the scales' and roundings'
+// instructions) and 48 us (6.6 TB/s); rows without alignment (6,159 columns) 95
+// and 91 us in fp32, 85 and 82 us in bf16.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
