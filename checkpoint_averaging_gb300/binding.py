@@ -10,6 +10,7 @@ Every step of a merge runs in libcam's CUDA kernels; there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 import weakref
 from typing import Sequence
@@ -121,7 +122,11 @@ EXPORTS = ("cam_ctx_create", "cam_ctx_destroy", "cam_merge_begin", "cam_merge_ac
            "cam_ctx_get_quorum", "cam_ctx_set_quorum",
            "cam_merge_round_noalloc", "cam_last_error", "cam_version",
            "cam_pack4_bytes", "cam_pack4", "cam_unpack4", "cam_gemv4",
-           "cam_token_logprobs", "cam_token_logprobs_backward")
+           "cam_token_logprobs", "cam_token_logprobs_backward",
+           "cam_pack8_bytes", "cam_pack8", "cam_unpack8", "cam_matmul8_workspace", "cam_matmul8",
+           "cam_head_logprobs_workspace", "cam_head_logprobs",
+           "cam_head_logprobs_backward_workspace", "cam_head_logprobs_backward",
+           "cam_operators_status")
 
 LOGPROBS_MAX_TOP = 32
 
@@ -189,6 +194,21 @@ def lib() -> ctypes.CDLL:
                                      vp, vp]
     L.cam_token_logprobs_backward.argtypes = [i64, i64, vp, i64, ctypes.c_int, vp, vp, vp, vp, vp,
                                               vp, vp, i64, vp]
+    L.cam_pack8_bytes.argtypes = [i64, i64, ctypes.POINTER(i64)]
+    L.cam_pack8.argtypes = [i64, i64, vp, i64, ctypes.c_int, vp, vp]
+    L.cam_unpack8.argtypes = [i64, i64, vp, vp, i64, ctypes.c_int, vp]
+    L.cam_matmul8_workspace.argtypes = [i64, i64, i64, ctypes.POINTER(i64)]
+    L.cam_matmul8.argtypes = [i64, i64, i64, vp, i64, ctypes.c_int, vp, vp, i64, ctypes.c_int, vp,
+                              i64, vp]
+    L.cam_head_logprobs_workspace.argtypes = [i64, i64, i64, vp, i64, vp, i64, ctypes.c_int,
+                                              ctypes.POINTER(i64)]
+    L.cam_head_logprobs.argtypes = [i64, i64, i64, vp, i64, vp, i64, ctypes.c_int, vp, vp, vp, vp,
+                                    vp, vp, i64, vp]
+    L.cam_head_logprobs_backward_workspace.argtypes = [i64, i64, i64, vp, i64, ctypes.c_int,
+                                                       ctypes.POINTER(i64)]
+    L.cam_head_logprobs_backward.argtypes = [i64, i64, i64, vp, i64, vp, i64, ctypes.c_int, vp, vp,
+                                             vp, vp, vp, vp, vp, i64, vp, i64, vp, i64, vp]
+    L.cam_operators_status.argtypes = [ctypes.POINTER(i32)]
     L.cam_last_error.argtypes = []
     L.cam_last_error.restype = ctypes.c_char_p
     L.cam_version.argtypes = []
@@ -494,21 +514,23 @@ def _stream_handle(stream) -> int:
     return int(stream.cuda_stream)
 
 
-# ---- beside the merge: 4-bit publishing, its products, and the token probe -----------
+# ---- beside the merge: publishing, products, and the token probe -----------
 
-# The torch-facing calls live in operators.py, which needs torch at import;
+# The torch-facing calls live in operators.py and contexts.py, which need torch at import;
 # they are this module's too (binding.pack4, ...), looked up at first use.
-_OPERATORS = ("Packed4", "TokenLogprobs", "pack4", "pack4_bytes", "unpack4", "gemv4",
-              "token_logprobs", "token_logprobs_backward")
+_OPERATORS = {"operators": ("Packed4", "TokenLogprobs", "pack4", "pack4_bytes", "unpack4", "gemv4",
+                            "token_logprobs", "token_logprobs_backward"),
+              "contexts": ("Packed8", "pack8", "pack8_bytes", "unpack8", "matmul8",
+                           "head_logprobs", "head_logprobs_backward", "operators_status")}
 
 
 def __getattr__(name: str):
-    if name in _OPERATORS:
-        from . import operators
-
-        for n in _OPERATORS:
-            globals()[n] = getattr(operators, n)
-        return globals()[name]
+    for module, names in _OPERATORS.items():
+        if name in names:
+            found = importlib.import_module(f".{module}", __package__)
+            for n in names:
+                globals()[n] = getattr(found, n)
+            return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 

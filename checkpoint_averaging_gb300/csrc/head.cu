@@ -1,0 +1,615 @@
+// head.cu -- log probabilities of a head's tokens from hidden states, without the logits
+// (cam_head_logprobs), and the gradients of the hidden states and of the head
+// (cam_head_logprobs_backward).
+//
+// Forward: one product of hidden [R x D] and head [V x D] on the tensor cores
+// (tile_products.cu), whose epilogue reduces each tile of logits to a few numbers per row;
+// stats_kernel joins them. 2 R V D operations bound it, or reading the head for few rows.
+//
+// Backward, by pieces of the vocabulary: the logits again, with
+//
+//     G_j = g (1[j = token] - p_j) - h p_j (log p_j + H)
+//
+// as their tiles' epilogue, kept in bf16 terms for one piece; then, in one launch,
+// d head = G^T hidden of the piece and the piece's share of d hidden = G head (fp32
+// partials, joined in a fixed order by join_kernel). 6 R V D operations.
+//
+// fp32 matrices are taken as three bf16 terms each (24 bits: the whole significand) and
+// the six largest of the nine products of terms; what is left out is 2^-23 of
+// |hidden| |head| at most, where fp32 products round by 2^-24 each. bf16 matrices are one
+// term; their G is rounded to bf16 (2^-8 of each G_j at most: the bf16 gradients that hold
+// sums of them round by as much again).
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "cam_internal.h"
+#include "op_launch.h"
+#include "tile_products.h"
+
+#define CAM_API extern "C" __attribute__((visibility("default")))
+
+namespace cam {
+namespace {
+
+constexpr int kHeadThreads = 256;
+
+// ---- terms ------------------------------------------------------------------------------
+
+// The nearest bf16, but the largest one where that would be an infinity.
+__device__ __forceinline__ __nv_bfloat16 term(float x) {
+    __nv_bfloat16 h = __float2bfloat16_rn(x);
+    if ((__bfloat16_as_ushort(h) & 0x7FFFu) == 0x7F80u && isfinite(x)) h = __float2bfloat16_rz(x);
+    return h;
+}
+
+struct TermArgs {
+    const void* src;
+    int64_t stride, rows, cols;
+    __nv_bfloat16* out;  // [planes][rows][ld]
+    int64_t ld, plane_stride;
+    // rows without a gradient are taken as zeros (all three null: every row as it is)
+    const int64_t* tokens;
+    const float *g, *h;
+};
+
+// A matrix in one (bf16) or three (fp32) bf16 terms, eight columns per thread.
+template <typename T>
+__global__ void __launch_bounds__(kHeadThreads) terms_kernel(const TermArgs a) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    constexpr int kTerms = sizeof(T) == 4 ? 3 : 1;
+    const int64_t across = a.ld / 8, all = across * a.rows;
+    const T* src = static_cast<const T*>(a.src);
+    const bool vec = reinterpret_cast<uintptr_t>(src) % 16 == 0 && a.stride * sizeof(T) % 16 == 0;
+    for (int64_t i = int64_t(blockIdx.x) * kHeadThreads + threadIdx.x; i < all;
+         i += int64_t(gridDim.x) * kHeadThreads) {
+        const int64_t row = i / across, col = (i - row * across) * 8;
+        bool keep = true;
+        if (a.g || a.h)
+            keep = (a.g && a.tokens[row] >= 0 && a.g[row] != 0.0f) || (a.h && a.h[row] != 0.0f);
+        float v[8];
+        const T* at = src + row * a.stride + col;
+        if (keep && vec && col + 8 <= a.cols) {
+            if constexpr (sizeof(T) == 4) {
+                const float4 x = __ldg(reinterpret_cast<const float4*>(at));
+                const float4 y = __ldg(reinterpret_cast<const float4*>(at) + 1);
+                v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+                v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+            } else {
+                const uint4 x = __ldg(reinterpret_cast<const uint4*>(at));
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    v[2 * k] = __uint_as_float(w[k] << 16);
+                    v[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                v[k] = keep && col + k < a.cols ? static_cast<float>(at[k]) : 0.0f;
+        }
+#pragma unroll
+        for (int t = 0; t < kTerms; ++t) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const __nv_bfloat16 lo = term(v[2 * k]), hi = term(v[2 * k + 1]);
+                w[k] = __bfloat16_as_ushort(lo) | (uint32_t(__bfloat16_as_ushort(hi)) << 16);
+                v[2 * k] -= __bfloat162float(lo);
+                v[2 * k + 1] -= __bfloat162float(hi);
+            }
+            *reinterpret_cast<uint4*>(a.out + t * a.plane_stride + row * a.ld + col) =
+                make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+}
+
+// ---- joining ----------------------------------------------------------------------------
+
+struct StatArgs {
+    const TileStat* stats;  // [parts][rows]
+    int64_t parts, rows, vocab;
+    const float* mine;
+    const int64_t* tokens;
+    float *logp, *entropy, *lse, *lse_lo;
+};
+
+__device__ __forceinline__ void join(TileStat& s, const TileStat& o) {
+    if (o.a + o.c == 0.0f) return;  // (a thread without a part)
+    if (s.a + s.c == 0.0f) {
+        s = o;
+        return;
+    }
+    const bool mine = s.m >= o.m;
+    const TileStat hi = mine ? s : o, lo = mine ? o : s;
+    const float d = lo.m - hi.m;
+    if (d == 0.0f) {
+        s = TileStat{hi.m, hi.a + lo.a, hi.c + lo.c, hi.t + lo.t};
+    } else {
+        const float f = exp2f(d * 1.4426950408889634f), sum = lo.a + lo.c;
+        s = TileStat{hi.m, fmaf(f, sum, hi.a), hi.c, fmaf(f, fmaf(d, sum, lo.t), hi.t)};
+    }
+}
+
+// Eight rows per block, 32 threads each: their parts are one line of 128 bytes.
+__global__ void __launch_bounds__(kHeadThreads) stats_kernel(const StatArgs a) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    __shared__ TileStat all[32][8];
+    const int r = threadIdx.x & 7, y = threadIdx.x >> 3;
+    const int64_t row = int64_t(blockIdx.x) * 8 + r;
+    TileStat s{0.0f, 0.0f, 0.0f, 0.0f};
+    if (row < a.rows) {
+#pragma unroll 4
+        for (int64_t p = y; p < a.parts; p += 32) join(s, a.stats[p * a.rows + row]);
+    }
+    all[y][r] = s;
+    __syncthreads();
+    if (threadIdx.x >= 8 || row >= a.rows) return;
+#pragma unroll 1
+    for (int k = 1; k < 32; ++k) join(s, all[k][r]);
+    // log(a + c) from its small part where one token leads
+    const double sum = double(s.a) + double(s.c);
+    const double log_s = log1p(double(s.a) + (double(s.c) - 1.0));
+    const bool broken = isnan(s.t);
+    const float nan = __int_as_float(0x7FC00000);
+    const float top = static_cast<float>(double(s.m) + log_s);
+    if (a.lse) a.lse[row] = broken ? nan : top;
+    if (a.lse_lo)
+        a.lse_lo[row] = broken ? nan : static_cast<float>((double(s.m) - double(top)) + log_s);
+    if (a.entropy) a.entropy[row] = broken ? nan : static_cast<float>(log_s - double(s.t) / sum);
+    if (a.logp) {
+        const int64_t token = a.tokens[row];
+        float v = 0.0f;
+        if (token >= 0)
+            v = broken || token >= a.vocab
+                    ? nan
+                    : static_cast<float>((double(a.mine[row]) - double(s.m)) - log_s);
+        a.logp[row] = v;
+    }
+}
+
+struct JoinArgs {
+    const float* part;  // [splits][rows][ld]
+    int64_t rows, cols, ld;
+    int32_t splits;
+    void* out;
+    int64_t stride;
+};
+
+// Sums of partials in the order of their ranges, in eight runs: a block of 32 x 8 threads
+// takes 32 columns of a row.
+template <typename T>
+__global__ void __launch_bounds__(kHeadThreads) join_kernel(const JoinArgs a) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    __shared__ float runs[8][33];
+    const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+    const int64_t across = (a.cols + 31) / 32, tiles = across * a.rows;
+    for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+        const int64_t row = t / across, col = (t - row * across) * 32 + x;
+        const int32_t per = (a.splits + 7) / 8, s0 = y * per, s1 = min(a.splits, s0 + per);
+        float sum = 0.0f;
+        if (col < a.cols) {
+            const float* p = a.part + row * a.ld + col;
+#pragma unroll 4
+            for (int32_t s = s0; s < s1; ++s) sum += p[int64_t(s) * a.rows * a.ld];
+        }
+        runs[y][x] = sum;
+        __syncthreads();
+        if (y == 0 && col < a.cols) {
+#pragma unroll
+            for (int k = 1; k < 8; ++k) sum += runs[k][x];
+            static_cast<T*>(a.out)[row * a.stride + col] = T(sum);
+        }
+        __syncthreads();
+    }
+}
+
+// ---- host side --------------------------------------------------------------------------
+
+template <typename A>
+cudaError_t launch(void (*kernel)(A), int64_t blocks, const A& a, cudaStream_t s) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(std::max<int64_t>(1, blocks)));
+    cfg.blockDim = dim3(kHeadThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+struct Matrix {
+    const void* base;
+    int64_t rows, stride;
+};
+
+struct HeadCall {
+    int64_t rows, vocab, width;
+    Matrix hidden, head;
+    cam_dtype dtype;
+    int terms;       // 1 (bf16) or 3
+    int64_t ld;      // of a matrix in terms
+    bool x_direct, w_direct;  // read where they are
+    bool pair;
+};
+
+int64_t padded(int64_t bytes) { return (bytes + 511) / 512 * 512; }
+
+int check_head(const char* fn, HeadCall& c) {
+    if (c.rows < 0 || c.rows > (int64_t(1) << 24))
+        return record_error(CAM_E_ARG, "%s: rows out of range", fn);
+    if (c.vocab < 1 || c.vocab > CAM_LOGPROBS_MAX_VOCAB)
+        return record_error(CAM_E_ARG, "%s: vocab out of range", fn);
+    if (c.width < 1 || c.width > CAM_HEAD_MAX_WIDTH)
+        return record_error(CAM_E_ARG, "%s: width out of range", fn);
+    if (c.dtype != CAM_F32 && c.dtype != CAM_BF16)
+        return record_error(CAM_E_ARG, "%s: unknown dtype %d", fn, static_cast<int>(c.dtype));
+    const int64_t size = c.dtype == CAM_F32 ? 4 : 2;
+    if (c.rows > 0) {
+        for (const Matrix& m : {c.hidden, c.head}) {
+            if (!m.base) return record_error(CAM_E_ARG, "%s: a pointer is NULL", fn);
+            if (m.stride < c.width || m.stride > (int64_t(1) << 34))
+                return record_error(CAM_E_ARG, "%s: stride out of range", fn);
+            if (reinterpret_cast<uintptr_t>(m.base) % size != 0)
+                return record_error(CAM_E_ARG, "%s: an array is not aligned to its elements", fn);
+        }
+    }
+    c.terms = c.dtype == CAM_F32 ? 3 : 1;
+    c.ld = (c.width + 7) / 8 * 8;
+    // (the tensor maps want rows that start on 16 bytes)
+    auto direct = [&](const Matrix& m) {
+        return c.dtype == CAM_BF16 && reinterpret_cast<uintptr_t>(m.base) % 16 == 0 && m.stride % 8 == 0;
+    };
+    c.x_direct = direct(c.hidden);
+    c.w_direct = direct(c.head);
+    // a pair of SMs takes 256 rows, one SM 128
+    c.pair = c.rows > 128;
+    return CAM_OK;
+}
+
+// Bytes of a matrix in terms.
+int64_t term_bytes(const HeadCall& c, int64_t rows) { return padded(c.terms * rows * c.ld * 2); }
+
+TileOperand operand(const HeadCall& c, const Matrix& m, int64_t rows, bool direct, const void* terms,
+                    bool mn) {
+    TileOperand o{};
+    o.base = direct ? m.base : terms;
+    o.ld = direct ? m.stride : c.ld;
+    o.planes = direct ? 1 : c.terms;
+    o.plane_stride = rows * o.ld;
+    o.mn_major = mn;
+    o.rows = mn ? c.width : rows;
+    o.k = mn ? rows : c.width;
+    return o;
+}
+
+cudaError_t make_terms(const HeadCall& c, const Matrix& m, int64_t rows, void* out,
+                       const int64_t* tokens, const float* g, const float* h, int sms,
+                       cudaStream_t s) {
+    TermArgs a{m.base, m.stride, rows, c.width, static_cast<__nv_bfloat16*>(out), c.ld, rows * c.ld,
+               tokens, g, h};
+    const int64_t blocks = std::min<int64_t>((rows * (c.ld / 8) + kHeadThreads - 1) / kHeadThreads,
+                                             int64_t(sms) * 32);
+    return c.dtype == CAM_F32 ? launch(terms_kernel<float>, blocks, a, s)
+                              : launch(terms_kernel<__nv_bfloat16>, blocks, a, s);
+}
+
+Matrix piece_of(const HeadCall& c, int64_t at) {
+    const int64_t size = c.dtype == CAM_F32 ? 4 : 2;
+    return Matrix{static_cast<const char*>(c.head.base) + at * c.head.stride * size, c.vocab - at,
+                  c.head.stride};
+}
+
+// Equal pieces of the vocabulary, whole tiles of columns, within `budget` bytes of `per` each.
+int64_t piece_rows(const HeadCall& c, int64_t per, int64_t budget) {
+    if (per == 0) return c.vocab;
+    const int64_t most = std::max<int64_t>(kTileCols, budget / per / kTileCols * kTileCols);
+    const int64_t n = (c.vocab + most - 1) / most;
+    return ((c.vocab + n - 1) / n + kTileCols - 1) / kTileCols * kTileCols;
+}
+
+constexpr int64_t kForwardBudget = int64_t(1) << 29;   // a piece of the head in terms
+constexpr int64_t kBackwardBudget = int64_t(1) << 28;  // a piece of G, and of the head in terms
+
+struct ForwardPlan {
+    int64_t piece, x, w, stats, mine, bytes;  // offsets in the workspace
+};
+
+ForwardPlan forward_plan(const HeadCall& c) {
+    ForwardPlan p{};
+    p.piece = std::min(c.vocab, piece_rows(c, c.w_direct ? 0 : c.terms * c.ld * 2, kForwardBudget));
+    int64_t at = 0;
+    p.x = at;
+    if (!c.x_direct) at += term_bytes(c, c.rows);
+    p.w = at;
+    if (!c.w_direct) at += term_bytes(c, p.piece);
+    p.stats = at;
+    at += padded((c.vocab + 127) / 128 * c.rows * int64_t(sizeof(TileStat)));
+    p.mine = at;
+    at += padded(c.rows * 4);
+    p.bytes = at;
+    return p;
+}
+
+struct BackwardPlan {
+    int64_t piece, x, w, grad, hidden, head, bytes;
+    int32_t hidden_splits, head_splits;
+    int64_t part_ld;
+};
+
+// Ranges of K for a product of `tiles` tiles of `steps` steps: enough units for `want`,
+// none shorter than eight steps.
+int32_t splits_for(int64_t tiles, int64_t steps, int64_t want) {
+    const int64_t n = std::min((want + tiles - 1) / tiles, std::max<int64_t>(1, steps / 8));
+    const int64_t per = (steps + n - 1) / n;
+    return static_cast<int32_t>((steps + per - 1) / per);
+}
+
+BackwardPlan backward_plan(const HeadCall& c, int sms, bool want_hidden, bool want_head) {
+    BackwardPlan p{};
+    const int64_t per = c.terms * c.rows * 2 + (c.w_direct ? 0 : c.terms * c.ld * 2);
+    p.piece = piece_rows(c, per, kBackwardBudget);
+    const int64_t piece = std::min(p.piece, c.vocab);
+    const int64_t grid = c.pair ? sms / 2 : sms, tile = tile_rows(c.pair);
+    const int64_t across = (c.width + kTileCols - 1) / kTileCols, pairs = c.terms == 3 ? 6 : 1;
+    p.part_ld = c.ld;
+    p.hidden_splits = splits_for((c.rows + tile - 1) / tile * across, (piece + 63) / 64 * pairs, 2 * grid);
+    p.head_splits = splits_for((piece + tile - 1) / tile * across, (c.rows + 63) / 64 * pairs, grid);
+    int64_t at = 0;
+    p.x = at;
+    at += term_bytes(c, c.rows);
+    p.w = at;
+    if (!c.w_direct) at += term_bytes(c, piece);
+    p.grad = at;
+    at += padded(c.terms * c.rows * p.piece * 2);
+    p.hidden = at;
+    if (want_hidden && (p.hidden_splits > 1 || p.piece < c.vocab))
+        at += padded(p.hidden_splits * c.rows * p.part_ld * 4);
+    p.head = at;
+    if (want_head && p.head_splits > 1) at += padded(p.head_splits * piece * p.part_ld * 4);
+    p.bytes = at;
+    return p;
+}
+
+cudaError_t join_parts(const HeadCall& c, const float* part, int64_t rows, int32_t splits, void* out,
+                       int64_t stride, int sms, cudaStream_t s) {
+    JoinArgs a{part, rows, c.width, c.ld, splits, out, stride};
+    const int64_t blocks = std::min<int64_t>((c.width + 31) / 32 * rows, int64_t(sms) * 16);
+    return c.dtype == CAM_F32 ? launch(join_kernel<float>, blocks, a, s)
+                              : launch(join_kernel<__nv_bfloat16>, blocks, a, s);
+}
+
+int fail(const char* fn, cudaError_t ce) {
+    return record_error(CAM_E_CUDA, "%s: launch: %s", fn, cudaGetErrorString(ce));
+}
+
+int check_workspace(const char* fn, const void* ws, int64_t bytes, int64_t need) {
+    if (need > 0 && !ws) return record_error(CAM_E_ARG, "%s: workspace is NULL", fn);
+    if (reinterpret_cast<uintptr_t>(ws) % 256 != 0)
+        return record_error(CAM_E_ARG, "%s: workspace is not 256-byte aligned", fn);
+    if (bytes < need)
+        return record_error(CAM_E_ARG, "%s: workspace of %lld bytes, %lld needed", fn,
+                            static_cast<long long>(bytes), static_cast<long long>(need));
+    return CAM_OK;
+}
+
+int device_of(const char* fn, int* sms) {
+    int dev = 0;
+    const cudaError_t ce = current_device(&dev, sms);
+    return ce == cudaSuccess ? CAM_OK
+                             : record_error(CAM_E_CUDA, "%s: no usable CUDA device: %s", fn,
+                                            cudaGetErrorString(ce));
+}
+
+}  // namespace
+}  // namespace cam
+
+using cam::record_error;
+
+CAM_API int cam_head_logprobs_workspace(int64_t rows, int64_t vocab, int64_t width,
+                                        const void* hidden, int64_t hidden_stride, const void* head,
+                                        int64_t head_stride, cam_dtype dtype, int64_t* bytes) {
+    using namespace cam;
+    const char* fn = "cam_head_logprobs_workspace";
+    if (!bytes) return record_error(CAM_E_ARG, "%s: bytes is NULL", fn);
+    HeadCall c{rows, vocab, width, {hidden, rows, hidden_stride}, {head, vocab, head_stride}, dtype};
+    if (const int rc = check_head(fn, c)) return rc;
+    *bytes = rows ? forward_plan(c).bytes : 0;
+    return CAM_OK;
+}
+
+CAM_API int cam_head_logprobs(int64_t rows, int64_t vocab, int64_t width, const void* hidden,
+                              int64_t hidden_stride, const void* head, int64_t head_stride,
+                              cam_dtype dtype, const int64_t* tokens, float* logp, float* entropy,
+                              float* lse, float* lse_lo, void* workspace, int64_t workspace_bytes,
+                              void* stream) {
+    using namespace cam;
+    const char* fn = "cam_head_logprobs";
+    HeadCall c{rows, vocab, width, {hidden, rows, hidden_stride}, {head, vocab, head_stride}, dtype};
+    if (const int rc = check_head(fn, c)) return rc;
+    if ((tokens == nullptr) != (logp == nullptr) && rows > 0)
+        return record_error(CAM_E_ARG, "%s: tokens and logp go together", fn);
+    if (rows == 0) return CAM_OK;
+    const ForwardPlan p = forward_plan(c);
+    if (const int rc = check_workspace(fn, workspace, workspace_bytes, p.bytes)) return rc;
+    int sms = 0;
+    if (const int rc = device_of(fn, &sms)) return rc;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    char* ws = static_cast<char*>(workspace);
+    TileStat* stats = reinterpret_cast<TileStat*>(ws + p.stats);
+    float* mine = reinterpret_cast<float*>(ws + p.mine);
+    cudaError_t ce = cudaSuccess;
+    if (!c.x_direct)
+        ce = make_terms(c, c.hidden, rows, ws + p.x, nullptr, nullptr, nullptr, sms, s);
+    for (int64_t at = 0; at < vocab && ce == cudaSuccess; at += p.piece) {
+        const int64_t n = std::min(p.piece, vocab - at);
+        const Matrix piece = piece_of(c, at);
+        if (!c.w_direct) ce = make_terms(c, piece, n, ws + p.w, nullptr, nullptr, nullptr, sms, s);
+        if (ce != cudaSuccess) break;
+        TileProduct t{};
+        t.a = operand(c, c.hidden, rows, c.x_direct, ws + p.x, false);
+        t.b = operand(c, piece, n, c.w_direct, ws + p.w, false);
+        t.splits = 1;
+        t.out.stats = stats + at / 128 * rows;
+        t.out.mine = mine;
+        t.out.tokens = tokens;
+        t.out.token0 = at;
+        t.out.vocab = vocab;
+        if (const int rc = tile_products(fn, &t, 1, false, c.pair, kTileStats, sms, s)) return rc;
+    }
+    if (ce == cudaSuccess) {
+        StatArgs a{stats, (vocab + 127) / 128, rows, vocab, mine, tokens, logp, entropy, lse, lse_lo};
+        ce = launch(stats_kernel, (rows + 7) / 8, a, s);
+    }
+    return ce == cudaSuccess ? CAM_OK : fail(fn, ce);
+}
+
+CAM_API int cam_head_logprobs_backward_workspace(int64_t rows, int64_t vocab, int64_t width,
+                                                 const void* head, int64_t head_stride,
+                                                 cam_dtype dtype, int64_t* bytes) {
+    using namespace cam;
+    const char* fn = "cam_head_logprobs_backward_workspace";
+    if (!bytes) return record_error(CAM_E_ARG, "%s: bytes is NULL", fn);
+    HeadCall c{rows, vocab, width, {head, rows, width}, {head, vocab, head_stride}, dtype};
+    if (const int rc = check_head(fn, c)) return rc;
+    *bytes = 0;
+    if (rows == 0) return CAM_OK;
+    int sms = 0;
+    if (const int rc = device_of(fn, &sms)) return rc;
+    *bytes = backward_plan(c, sms, true, true).bytes;
+    return CAM_OK;
+}
+
+CAM_API int cam_head_logprobs_backward(int64_t rows, int64_t vocab, int64_t width,
+                                       const void* hidden, int64_t hidden_stride, const void* head,
+                                       int64_t head_stride, cam_dtype dtype, const int64_t* tokens,
+                                       const float* lse, const float* lse_lo, const float* entropy,
+                                       const float* grad_logp, const float* grad_entropy,
+                                       void* grad_hidden, int64_t grad_hidden_stride,
+                                       void* grad_head, int64_t grad_head_stride, void* workspace,
+                                       int64_t workspace_bytes, void* stream) {
+    using namespace cam;
+    const char* fn = "cam_head_logprobs_backward";
+    HeadCall c{rows, vocab, width, {hidden, rows, hidden_stride}, {head, vocab, head_stride}, dtype};
+    if (const int rc = check_head(fn, c)) return rc;
+    // (arrays of no rows may well be NULL)
+    if (rows > 0 && !grad_logp && !grad_entropy)
+        return record_error(CAM_E_ARG, "%s: grad_logp and grad_entropy are both NULL", fn);
+    if (rows > 0 && !grad_hidden && !grad_head)
+        return record_error(CAM_E_ARG, "%s: grad_hidden and grad_head are both NULL", fn);
+    const int64_t size = dtype == CAM_F32 ? 4 : 2;
+    const struct { void* p; int64_t stride; } out[2] = {{grad_hidden, grad_hidden_stride},
+                                                        {grad_head, grad_head_stride}};
+    for (const auto& o : out) {
+        if (!o.p) continue;
+        if (o.stride < width || o.stride > (int64_t(1) << 34))
+            return record_error(CAM_E_ARG, "%s: stride of a gradient out of range", fn);
+        if (reinterpret_cast<uintptr_t>(o.p) % size != 0)
+            return record_error(CAM_E_ARG, "%s: a gradient is not aligned to its elements", fn);
+        if (rows > 0 && (o.p == hidden || o.p == head))
+            return record_error(CAM_E_ARG, "%s: a gradient in the place of an input", fn);
+    }
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int sms = 0;
+    if (rows == 0) {  // a sum over no rows
+        if (!grad_head) return CAM_OK;
+        if (const int rc = device_of(fn, &sms)) return rc;
+        const cudaError_t ce = cudaMemset2DAsync(grad_head, grad_head_stride * size, 0, width * size,
+                                                 vocab, s);
+        return ce == cudaSuccess ? CAM_OK : fail(fn, ce);
+    }
+    if (grad_logp && !tokens) return record_error(CAM_E_ARG, "%s: grad_logp without tokens", fn);
+    if (grad_entropy && !entropy)
+        return record_error(CAM_E_ARG, "%s: grad_entropy without entropy", fn);
+    if (!lse) return record_error(CAM_E_ARG, "%s: lse is NULL", fn);
+    if (!workspace) return record_error(CAM_E_ARG, "%s: workspace is NULL", fn);
+    if (const int rc = device_of(fn, &sms)) return rc;
+    const BackwardPlan p = backward_plan(c, sms, grad_hidden != nullptr, grad_head != nullptr);
+    if (const int rc = check_workspace(fn, workspace, workspace_bytes, p.bytes)) return rc;
+    char* ws = static_cast<char*>(workspace);
+    // hidden states in terms, rows without a gradient as zeros: what they hold, NaN say, then
+    // reaches nothing
+    cudaError_t ce = make_terms(c, c.hidden, rows, ws + p.x, tokens, grad_logp, grad_entropy, sms, s);
+    const bool parts = p.hidden_splits > 1 || p.piece < vocab;
+    for (int64_t at = 0; at < vocab && ce == cudaSuccess; at += p.piece) {
+        const int64_t n = std::min(p.piece, vocab - at);
+        const Matrix piece = piece_of(c, at);
+        if (!c.w_direct) ce = make_terms(c, piece, n, ws + p.w, nullptr, nullptr, nullptr, sms, s);
+        if (ce != cudaSuccess) break;
+        TileProduct t{};
+        t.a = operand(c, c.hidden, rows, false, ws + p.x, false);
+        t.b = operand(c, piece, n, c.w_direct, ws + p.w, false);
+        t.splits = 1;
+        t.out.y = ws + p.grad;
+        t.out.ldy = p.piece;
+        t.out.planes = c.terms;
+        t.out.plane_stride = rows * p.piece;
+        t.out.tokens = tokens;
+        t.out.token0 = at;
+        t.out.vocab = vocab;
+        t.out.lse = lse;
+        t.out.lse_lo = lse_lo;
+        t.out.entropy = entropy;
+        t.out.g = grad_logp;
+        t.out.h = grad_entropy;
+        if (const int rc = tile_products(fn, &t, 1, false, c.pair, kTileGrad, sms, s)) return rc;
+
+        TileOperand grad{};
+        grad.base = ws + p.grad;
+        grad.ld = p.piece;
+        grad.planes = c.terms;
+        grad.plane_stride = rows * p.piece;
+        TileProduct both[2] = {};
+        int count = 0;
+        if (grad_hidden) {
+            TileProduct& q = both[count++];
+            q.a = grad;
+            q.a.rows = rows;
+            q.a.k = n;
+            q.b = operand(c, piece, n, c.w_direct, ws + p.w, true);
+            q.splits = p.hidden_splits;
+            if (parts) {
+                q.out.part = reinterpret_cast<float*>(ws + p.hidden);
+                q.out.part_ld = p.part_ld;
+                q.out.add = at > 0;
+            } else {
+                q.out.y = grad_hidden;
+                q.out.ldy = grad_hidden_stride;
+                q.out.y_bf16 = dtype == CAM_BF16;
+            }
+        }
+        if (grad_head) {
+            TileProduct& q = both[count++];
+            q.a = grad;
+            q.a.rows = n;
+            q.a.k = rows;
+            q.a.mn_major = true;
+            q.b = operand(c, c.hidden, rows, false, ws + p.x, true);
+            q.splits = p.head_splits;
+            if (p.head_splits > 1) {
+                q.out.part = reinterpret_cast<float*>(ws + p.head);
+                q.out.part_ld = p.part_ld;
+            } else {
+                q.out.y = static_cast<char*>(grad_head) + at * grad_head_stride * size;
+                q.out.ldy = grad_head_stride;
+                q.out.y_bf16 = dtype == CAM_BF16;
+            }
+        }
+        if (const int rc = tile_products(fn, both, count, false, c.pair, kTileOut, sms, s)) return rc;
+        if (grad_head && p.head_splits > 1)
+            ce = join_parts(c, reinterpret_cast<const float*>(ws + p.head), n, p.head_splits,
+                            static_cast<char*>(grad_head) + at * grad_head_stride * size,
+                            grad_head_stride, sms, s);
+    }
+    if (ce == cudaSuccess && grad_hidden && parts)
+        ce = join_parts(c, reinterpret_cast<const float*>(ws + p.hidden), rows, p.hidden_splits,
+                        grad_hidden, grad_hidden_stride, sms, s);
+    return ce == cudaSuccess ? CAM_OK : fail(fn, ce);
+}

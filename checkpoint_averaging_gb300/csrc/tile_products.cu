@@ -1,0 +1,825 @@
+// tile_products.cu -- the kernel behind tile_products.h.
+//
+// A persistent grid, one block per SM or one pair of blocks (a cluster of two) per pair of
+// SMs; unit u of the launch (a tile of one product, or one K range of it) goes to block
+// (pair) u, u + grid, ... Ten warps with fixed roles:
+//
+//   warp 0 (lane 0)  TMA producer: per K step of 128 bytes, this SM's 128 rows of A
+//                    and its share of B (the tile's columns, or half of them in a
+//                    pair) into a ring of shared-memory stages;
+//   warp 1 (lane 0)  MMA issuer (of a pair: the first block's): four tcgen05.mma
+//                    of 32 bytes of K per stage into one of two TMEM accumulators;
+//                    e4m3 operands' scales go from the stage into TMEM first
+//                    (tcgen05.cp) and are applied by the tensor core;
+//   warps 2..9       epilogue: TMEM lanes 32 (warp % 4) .. + 31, warps 2..5 the left
+//                    half of the columns and 6..9 the right one. A thread holds its half
+//                    of one row of the tile in registers.
+//
+// A pair of SMs works on one 256-row tile (cta_group::2): each stages its own rows of A
+// and half of B's columns, so an SM fetches 32 KB per 128 x 256 x 64 products
+// instead of 48.
+//
+// The tensor core adds to its accumulator without rounding to nearest: what is lost grows
+// with the number of additions and leans to zero. Where that would show in the result (fp32
+// results of long rows) the sum is cut into runs of K steps, each accumulated in TMEM and
+// added to the thread's registers in fp32.
+//
+// Every mbarrier wait is bounded; one that runs out sets CAM_STATUS_GEMM_TIMEOUT in the
+// library's status word (cam_operators_status) and an abort flag of the block. Every role
+// then leaves its loop, the producer waits (bounded) for its copies, the issuer for its
+// MMAs, and the TMEM is freed.
+#include "tile_products.h"
+
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <atomic>
+#include <climits>
+#include <cstring>
+
+#include "cam_internal.h"
+#include "op_launch.h"
+#include "tc_device.cuh"
+
+#define CAM_API extern "C" __attribute__((visibility("default")))
+
+namespace cam {
+namespace tc {
+namespace {
+
+__device__ int32_t g_operators_status;
+
+constexpr int kRows = 128;       // TMEM lanes: rows of an SM's tile
+constexpr int kThreads = 320;    // ten warps
+constexpr int kEpilogueWarps = 8;
+constexpr int kStepBytes = 128;  // bytes of K per stage
+constexpr int kMnBox = 64 * kStepBytes;  // MN-major box: 64 K rows of 64 elements
+constexpr int kRing = 222 * 1024;
+
+struct alignas(128) Prob {
+    CUtensorMap ta, tb;    // operands
+    CUtensorMap tsa, tsb;  // e4m3: their scales
+    int32_t m_tiles, n_tiles, m_fast;
+    int32_t steps;         // K steps of one pair of terms
+    int32_t all_steps, per_split;
+    int32_t main0, run;    // from step main0 on, accumulated in runs of `run` steps
+    int32_t a_mn, b_mn;
+    int32_t unit0;
+    uint8_t term_a[6], term_b[6];
+    int64_t M, N;
+    TileOut o;
+};
+
+struct alignas(128) Args {
+    Prob prob[2];
+    int32_t n_prob, n_units;
+};
+
+template <bool E4M3, bool PAIR>
+struct Geo {
+    static constexpr int kCols = E4M3 ? kTileCols8 : kTileCols;
+    static constexpr int kBCols = PAIR ? kCols / 2 : kCols;  // B rows an SM stages
+    static constexpr int kABytes = kRows * kStepBytes;
+    static constexpr int kBBytes = kBCols * kStepBytes;
+    static constexpr int kScaleA = E4M3 ? 512 : 0;   // one block of 128 rows
+    static constexpr int kScaleB = E4M3 ? 1024 : 0;  // two blocks cover 192 columns
+    static constexpr int kTx = kABytes + kBBytes + kScaleA + kScaleB;
+    static constexpr int kStage = (kTx + 1023) / 1024 * 1024;
+    static constexpr int kStages = kRing / kStage < 8 ? kRing / kStage : 8;
+    static constexpr int kBars = 2 * kStages + 5;
+    static constexpr int kSmem = kStages * kStage + 8 * kBars + 16 + 1024;
+    static_assert(kSmem <= kMaxSharedBytes, "over the per-block shared memory limit");
+};
+
+constexpr int kScaleColumn = 2 * kTileCols8;  // TMEM column of the scales
+
+// ---- what a pair of blocks adds to tc_device.cuh --------------------------------------
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address of the first block's copy of a shared variable.
+__device__ __forceinline__ uint32_t first_block(uint32_t addr) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+    return r;
+}
+__device__ __forceinline__ void bar_arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+                 : "memory");
+}
+
+// The load of a pair: `bar` may be the other block's.
+template <bool PAIR>
+__device__ __forceinline__ void load(uint32_t dst, const CUtensorMap* map, int x, int y, int z,
+                                     uint32_t bar) {
+    if constexpr (PAIR)
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+            ".cta_group::2 [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+            : "memory");
+    else
+        tma_load(dst, map, x, y, z, bar);
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void commit(uint32_t bar) {
+    if constexpr (PAIR)
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster"
+            ".multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+            "h"(static_cast<uint16_t>(3))
+            : "memory");
+    else
+        mma_commit(bar);
+}
+
+// Instruction descriptors: fp32 accumulator; bf16 operands (formats 1, majorness in bits
+// 15 and 16), or e4m3 operands (formats 0) with one UE8M0 scale per 32 elements of K (bit
+// 23), scale bytes 0 of their words. N / 8 in bits 17-22, M / 16 in bits 24-28.
+template <bool E4M3, bool PAIR>
+__device__ __forceinline__ uint32_t instruction(uint32_t a_mn, uint32_t b_mn) {
+    constexpr uint32_t n = Geo<E4M3, PAIR>::kCols >> 3, m = (PAIR ? 256 : 128) >> 4;
+    if constexpr (E4M3)
+        return (n << 17) | (1u << 23) | (m << 24);
+    else
+        return (1u << 4) | (1u << 7) | (1u << 10) | (a_mn << 15) | (b_mn << 16) | (n << 17) |
+               (m << 24);
+}
+
+template <bool E4M3, bool PAIR>
+__device__ __forceinline__ void multiply(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                         uint32_t accumulate, uint32_t sa, uint32_t sb) {
+    if constexpr (E4M3 && PAIR)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale [%0], %1, %2, %3, [%5], [%6], "
+            "p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(sa), "r"(sb)
+            : "memory");
+    else if constexpr (E4M3)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale [%0], %1, %2, %3, [%5], [%6], "
+            "p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(sa), "r"(sb)
+            : "memory");
+    else if constexpr (PAIR)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+            : "memory");
+    else
+        mma<true>(d, a, b, idesc, accumulate);
+}
+
+// 128 rows' scales (32 lanes of 16 bytes) into four TMEM columns, for every quarter of lanes.
+template <bool PAIR>
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t smem) {
+    // no swizzle, 8 x 16-byte core matrices 128 bytes apart
+    const uint64_t desc = static_cast<uint64_t>((smem & 0x3FFFFu) >> 4) | (uint64_t(8) << 16) |
+                          (uint64_t(8) << 32) | (uint64_t(1) << 46);
+    if constexpr (PAIR)
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+                     : "memory");
+    else
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+                     : "memory");
+}
+
+// 16 consecutive fp32 columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// ---- units -----------------------------------------------------------------------------
+
+struct Unit {
+    int p, mt, nt, split, s0, s1;
+};
+
+__device__ __forceinline__ Unit unit_of(const Args& a, int u) {
+    Unit t;
+    t.p = a.n_prob > 1 && u >= a.prob[1].unit0 ? 1 : 0;
+    const Prob& P = a.prob[t.p];
+    u -= P.unit0;
+    const int per = P.m_tiles * P.n_tiles;
+    t.split = u / per;
+    u -= t.split * per;
+    if (P.m_fast) {
+        t.nt = u / P.m_tiles;
+        t.mt = u - t.nt * P.m_tiles;
+    } else {
+        t.mt = u / P.n_tiles;
+        t.nt = u - t.mt * P.n_tiles;
+    }
+    t.s0 = t.split * P.per_split;
+    t.s1 = min(P.all_steps, t.s0 + P.per_split);
+    return t;
+}
+
+// The end of the run of K steps that starts with s.
+__device__ __forceinline__ int run_end(const Prob& P, int s, int s1) {
+    if (s < P.main0) return min(s1, P.main0);
+    return min(int64_t(s1), int64_t(s) + P.run - (s - P.main0) % P.run);
+}
+
+// ---- epilogues -------------------------------------------------------------------------
+
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Eight 32-bit words to a 32-byte aligned address.
+__device__ __forceinline__ void store8(void* p, const uint32_t* w) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
+// 32 columns of a row as bf16, `n` of them inside the matrix.
+__device__ __forceinline__ void store_bf16(__nv_bfloat16* y, const float* v, int n) {
+    if (n >= 32 && (reinterpret_cast<uintptr_t>(y) & 31) == 0) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            uint32_t w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = bf16x2(v[16 * k + 2 * i], v[16 * k + 2 * i + 1]);
+            store8(y + 16 * k, w);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (i < n) y[i] = __float2bfloat16_rn(v[i]);
+    }
+}
+
+__device__ __forceinline__ void store_f32(float* y, const float* v, int n) {
+    if (n >= 32 && (reinterpret_cast<uintptr_t>(y) & 31) == 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t w[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) w[k] = __float_as_uint(v[8 * i + k]);
+            store8(y + 8 * i, w);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (i < n) y[i] = v[i];
+    }
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// The element of 32 at a place known at run time.
+__device__ __forceinline__ float pick(const float* v, int64_t at) {
+    float x = v[0];
+#pragma unroll
+    for (int i = 1; i < 32; ++i) x = at == i ? v[i] : x;
+    return x;
+}
+
+// A row's statistics over a tile's columns, 32 at a time. The exponentials are relative to
+// the largest logit so far; those equal to it are counted, not summed, so that a row whose
+// leading token has nearly all the probability keeps the others' share to full precision.
+struct RowStat {
+    float m, a, c, t;
+    __device__ __forceinline__ void add(const float* v, int n, bool first) {
+        float top = v[0];
+#pragma unroll
+        for (int i = 1; i < 32; ++i) top = i < n ? fmaxf(top, v[i]) : top;
+        if (first) {
+            m = top;
+            a = c = t = 0.0f;
+        } else if (top > m) {
+            const float d = m - top, f = exp2_fast(d * kLog2e), s = a + c;
+            t = f * fmaf(d, s, t);
+            a = s * f;
+            c = 0.0f;
+            m = top;
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            if (i >= n) break;
+            const float d = v[i] - m;
+            const float e = exp2_fast(d * kLog2e);
+            // (NaN wherever a logit is NaN or infinite: through t)
+            t = fmaf(e, d, t);
+            if (d < 0.0f) a += e;
+            else c += 1.0f;
+        }
+    }
+};
+
+// ---- the kernel ------------------------------------------------------------------------
+
+template <bool E4M3, bool PAIR, int EPI>
+__global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant__ Args a) {
+    using G = Geo<E4M3, PAIR>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + G::kStages * G::kStage);
+    const uint32_t full0 = su32(bars);
+    const uint32_t empty0 = full0 + 8 * G::kStages;
+    const uint32_t tfull0 = empty0 + 8 * G::kStages;
+    const uint32_t tempty0 = tfull0 + 16;
+    const uint32_t drain = tempty0 + 16;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + G::kBars);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    int32_t* status = &g_operators_status;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = PAIR ? cluster_rank() : 0;
+    const int worker = PAIR ? int(blockIdx.x >> 1) : int(blockIdx.x);
+    const int workers = PAIR ? int(gridDim.x >> 1) : int(gridDim.x);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < G::kStages; ++s) {
+            bar_init(full0 + 8 * s, 1);
+            bar_init(empty0 + 8 * s, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            bar_init(tfull0 + 8 * i, 1);
+            bar_init(tempty0 + 8 * i, (PAIR ? 2 : 1) * kEpilogueWarps);
+        }
+        bar_init(drain, 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        if constexpr (PAIR) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                             su32(tmem_slot))
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                             su32(tmem_slot))
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if constexpr (PAIR) cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    // a programmatic dependent of the kernel before it: set-up overlapped that kernel's end
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    if (warp == 0 && lane == 0) {
+        // ---- producer ----
+        int stage = 0;
+        uint32_t phase = 0, issued = 0, filled_parity = 0;
+        bool ok = true;
+        for (int u = worker; u < a.n_units && ok; u += workers) {
+            const Unit t = unit_of(a, u);
+            const Prob& P = a.prob[t.p];
+            const int arow = (t.mt * (PAIR ? 2 : 1) + int(rank)) * kRows;
+            const int bcol = t.nt * G::kCols, brow = bcol + int(rank) * G::kBCols;
+            int pair = t.s0 / P.steps, ks = t.s0 - pair * P.steps;
+            for (int s = t.s0; s < t.s1; ++s) {
+                if (!bar_wait(empty0 + 8 * stage, phase ^ 1, abort_flag, status)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t sa = su32(smem + stage * G::kStage), sb = sa + G::kABytes;
+                uint32_t fb = full0 + 8 * stage;
+                if (rank == 0) bar_expect(fb, (PAIR ? 2 : 1) * G::kTx);
+                if constexpr (PAIR) fb = first_block(fb);
+                if constexpr (E4M3) {
+                    const int x = ks * kStepBytes;
+                    load<PAIR>(sa, &P.ta, x, arow, 0, fb);
+                    load<PAIR>(sb, &P.tb, x, brow, 0, fb);
+                    const uint32_t ss = sb + G::kBBytes;
+                    load<PAIR>(ss, &P.tsa, 0, arow / 128, ks, fb);
+                    load<PAIR>(ss + G::kScaleA, &P.tsb, 0, bcol / 128, ks, fb);
+                } else {
+                    const int x = ks * 64, za = P.term_a[pair], zb = P.term_b[pair];
+                    if (P.a_mn) {
+#pragma unroll
+                        for (int i = 0; i < kRows / 64; ++i)
+                            load<PAIR>(sa + i * kMnBox, &P.ta, arow + 64 * i, x, za, fb);
+                    } else {
+                        load<PAIR>(sa, &P.ta, x, arow, za, fb);
+                    }
+                    if (P.b_mn) {
+#pragma unroll
+                        for (int i = 0; i < G::kBCols / 64; ++i)
+                            load<PAIR>(sb + i * kMnBox, &P.tb, brow + 64 * i, x, zb, fb);
+                    } else {
+                        load<PAIR>(sb, &P.tb, x, brow, zb, fb);
+                    }
+                }
+                issued |= 1u << stage;
+                filled_parity = (filled_parity & ~(1u << stage)) | (phase << stage);
+                if (++stage == G::kStages) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+                if (++ks == P.steps) {
+                    ks = 0;
+                    ++pair;
+                }
+            }
+        }
+        if (*abort_flag && rank == 0) {  // let the copies in flight land
+            for (int s = 0; s < G::kStages; ++s)
+                if ((issued >> s) & 1) {
+                    const unsigned long long t0 = now_ns();
+                    while (!bar_test(full0 + 8 * s, (filled_parity >> s) & 1))
+                        if (now_ns() - t0 > kTcWaitLimitNs) break;
+                }
+        }
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+        // ---- MMA issuer ----
+        int stage = 0, acc = 0;
+        uint32_t phase = 0, acc_phase = 0;
+        uint32_t scale_at = 0;
+        bool ok = true;
+        for (int u = worker; u < a.n_units && ok; u += workers) {
+            const Unit t = unit_of(a, u);
+            const Prob& P = a.prob[t.p];
+            const uint32_t idesc = instruction<E4M3, PAIR>(P.a_mn, P.b_mn);
+            // 32 bytes further along a K-major row, or 16 rows further down an MN-major box
+            const uint32_t step_a = P.a_mn ? 16 * kStepBytes / 16 : 2;
+            const uint32_t step_b = P.b_mn ? 16 * kStepBytes / 16 : 2;
+            for (int s = t.s0; s < t.s1 && ok;) {
+                const int end = run_end(P, s, t.s1);
+                if (!bar_wait(tempty0 + 8 * acc, acc_phase ^ 1, abort_flag, status)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t d = tmem + uint32_t(acc * G::kCols);
+                uint32_t accumulate = 0;
+                for (; s < end; ++s) {
+                    if (!bar_wait(full0 + 8 * stage, phase, abort_flag, status)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sa = su32(smem + stage * G::kStage), sb = sa + G::kABytes;
+                    const uint64_t da = P.a_mn ? smem_desc_mn(sa, kMnBox) : smem_desc(sa);
+                    const uint64_t db = P.b_mn ? smem_desc_mn(sb, kMnBox) : smem_desc(sb);
+                    uint32_t ta = 0, tb = 0;
+                    if constexpr (E4M3) {
+                        // four columns of A's scales, eight of B's; a tile that starts in the
+                        // middle of a block of 128 starts two columns into them
+                        ta = tmem + kScaleColumn + scale_at;
+                        tb = ta + 4;
+                        const uint32_t ss = sb + G::kBBytes;
+                        copy_scales<PAIR>(ta, ss);
+                        copy_scales<PAIR>(tb, ss + 512);
+                        copy_scales<PAIR>(tb + 4, ss + 1024);
+                        tb += (t.nt & 1) ? 2 : 0;
+                        scale_at ^= 16;
+                    }
+#pragma unroll
+                    for (int k = 0; k < kStepBytes / 32; ++k) {
+                        multiply<E4M3, PAIR>(d, da + uint64_t(step_a * k), db + uint64_t(step_b * k),
+                                             idesc, accumulate, ta, tb);
+                        accumulate = 1;
+                    }
+                    commit<PAIR>(empty0 + 8 * stage);
+                    if (++stage == G::kStages) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+                if (!ok) break;
+                commit<PAIR>(tfull0 + 8 * acc);
+                if (++acc == 2) {
+                    acc = 0;
+                    acc_phase ^= 1;
+                }
+            }
+        }
+        if (*abort_flag) {  // every MMA issued so far completes before TMEM is freed
+            commit<PAIR>(drain);
+            const unsigned long long t0 = now_ns();
+            while (!bar_test(drain, 0))
+                if (now_ns() - t0 > kTcWaitLimitNs) break;
+        }
+    } else if (warp >= 2) {
+        // ---- epilogue ----
+        const int quarter = warp & 3, half = (warp - 2) >> 2;
+        constexpr int kHalf = G::kCols / 2, kGroups = kHalf / 32;
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        bool ok = true;
+        for (int u = worker; u < a.n_units && ok; u += workers) {
+            const Unit t = unit_of(a, u);
+            const Prob& P = a.prob[t.p];
+            const TileOut& o = P.o;
+            const int64_t row0 =
+                int64_t(t.mt * (PAIR ? 2 : 1) + int(rank)) * kRows + quarter * 32;
+            const int64_t row = row0 + lane;
+            const int64_t col0 = int64_t(t.nt) * G::kCols + half * kHalf;
+            const bool in = row < P.M;
+            // what a row brings, asked for before its tile is done
+            float lse = 0, lo = 0, H = 0, g = 0, h = 0;
+            int64_t token = -1;
+            if constexpr (EPI != kTileOut) {
+                if (in && o.tokens) token = __ldg(o.tokens + row);
+            }
+            bool skip = false;  // kTileGrad: a row without a gradient gets zeros
+            if constexpr (EPI == kTileGrad) {
+                if (in) {
+                    lse = __ldg(o.lse + row);
+                    if (o.lse_lo) lo = __ldg(o.lse_lo + row);
+                    if (o.g && token >= 0) g = __ldg(o.g + row);
+                    if (o.h) {
+                        h = __ldg(o.h + row);
+                        H = __ldg(o.entropy + row);
+                    }
+                }
+                skip = g == 0.0f && h == 0.0f;
+                // (a token that the vocabulary does not have)
+                if (g != 0.0f && token >= o.vocab) lse = __int_as_float(0x7FC00000);
+            }
+            if constexpr (EPI != kTileOut) token -= o.token0;  // its column in this product
+            const bool work = row0 < P.M && col0 < P.N;  // (of the warp)
+            // the thread's part of the row, summed over the runs of K
+            float sum[kHalf];
+            for (int s = t.s0; s < t.s1;) {
+                const bool first = s == t.s0;
+                s = run_end(P, s, t.s1);
+                ok = bar_wait(tfull0 + 8 * acc, acc_phase, abort_flag, status);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                if (work) {
+                    const uint32_t tbase = tmem + (uint32_t(quarter * 32) << 16) +
+                                           uint32_t(acc * G::kCols + half * kHalf);
+                    if (first) {
+#pragma unroll
+                        for (int c = 0; c < kGroups; ++c) tmem_ld32(tbase + uint32_t(c * 32), sum + 32 * c);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < kHalf / 16; ++c) {
+                            float v[16];
+                            tmem_ld16(tbase + uint32_t(c * 16), v);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) sum[16 * c + i] += v[i];
+                        }
+                    }
+                }
+                // the accumulator is free for the run after the next
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (PAIR) bar_arrive_cluster(first_block(tempty0 + 8 * acc));
+                    else bar_arrive(tempty0 + 8 * acc);
+                }
+                if (++acc == 2) {
+                    acc = 0;
+                    acc_phase ^= 1;
+                }
+            }
+            if (!ok) break;
+            if (!work) continue;
+            RowStat stat;
+            stat.m = stat.a = stat.c = stat.t = 0.0f;
+#pragma unroll
+            for (int c = 0; c < kGroups; ++c) {
+                const int64_t col = col0 + 32 * c;
+                if (col >= P.N) break;
+                float* v = sum + 32 * c;
+                const int n = P.N - col < 32 ? int(P.N - col) : 32;
+                if constexpr (EPI == kTileStats) {
+                    if (n == 32) stat.add(v, 32, c == 0);
+                    else stat.add(v, n, c == 0);
+                    const int64_t at = token - col;
+                    if (in && at >= 0 && at < n) o.mine[row] = pick(v, at);
+                } else if constexpr (EPI == kTileGrad) {
+                    const int64_t at = token - col;
+                    float hit = 0.0f;  // g (1 - p) of the row's token, without cancellation
+                    if (at >= 0 && at < n) hit = -g * expm1f((pick(v, at) - lse) - lo);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const float d = (v[i] - lse) - lo;
+                        const float p = exp2_fast(d * kLog2e);
+                        float w = at == i ? hit : -g * p;
+                        if (o.h) w -= h * p * (d + H);
+                        v[i] = skip ? 0.0f : w;
+                    }
+                    if (in) {
+                        __nv_bfloat16* y = static_cast<__nv_bfloat16*>(o.y) + row * o.ldy + col;
+                        for (int k = 0; k < o.planes; ++k) {
+                            store_bf16(y + k * o.plane_stride, v, n);
+                            if (k + 1 < o.planes) {
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    v[i] -= __bfloat162float(__float2bfloat16_rn(v[i]));
+                            }
+                        }
+                    }
+                } else {
+                    if (in) {
+                        if (o.part) {
+                            float* y = o.part + (int64_t(t.split) * P.M + row) * o.part_ld + col;
+                            if (o.add) {
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    if (i < n) v[i] += y[i];
+                            }
+                            store_f32(y, v, n);
+                        } else if (o.y_bf16) {
+                            store_bf16(static_cast<__nv_bfloat16*>(o.y) + row * o.ldy + col, v, n);
+                        } else {
+                            store_f32(static_cast<float*>(o.y) + row * o.ldy + col, v, n);
+                        }
+                    }
+                }
+            }
+            if constexpr (EPI == kTileStats) {
+                if (in)
+                    o.stats[(int64_t(t.nt) * 2 + half) * P.M + row] =
+                        TileStat{stat.m, stat.a, stat.c, stat.t};
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if constexpr (PAIR) cluster_sync();  // (nothing of the other block's is in flight here)
+    if (warp == 1) {
+        tc_fence_after();
+        if constexpr (PAIR)
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem)
+                         : "memory");
+        else
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem)
+                         : "memory");
+    }
+}
+
+// ---- host side --------------------------------------------------------------------------
+
+bool encode(CUtensorMap* map, CUtensorMapDataType type, const void* base, int64_t x, int64_t y,
+            int64_t z, int64_t y_bytes, int64_t z_bytes, int box_x, int box_y,
+            CUtensorMapSwizzle swizzle) {
+    const auto enc = encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {cuuint64_t(x), cuuint64_t(y), cuuint64_t(z)};
+    const cuuint64_t strides[2] = {cuuint64_t(y_bytes), cuuint64_t(z_bytes)};
+    const cuuint32_t box[3] = {cuuint32_t(box_x), cuuint32_t(box_y), 1};
+    const cuuint32_t unit[3] = {1, 1, 1};
+    return enc(map, type, 3, const_cast<void*>(base), dims, strides, box, unit,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// bf16 terms: boxes of 64 elements of K by `rows` rows, or MN-major of 64 rows by 64 of K.
+bool operand_map(CUtensorMap* map, const TileOperand& o, int rows) {
+    const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+    return o.mn_major
+               ? encode(map, bf, o.base, o.rows, o.k, o.planes, o.ld * 2, o.plane_stride * 2, 64, 64, sw)
+               : encode(map, bf, o.base, o.k, o.rows, o.planes, o.ld * 2, o.plane_stride * 2, 64, rows,
+                        sw);
+}
+
+// e4m3: boxes of 128 columns by `rows` rows; scales: blocks of 128 words.
+bool operand_map8(CUtensorMap* map, CUtensorMap* scales, const TileOperand& o, int rows, int blocks) {
+    const int64_t row_blocks = (o.rows + 127) / 128, col_blocks = (o.k + 127) / 128;
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, o.base, o.ld, o.rows, 1, o.ld, o.ld * o.rows,
+                  kStepBytes, rows, CU_TENSOR_MAP_SWIZZLE_128B) &&
+           encode(scales, CU_TENSOR_MAP_DATA_TYPE_UINT32, o.scales, 128, row_blocks, col_blocks, 512,
+                  512 * row_blocks, 128, blocks, CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+template <bool E4M3, bool PAIR, int EPI>
+cudaError_t launch(const Args& a, int sms, cudaStream_t s) {
+    using G = Geo<E4M3, PAIR>;
+    static std::atomic<uint64_t> allowed{0};
+    auto* kernel = tile_kernel<E4M3, PAIR, EPI>;
+    int dev = 0;
+    cudaError_t ce = cudaGetDevice(&dev);
+    if (ce == cudaSuccess) ce = allow_shared(reinterpret_cast<const void*>(kernel), dev, allowed);
+    if (ce != cudaSuccess) return ce;
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof cfg);
+    cfg.gridDim = dim3(PAIR ? 2 * std::min(a.n_units, sms / 2) : std::min(a.n_units, sms));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = G::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = PAIR ? 2 : 1;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = PAIR ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+template <bool PAIR>
+cudaError_t launch_any(const Args& a, bool e4m3, TileEpilogue epi, int sms, cudaStream_t s) {
+    if (e4m3) return epi == kTileOut ? launch<true, PAIR, kTileOut>(a, sms, s) : cudaErrorInvalidValue;
+    switch (epi) {
+        case kTileOut: return launch<false, PAIR, kTileOut>(a, sms, s);
+        case kTileStats: return launch<false, PAIR, kTileStats>(a, sms, s);
+        default: return launch<false, PAIR, kTileGrad>(a, sms, s);
+    }
+}
+
+}  // namespace
+}  // namespace tc
+
+int tile_products(const char* fn, const TileProduct* ps, int n, bool e4m3, bool pair,
+                  TileEpilogue epilogue, int sms, cudaStream_t stream) {
+    using namespace tc;
+    Args a;
+    std::memset(&a, 0, sizeof a);
+    const int cols = e4m3 ? kTileCols8 : kTileCols, rows = tile_rows(pair);
+    const int b_rows = pair ? cols / 2 : cols;
+    int32_t units = 0;
+    for (int i = 0; i < n; ++i) {
+        const TileProduct& p = ps[i];
+        Prob& P = a.prob[i];
+        const bool ok = e4m3 ? operand_map8(&P.ta, &P.tsa, p.a, kRows, 1) &&
+                                   operand_map8(&P.tb, &P.tsb, p.b, b_rows, 2)
+                             : operand_map(&P.ta, p.a, kRows) && operand_map(&P.tb, p.b, b_rows);
+        if (!ok) return record_error(CAM_E_CUDA, "%s: cuTensorMapEncodeTiled failed", fn);
+        P.M = p.a.rows;
+        P.N = p.b.rows;
+        P.m_tiles = static_cast<int32_t>((P.M + rows - 1) / rows);
+        P.n_tiles = static_cast<int32_t>((P.N + cols - 1) / cols);
+        // tiles that run at once share the longer side's operand
+        P.m_fast = P.m_tiles <= P.n_tiles;
+        P.a_mn = p.a.mn_major;
+        P.b_mn = p.b.mn_major;
+        // Pairs of terms, smallest products first: the sums of the small ones round at their
+        // own size. Of three terms each, those of 2^-24 and less of the whole are left out.
+        int pairs = 0;
+        for (int sum = std::min(2, p.a.planes + p.b.planes - 2); sum >= 0; --sum)
+            for (int k = 0; k <= sum; ++k)
+                if (k < p.a.planes && sum - k < p.b.planes) {
+                    P.term_a[pairs] = static_cast<uint8_t>(k);
+                    P.term_b[pairs++] = static_cast<uint8_t>(sum - k);
+                }
+        const int step = e4m3 ? 128 : 64;
+        P.steps = static_cast<int32_t>((p.a.k + step - 1) / step);
+        P.all_steps = P.steps * pairs;
+        // Runs of the leading products: fp32 inputs' of 256 terms, logits of bf16 ones of 512,
+        // e4m3 ones' of 2,048 (their steps add twice as many terms); bf16 results of bf16
+        // inputs hide what a long run loses.
+        P.main0 = P.steps * (pairs - 1);
+        P.run = pairs > 1 ? 4 : e4m3 ? 16 : epilogue == kTileStats ? 8 : INT_MAX;
+        const int splits = std::max(1, std::min(p.splits, P.all_steps));
+        P.per_split = (P.all_steps + splits - 1) / splits;
+        P.unit0 = units;
+        P.o = p.out;
+        units += P.m_tiles * P.n_tiles * ((P.all_steps + P.per_split - 1) / P.per_split);
+    }
+    a.n_prob = n;
+    a.n_units = units;
+    const cudaError_t ce = pair ? launch_any<true>(a, e4m3, epilogue, sms, stream)
+                                : launch_any<false>(a, e4m3, epilogue, sms, stream);
+    if (ce != cudaSuccess)
+        return record_error(CAM_E_CUDA, "%s: launch: %s", fn, cudaGetErrorString(ce));
+    return CAM_OK;
+}
+
+}  // namespace cam
+
+CAM_API int cam_operators_status(int32_t* out) {
+    const char* fn = "cam_operators_status";
+    if (!out) return cam::record_error(CAM_E_ARG, "%s: out is NULL", fn);
+    cudaError_t ce = cudaDeviceSynchronize();
+    if (ce == cudaSuccess) ce = cudaMemcpyFromSymbol(out, cam::tc::g_operators_status, sizeof *out);
+    if (ce != cudaSuccess)
+        return cam::record_error(CAM_E_CUDA, "%s: %s", fn, cudaGetErrorString(ce));
+    return CAM_OK;
+}

@@ -1,0 +1,79 @@
+// tile_products.h -- products of long rows on the fifth-generation tensor
+// cores with an epilogue of the caller's choice, for the operators beside the
+// merge: ragged extents, operands in one to three bf16 terms or in e4m3 with
+// scales, either majorness, products split along K.
+//
+//     D[i][j] = sum over term pairs (a, b), sum_k A_a[i][k] * B_b[j][k]
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace cam {
+
+// The terms of a matrix: planes of rows x k elements (k contiguous) or, MN-major, of
+// k x rows (rows contiguous). bf16 by default; e4m3 operands have one plane of
+// bytes and `scales` (see pack8_layout.h).
+struct TileOperand {
+    const void* base;
+    int64_t rows, k;
+    int64_t ld;            // elements between rows of the stored matrix (16-byte multiples)
+    int64_t plane_stride;  // elements between terms (16-byte multiple)
+    int32_t planes;
+    bool mn_major;
+    const void* scales;
+};
+
+enum TileEpilogue : int {
+    kTileOut = 0,    // D stored in fp32 or bf16, or added into fp32 partials
+    kTileStats = 1,  // softmax statistics of D's rows (logits)
+    kTileGrad = 2,   // the logits' gradient, in bf16 terms
+};
+
+// What kTileStats leaves of a row and half a tile of columns: the largest logit m,
+// the sum a of exp(x - m) over logits below it, the number c of logits equal to it, and
+// t = sum exp(x - m) (x - m).
+struct alignas(16) TileStat {
+    float m, a, c, t;
+};
+
+struct TileOut {
+    // kTileOut: y, or (part != null) fp32 partials, part[split][M][part_ld], written or,
+    // with `add`, added to
+    void* y;
+    int64_t ldy;
+    int32_t y_bf16;
+    int32_t add;
+    float* part;
+    int64_t part_ld;
+    // kTileStats: stats[tile of columns * 2 + half][M]; `mine` [M] takes the logit of each
+    // row's token. kTileGrad: G into `planes` terms of y (bf16, row stride ldy).
+    TileStat* stats;
+    float* mine;
+    const int64_t* tokens;
+    int64_t token0;  // the id of column 0
+    int64_t vocab;
+    const float *lse, *lse_lo, *entropy, *g, *h;
+    int32_t planes;
+    int64_t plane_stride;
+};
+
+struct TileProduct {
+    TileOperand a, b;
+    int32_t splits;  // kTileOut with partials: ranges of K
+    TileOut out;
+};
+
+constexpr int kTileCols = 256;   // columns of a bf16 tile
+constexpr int kTileCols8 = 192;  // of an e4m3 tile
+
+// Rows of a tile: a pair of SMs takes 256, one SM 128 (for few rows).
+inline int tile_rows(bool pair) { return pair ? 256 : 128; }
+
+// Enqueues n (1 or 2) products as one launch whose tiles share the SMs, the first's
+// first. Both take pairs of SMs or neither. Errors: CAM_E_CUDA.
+int tile_products(const char* fn, const TileProduct* p, int n, bool e4m3, bool pair,
+                  TileEpilogue epilogue, int sms, cudaStream_t stream);
+
+}  // namespace cam

@@ -798,6 +798,125 @@ int cam_token_logprobs_backward(int64_t rows, int64_t vocab, const void* logits,
                                 const float* grad_logp, const float* grad_entropy,
                                 void* grad_logits, int64_t grad_stride, void* stream);
 
+/*
+ * The 8-bit form of a row-major rows x cols matrix, for products with whole
+ * contexts on the tensor cores. Each row is cut into blocks of 128 columns,
+ * the last of them possibly short. Per block:
+ *
+ *   e = the least integer, -126 or more, with max|w| <= 448 * 2^e
+ *   q = w * 2^-e rounded to the nearest e4m3 number, ties to even (and held
+ *       to [-240, 240] where e is 120, so that q * 2^e stays finite)
+ *
+ * and the block stands for the values q * 2^e: the only rounding is that to
+ * e4m3 (at most 2^-4 of a value, or 2^-10 * 2^e for small ones). A block that
+ * holds a NaN or an infinity stands for NaN (every q a NaN). The bytes: rows
+ * of q, ceil(cols / 16) * 16 bytes each, q = 0 past the columns (NaN in a
+ * broken block); from the next multiple of 512 bytes on, the scales, as the tensor
+ * cores take them: for each block of columns and each 128 rows, 512 bytes,
+ * whose 32-bit word at byte 16 * (r % 32) + 4 * (r / 32) holds e + 127 of
+ * row r in each of its bytes.
+ */
+
+/* The bytes of the 8-bit form. rows >= 0, cols in [0, CAM_PACK4_MAX_COLS].
+ * Errors: CAM_E_ARG. */
+int cam_pack8_bytes(int64_t rows, int64_t cols, int64_t* out);
+
+/* Writes the 8-bit form of w (fp32 or bf16, `stride` >= cols) into packed
+ * (cam_pack8_bytes bytes, 16-byte aligned). Errors: CAM_E_ARG, CAM_E_CUDA. */
+int cam_pack8(int64_t rows, int64_t cols, const void* w, int64_t stride, cam_dtype dtype,
+              void* packed, void* stream);
+
+/* Writes the values q * 2^e that packed stands for, exact in fp32 and rounded
+ * to nearest-even in bf16 (where only values below 2^-126 round).
+ * Errors: CAM_E_ARG, CAM_E_CUDA. */
+int cam_unpack8(int64_t rows, int64_t cols, const void* packed, void* values, int64_t stride,
+                cam_dtype dtype, void* stream);
+
+/*
+ * y = x W^T for W (rows x cols) in the 8-bit form and `tokens` rows of x (fp32
+ * or bf16), which the call brings into the same form: y[m][n] is the sum of
+ * the products of both forms' values, exact each, in binary32 on the tensor
+ * cores; y (fp32 or bf16) is rounded once. An x[m] or a row of W with a
+ * broken block gives NaN. cols = 0 writes zeros. workspace: cam_matmul8_workspace
+ * bytes of device memory, 256-byte aligned, the call's own until it has run
+ * (calls in flight at once, or graphs that may be, need one each).
+ * Errors: CAM_E_ARG, CAM_E_CUDA.
+ */
+int cam_matmul8_workspace(int64_t tokens, int64_t rows, int64_t cols, int64_t* bytes);
+int cam_matmul8(int64_t tokens, int64_t rows, int64_t cols, const void* x, int64_t x_stride,
+                cam_dtype x_dtype, const void* packed, void* y, int64_t y_stride,
+                cam_dtype y_dtype, void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * What a head says of given tokens, from hidden states: cam_token_logprobs of
+ * the logits x = hidden head^T, for `rows` rows of hidden [rows][width] and a
+ * head [vocab][width] of the same dtype (fp32 or bf16), without storing the
+ * logits: they are products summed in binary32 on the tensor cores and stay in
+ * binary32. fp32 inputs are taken in three bf16 terms each (all 24 bits);
+ * of their products those below 2^-23 of |hidden||head| are left out. logp (with
+ * tokens), entropy, lse and lse_lo are as there; tokens and logp may both be
+ * NULL, the others each. There are no alternatives: ask cam_token_logprobs.
+ * A row with a logit that is NaN, infinite or beyond binary32 has NaN
+ * throughout. A negative token id is no token (logp 0); one of `vocab` or more
+ * gives a logp of NaN. vocab in [1, CAM_LOGPROBS_MAX_VOCAB], width in
+ * [1, CAM_HEAD_MAX_WIDTH]; strides count elements between the starts of rows.
+ * Matrices whose rows start on 16 bytes (bf16) are read where they are, others
+ * and fp32 ones through the workspace, in pieces of the vocabulary. workspace:
+ * cam_head_logprobs_workspace bytes (for the same arguments) of device memory,
+ * 256-byte aligned, the call's own until it has run.
+ * Errors: CAM_E_ARG, CAM_E_CUDA.
+ */
+#define CAM_HEAD_MAX_WIDTH (1 << 17)
+int cam_head_logprobs_workspace(int64_t rows, int64_t vocab, int64_t width, const void* hidden,
+                                int64_t hidden_stride, const void* head, int64_t head_stride,
+                                cam_dtype dtype, int64_t* bytes);
+int cam_head_logprobs(int64_t rows, int64_t vocab, int64_t width, const void* hidden,
+                      int64_t hidden_stride, const void* head, int64_t head_stride,
+                      cam_dtype dtype, const int64_t* tokens, float* logp, float* entropy,
+                      float* lse, float* lse_lo, void* workspace, int64_t workspace_bytes,
+                      void* stream);
+
+/*
+ * The gradients of cam_head_logprobs with respect to the hidden states and the
+ * head, for the gradients grad_logp (g) of logp and grad_entropy (h) of
+ * entropy, fp32 [rows]: with G the logits' gradient of
+ * cam_token_logprobs_backward,
+ *
+ *   grad_hidden = G head      grad_head = G^T hidden
+ *
+ * in the inputs' dtype, sums in binary32, rounded once. The logits are
+ * computed again, and G is held for one piece of the vocabulary at a time,
+ * in three bf16 terms for fp32 inputs and rounded to bf16 for bf16 ones.
+ * Either of grad_hidden and grad_head may be NULL, not both, and either of
+ * grad_logp (with tokens) and grad_entropy (with entropy). lse, lse_lo (may be
+ * NULL) and entropy are as cam_head_logprobs wrote them. A negative token id
+ * counts as g = 0. Rows whose g and h are 0 give and get nothing, whatever
+ * their hidden states hold; a row whose lse is NaN, or whose token id is `vocab`
+ * or more (with g other than 0), has a G of NaN, and with it every row of
+ * grad_head. rows = 0 writes zeros to grad_head. The gradients may not overlap
+ * the inputs. Results are the same bits from call to call.
+ * workspace: cam_head_logprobs_backward_workspace bytes, 256-byte aligned, the
+ * call's own until it has run. Errors: CAM_E_ARG, CAM_E_CUDA.
+ */
+int cam_head_logprobs_backward_workspace(int64_t rows, int64_t vocab, int64_t width,
+                                         const void* head, int64_t head_stride, cam_dtype dtype,
+                                         int64_t* bytes);
+int cam_head_logprobs_backward(int64_t rows, int64_t vocab, int64_t width, const void* hidden,
+                               int64_t hidden_stride, const void* head, int64_t head_stride,
+                               cam_dtype dtype, const int64_t* tokens, const float* lse,
+                               const float* lse_lo, const float* entropy, const float* grad_logp,
+                               const float* grad_entropy, void* grad_hidden,
+                               int64_t grad_hidden_stride, void* grad_head,
+                               int64_t grad_head_stride, void* workspace, int64_t workspace_bytes,
+                               void* stream);
+
+/* Waits for all work on the current device, then writes the status word of the
+ * calls above that need no context to *out: 0, or CAM_STATUS_GEMM_TIMEOUT once
+ * a tensor-core kernel of cam_matmul8, cam_head_logprobs or their gradients has
+ * given up waiting on a barrier (a fault of this library, never expected),
+ * whose results are then undefined. Errors: CAM_E_ARG, CAM_E_CUDA. */
+int cam_operators_status(int32_t* out);
+
 /* Message describing the calling thread's last error ("" if none). */
 const char* cam_last_error(void);
 
