@@ -17,12 +17,13 @@
 // fp32 matrices are taken as three bf16 terms each (24 bits: the whole significand) and
 // the six largest of the nine products of terms; what is left out is 2^-23 of
 // |hidden| |head| at most, where fp32 products round by 2^-24 each. bf16 matrices are one
-// term; their G is rounded to bf16 (2^-8 of each G_j at most: the bf16 gradients that hold
-// sums of them round by as much again).
+// term; their G is one bf16 term, too (2^-8 of each G_j at most: the bf16 gradients that hold
+// sums of them round by as much again), or two for few rows.
 #include <cuda_bf16.h>
 
 #include <algorithm>
 #include <cmath>
+#include <cstdint>
 
 #include "cam_internal.h"
 #include "op_launch.h"
@@ -235,6 +236,7 @@ struct HeadCall {
     Matrix hidden, head;
     cam_dtype dtype;
     int terms;       // 1 (bf16) or 3
+    int grad_terms;  // of G
     int64_t ld;      // of a matrix in terms
     bool x_direct, w_direct;  // read where they are
     bool pair;
@@ -269,6 +271,10 @@ int check_head(const char* fn, HeadCall& c) {
     };
     c.x_direct = direct(c.hidden);
     c.w_direct = direct(c.head);
+    // G of bf16 inputs: one term, whose rounding adds in squares to that of the results (0.0024
+    // of their norm off 64 bits where 0.0017 is their own), over many rows; the large entries of a
+    // few rows may round alike (0.0031 for 16), and a second term costs little there.
+    c.grad_terms = c.terms == 3 ? 3 : c.rows > 256 ? 1 : 2;
     // a pair of SMs takes 256 rows, one SM 128
     c.pair = c.rows > 128;
     return CAM_OK;
@@ -316,7 +322,7 @@ int64_t piece_rows(const HeadCall& c, int64_t per, int64_t budget) {
 }
 
 constexpr int64_t kForwardBudget = int64_t(1) << 29;   // a piece of the head in terms
-constexpr int64_t kBackwardBudget = int64_t(1) << 28;  // a piece of G, and of the head in terms
+constexpr int64_t kBackwardBudget = int64_t(1) << 29;  // a piece of G, and of the head in terms
 
 struct ForwardPlan {
     int64_t piece, x, w, stats, mine, bytes;  // offsets in the workspace
@@ -344,31 +350,36 @@ struct BackwardPlan {
     int64_t part_ld;
 };
 
-// Ranges of K for a product of `tiles` tiles of `steps` steps: enough units for `want`,
-// none shorter than eight steps.
-int32_t splits_for(int64_t tiles, int64_t steps, int64_t want) {
-    const int64_t n = std::min((want + tiles - 1) / tiles, std::max<int64_t>(1, steps / 8));
+// Ranges of K for a product of `tiles` tiles of `steps` steps: enough units for `want`, and
+// none longer than `most` steps, but none shorter than eight.
+int32_t splits_for(int64_t tiles, int64_t steps, int64_t want, int64_t most) {
+    const int64_t n = std::min(std::max((want + tiles - 1) / tiles, (steps + most - 1) / most),
+                               std::max<int64_t>(1, steps / 8));
     const int64_t per = (steps + n - 1) / n;
     return static_cast<int32_t>((steps + per - 1) / per);
 }
 
 BackwardPlan backward_plan(const HeadCall& c, int sms, bool want_hidden, bool want_head) {
     BackwardPlan p{};
-    const int64_t per = c.terms * c.rows * 2 + (c.w_direct ? 0 : c.terms * c.ld * 2);
+    const int64_t per = c.grad_terms * c.rows * 2 + (c.w_direct ? 0 : c.terms * c.ld * 2);
     p.piece = piece_rows(c, per, kBackwardBudget);
     const int64_t piece = std::min(p.piece, c.vocab);
     const int64_t grid = c.pair ? sms / 2 : sms, tile = tile_rows(c.pair);
-    const int64_t across = (c.width + kTileCols - 1) / kTileCols, pairs = c.terms == 3 ? 6 : 1;
+    const int64_t across = (c.width + kTileCols - 1) / kTileCols;
+    const int64_t pairs = c.terms == 3 ? 6 : c.grad_terms;
     p.part_ld = c.ld;
-    p.hidden_splits = splits_for((c.rows + tile - 1) / tile * across, (piece + 63) / 64 * pairs, 2 * grid);
-    p.head_splits = splits_for((piece + tile - 1) / tile * across, (c.rows + 63) / 64 * pairs, grid);
+    // both products share a launch: units of one length, so that its last round is full
+    const int64_t head_steps = (c.rows + 63) / 64 * pairs, hidden_steps = (piece + 63) / 64 * pairs;
+    p.head_splits = splits_for((piece + tile - 1) / tile * across, head_steps, grid, INT64_MAX);
+    p.hidden_splits = splits_for((c.rows + tile - 1) / tile * across, hidden_steps, 2 * grid,
+                                 std::max<int64_t>(64, head_steps));
     int64_t at = 0;
     p.x = at;
     at += term_bytes(c, c.rows);
     p.w = at;
     if (!c.w_direct) at += term_bytes(c, piece);
     p.grad = at;
-    at += padded(c.terms * c.rows * p.piece * 2);
+    at += padded(c.grad_terms * c.rows * p.piece * 2);
     p.hidden = at;
     if (want_hidden && (p.hidden_splits > 1 || p.piece < c.vocab))
         at += padded(p.hidden_splits * c.rows * p.part_ld * 4);
@@ -549,7 +560,7 @@ CAM_API int cam_head_logprobs_backward(int64_t rows, int64_t vocab, int64_t widt
         t.splits = 1;
         t.out.y = ws + p.grad;
         t.out.ldy = p.piece;
-        t.out.planes = c.terms;
+        t.out.planes = c.grad_terms;
         t.out.plane_stride = rows * p.piece;
         t.out.tokens = tokens;
         t.out.token0 = at;
@@ -564,7 +575,7 @@ CAM_API int cam_head_logprobs_backward(int64_t rows, int64_t vocab, int64_t widt
         TileOperand grad{};
         grad.base = ws + p.grad;
         grad.ld = p.piece;
-        grad.planes = c.terms;
+        grad.planes = c.grad_terms;
         grad.plane_stride = rows * p.piece;
         TileProduct both[2] = {};
         int count = 0;

@@ -61,7 +61,10 @@ __device__ __forceinline__ unsigned long long now_ns() {
 // the wait ran out (which starts the abort).
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                          int32_t* status) {
-    if (bar_test(bar, parity)) return true;
+    // (%globaltimer takes longer to read than most waits last: a few polls first)
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+        if (bar_test(bar, parity)) return true;
     const unsigned long long t0 = now_ns();
     while (!bar_test(bar, parity)) {
         if (*abort_flag) return false;

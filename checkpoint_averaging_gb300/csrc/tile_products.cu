@@ -4,10 +4,10 @@
 // SMs; unit u of the launch (a tile of one product, or one K range of it) goes to block
 // (pair) u, u + grid, ... Ten warps with fixed roles:
 //
-//   warp 0 (lane 0)  TMA producer: per K step of 128 bytes, this SM's 128 rows of A
+//   warp 0 (one lane)  TMA producer: per K step of 128 bytes, this SM's 128 rows of A
 //                    and its share of B (the tile's columns, or half of them in a
 //                    pair) into a ring of shared-memory stages;
-//   warp 1 (lane 0)  MMA issuer (of a pair: the first block's): four tcgen05.mma
+//   warp 1 (one lane)  MMA issuer (of a pair: the first block's): four tcgen05.mma
 //                    of 32 bytes of K per stage into one of two TMEM accumulators;
 //                    e4m3 operands' scales go from the stage into TMEM first
 //                    (tcgen05.cp) and are applied by the tensor core;
@@ -65,7 +65,7 @@ struct alignas(128) Prob {
     int32_t main0, run;    // from step main0 on, accumulated in runs of `run` steps
     int32_t a_mn, b_mn;
     int32_t unit0;
-    uint8_t term_a[6], term_b[6];
+    uint32_t terms_a, terms_b;  // the terms of each pair, four bits each
     int64_t M, N;
     TileOut o;
 };
@@ -99,6 +99,16 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
+}
+// One lane of the warp, in a form that the compiler knows for one: what it issues there
+// (TMA, MMA) takes its operands from uniform registers without a loop over the lanes
+// (2,048 x 38,912 logits of width 2,048: 257 us with a comparison of lanes, 196 with this).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred q;\n\telect.sync _|q, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(p));
+    return p != 0;
 }
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -298,6 +308,15 @@ __device__ __forceinline__ float exp2_fast(float x) {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+// exp(x - hi - lo) with what rounding x - hi and its product with log2(e) left out (both
+// matter in fp32 gradients: 2^-24 of an argument of 20 is 1e-6 of the exponential).
+__device__ __forceinline__ float exp_exact(float d, float rest) {
+    const float t = d * kLog2e;
+    const float c = fmaf(d, kLog2e, -t) + fmaf(d, 1.925963033500e-8f, rest * kLog2e);
+    const float e = exp2_fast(t);
+    return fmaf(e, c * 0.69314718f, e);
+}
+
 // The element of 32 at a place known at run time.
 __device__ __forceinline__ float pick(const float* v, int64_t at) {
     float x = v[0];
@@ -355,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + G::kBars);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int32_t* status = &g_operators_status;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const uint32_t rank = PAIR ? cluster_rank() : 0;
     const int worker = PAIR ? int(blockIdx.x >> 1) : int(blockIdx.x);
     const int workers = PAIR ? int(gridDim.x >> 1) : int(gridDim.x);
@@ -395,8 +414,10 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    if (warp == 0 && lane == 0) {
+    if (warp == 0 && elect_one()) {
         // ---- producer ----
+        const uint32_t ring = su32(smem);
+        const uint32_t to_full0 = PAIR ? first_block(full0) : full0;
         int stage = 0;
         uint32_t phase = 0, issued = 0, filled_parity = 0;
         bool ok = true;
@@ -405,38 +426,41 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
             const Prob& P = a.prob[t.p];
             const int arow = (t.mt * (PAIR ? 2 : 1) + int(rank)) * kRows;
             const int bcol = t.nt * G::kCols, brow = bcol + int(rank) * G::kBCols;
-            int pair = t.s0 / P.steps, ks = t.s0 - pair * P.steps;
-            for (int s = t.s0; s < t.s1; ++s) {
+            const int steps = P.steps, s1 = t.s1;
+            const bool a_mn = P.a_mn, b_mn = P.b_mn;
+            const CUtensorMap *ta = &P.ta, *tb = &P.tb;
+            int pair = t.s0 / steps, ks = t.s0 - pair * steps;
+            int za = P.terms_a >> (4 * pair) & 15, zb = P.terms_b >> (4 * pair) & 15;
+            for (int s = t.s0; s < s1; ++s) {
                 if (!bar_wait(empty0 + 8 * stage, phase ^ 1, abort_flag, status)) {
                     ok = false;
                     break;
                 }
-                const uint32_t sa = su32(smem + stage * G::kStage), sb = sa + G::kABytes;
-                uint32_t fb = full0 + 8 * stage;
-                if (rank == 0) bar_expect(fb, (PAIR ? 2 : 1) * G::kTx);
-                if constexpr (PAIR) fb = first_block(fb);
+                const uint32_t sa = ring + stage * G::kStage, sb = sa + G::kABytes;
+                const uint32_t fb = to_full0 + 8 * stage;
+                if (rank == 0) bar_expect(full0 + 8 * stage, (PAIR ? 2 : 1) * G::kTx);
                 if constexpr (E4M3) {
                     const int x = ks * kStepBytes;
-                    load<PAIR>(sa, &P.ta, x, arow, 0, fb);
-                    load<PAIR>(sb, &P.tb, x, brow, 0, fb);
+                    load<PAIR>(sa, ta, x, arow, 0, fb);
+                    load<PAIR>(sb, tb, x, brow, 0, fb);
                     const uint32_t ss = sb + G::kBBytes;
                     load<PAIR>(ss, &P.tsa, 0, arow / 128, ks, fb);
                     load<PAIR>(ss + G::kScaleA, &P.tsb, 0, bcol / 128, ks, fb);
                 } else {
-                    const int x = ks * 64, za = P.term_a[pair], zb = P.term_b[pair];
-                    if (P.a_mn) {
+                    const int x = ks * 64;
+                    if (a_mn) {
 #pragma unroll
                         for (int i = 0; i < kRows / 64; ++i)
-                            load<PAIR>(sa + i * kMnBox, &P.ta, arow + 64 * i, x, za, fb);
+                            load<PAIR>(sa + i * kMnBox, ta, arow + 64 * i, x, za, fb);
                     } else {
-                        load<PAIR>(sa, &P.ta, x, arow, za, fb);
+                        load<PAIR>(sa, ta, x, arow, za, fb);
                     }
-                    if (P.b_mn) {
+                    if (b_mn) {
 #pragma unroll
                         for (int i = 0; i < G::kBCols / 64; ++i)
-                            load<PAIR>(sb + i * kMnBox, &P.tb, brow + 64 * i, x, zb, fb);
+                            load<PAIR>(sb + i * kMnBox, tb, brow + 64 * i, x, zb, fb);
                     } else {
-                        load<PAIR>(sb, &P.tb, x, brow, zb, fb);
+                        load<PAIR>(sb, tb, x, brow, zb, fb);
                     }
                 }
                 issued |= 1u << stage;
@@ -445,9 +469,11 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                     stage = 0;
                     phase ^= 1;
                 }
-                if (++ks == P.steps) {
+                if (++ks == steps) {
                     ks = 0;
                     ++pair;
+                    za = P.terms_a >> (4 * pair) & 15;
+                    zb = P.terms_b >> (4 * pair) & 15;
                 }
             }
         }
@@ -459,8 +485,9 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                         if (now_ns() - t0 > kTcWaitLimitNs) break;
                 }
         }
-    } else if (warp == 1 && lane == 0 && rank == 0) {
+    } else if (warp == 1 && rank == 0 && elect_one()) {
         // ---- MMA issuer ----
+        const uint32_t ring = su32(smem);
         int stage = 0, acc = 0;
         uint32_t phase = 0, acc_phase = 0;
         uint32_t scale_at = 0;
@@ -470,8 +497,10 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
             const Prob& P = a.prob[t.p];
             const uint32_t idesc = instruction<E4M3, PAIR>(P.a_mn, P.b_mn);
             // 32 bytes further along a K-major row, or 16 rows further down an MN-major box
-            const uint32_t step_a = P.a_mn ? 16 * kStepBytes / 16 : 2;
-            const uint32_t step_b = P.b_mn ? 16 * kStepBytes / 16 : 2;
+            const uint64_t step_a = P.a_mn ? 16 * kStepBytes / 16 : 2;
+            const uint64_t step_b = P.b_mn ? 16 * kStepBytes / 16 : 2;
+            const uint64_t desc_a = P.a_mn ? smem_desc_mn(ring, kMnBox) : smem_desc(ring);
+            const uint64_t desc_b = P.b_mn ? smem_desc_mn(ring, kMnBox) : smem_desc(ring);
             for (int s = t.s0; s < t.s1 && ok;) {
                 const int end = run_end(P, s, t.s1);
                 if (!bar_wait(tempty0 + 8 * acc, acc_phase ^ 1, abort_flag, status)) {
@@ -487,16 +516,16 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t sa = su32(smem + stage * G::kStage), sb = sa + G::kABytes;
-                    const uint64_t da = P.a_mn ? smem_desc_mn(sa, kMnBox) : smem_desc(sa);
-                    const uint64_t db = P.b_mn ? smem_desc_mn(sb, kMnBox) : smem_desc(sb);
+                    // (addresses below 256 KB: no carry out of the descriptors' field)
+                    const uint64_t da = desc_a + uint32_t(stage * G::kStage / 16);
+                    const uint64_t db = desc_b + uint32_t((stage * G::kStage + G::kABytes) / 16);
                     uint32_t ta = 0, tb = 0;
                     if constexpr (E4M3) {
                         // four columns of A's scales, eight of B's; a tile that starts in the
                         // middle of a block of 128 starts two columns into them
                         ta = tmem + kScaleColumn + scale_at;
                         tb = ta + 4;
-                        const uint32_t ss = sb + G::kBBytes;
+                        const uint32_t ss = ring + stage * G::kStage + G::kABytes + G::kBBytes;
                         copy_scales<PAIR>(ta, ss);
                         copy_scales<PAIR>(tb, ss + 512);
                         copy_scales<PAIR>(tb + 4, ss + 1024);
@@ -505,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                     }
 #pragma unroll
                     for (int k = 0; k < kStepBytes / 32; ++k) {
-                        multiply<E4M3, PAIR>(d, da + uint64_t(step_a * k), db + uint64_t(step_b * k),
+                        multiply<E4M3, PAIR>(d, da + step_a * k, db + step_b * k,
                                              idesc, accumulate, ta, tb);
                         accumulate = 1;
                     }
@@ -624,10 +653,19 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                     const int64_t at = token - col;
                     float hit = 0.0f;  // g (1 - p) of the row's token, without cancellation
                     if (at >= 0 && at < n) hit = -g * expm1f((pick(v, at) - lse) - lo);
+                    const bool fine = o.planes == 3;
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
-                        const float d = (v[i] - lse) - lo;
-                        const float p = exp2_fast(d * kLog2e);
+                        float d = v[i] - lse, p;
+                        if (fine) {
+                            const float b = v[i] - d;  // (v - lse) - d, exactly: two-sum
+                            const float rest = ((v[i] - (d + b)) + (b - lse)) - lo;
+                            p = exp_exact(d, rest);
+                            d += rest;
+                        } else {
+                            d -= lo;
+                            p = exp2_fast(d * kLog2e);
+                        }
                         float w = at == i ? hit : -g * p;
                         if (o.h) w -= h * p * (d + H);
                         v[i] = skip ? 0.0f : w;
@@ -786,17 +824,17 @@ int tile_products(const char* fn, const TileProduct* ps, int n, bool e4m3, bool 
         for (int sum = std::min(2, p.a.planes + p.b.planes - 2); sum >= 0; --sum)
             for (int k = 0; k <= sum; ++k)
                 if (k < p.a.planes && sum - k < p.b.planes) {
-                    P.term_a[pairs] = static_cast<uint8_t>(k);
-                    P.term_b[pairs++] = static_cast<uint8_t>(sum - k);
+                    P.terms_a |= uint32_t(k) << (4 * pairs);
+                    P.terms_b |= uint32_t(sum - k) << (4 * pairs++);
                 }
         const int step = e4m3 ? 128 : 64;
         P.steps = static_cast<int32_t>((p.a.k + step - 1) / step);
         P.all_steps = P.steps * pairs;
-        // Runs of the leading products: fp32 inputs' of 256 terms, logits of bf16 ones of 512,
-        // e4m3 ones' of 2,048 (their steps add twice as many terms); bf16 results of bf16
-        // inputs hide what a long run loses.
+        // Runs of the leading products: fp32 inputs' of 256 terms, logits of bf16 ones of 768
+        // (of 512: 3 % slower), e4m3 ones' of 2,048 (their steps add twice as many terms); bf16
+        // results of bf16 inputs hide what a long run loses.
         P.main0 = P.steps * (pairs - 1);
-        P.run = pairs > 1 ? 4 : e4m3 ? 16 : epilogue == kTileStats ? 8 : INT_MAX;
+        P.run = pairs > 1 ? 4 : e4m3 ? 16 : epilogue == kTileStats ? 12 : INT_MAX;
         const int splits = std::max(1, std::min(p.splits, P.all_steps));
         P.per_split = (P.all_steps + splits - 1) / splits;
         P.unit0 = units;
