@@ -74,12 +74,12 @@ __global__ void __launch_bounds__(kHeadThreads) terms_kernel(const TermArgs a) {
         const T* at = src + row * a.stride + col;
         if (keep && vec && col + 8 <= a.cols) {
             if constexpr (sizeof(T) == 4) {
-                const float4 x = __ldg(reinterpret_cast<const float4*>(at));
-                const float4 y = __ldg(reinterpret_cast<const float4*>(at) + 1);
+                const float4 x = *reinterpret_cast<const float4*>(at);
+                const float4 y = reinterpret_cast<const float4*>(at)[1];
                 v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
                 v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
             } else {
-                const uint4 x = __ldg(reinterpret_cast<const uint4*>(at));
+                const uint4 x = *reinterpret_cast<const uint4*>(at);
                 const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
@@ -135,23 +135,56 @@ __device__ __forceinline__ void join(TileStat& s, const TileStat& o) {
     }
 }
 
-// Eight rows per block, 32 threads each: their parts are one line of 128 bytes.
+__device__ __forceinline__ void join_lanes(TileStat& s, int by) {
+    TileStat o;
+    o.m = __shfl_xor_sync(0xFFFFFFFFu, s.m, by);
+    o.a = __shfl_xor_sync(0xFFFFFFFFu, s.a, by);
+    o.c = __shfl_xor_sync(0xFFFFFFFFu, s.c, by);
+    o.t = __shfl_xor_sync(0xFFFFFFFFu, s.t, by);
+    join(s, o);
+}
+
+// ROWS rows per block (eight: a part's statistics of theirs are one line of 128 bytes; one
+// where there are few rows, so that their parts are read by many threads), 256 / ROWS
+// threads each, sixteen parts in flight per thread.
+template <int ROWS>
 __global__ void __launch_bounds__(kHeadThreads) stats_kernel(const StatArgs a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    __shared__ TileStat all[32][8];
-    const int r = threadIdx.x & 7, y = threadIdx.x >> 3;
-    const int64_t row = int64_t(blockIdx.x) * 8 + r;
+    constexpr int kAcross = kHeadThreads / ROWS, kAtOnce = 16;
+    __shared__ TileStat all[kHeadThreads / 32][ROWS];
+    const int r = threadIdx.x % ROWS, y = threadIdx.x / ROWS;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t row = int64_t(blockIdx.x) * ROWS + r;
     TileStat s{0.0f, 0.0f, 0.0f, 0.0f};
     if (row < a.rows) {
-#pragma unroll 4
-        for (int64_t p = y; p < a.parts; p += 32) join(s, a.stats[p * a.rows + row]);
+        for (int64_t p0 = y; p0 < a.parts; p0 += kAcross * kAtOnce) {
+            float4 v[kAtOnce];
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) {
+                const int64_t p = p0 + k * kAcross;
+                v[k] = p < a.parts
+                           ? *reinterpret_cast<const float4*>(a.stats + p * a.rows + row)
+                           : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            }
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) join(s, TileStat{v[k].x, v[k].y, v[k].z, v[k].w});
+        }
     }
-    all[y][r] = s;
+#pragma unroll
+    for (int by = ROWS; by < 32; by *= 2) join_lanes(s, by);
+    if (lane < ROWS) all[warp][lane] = s;
     __syncthreads();
-    if (threadIdx.x >= 8 || row >= a.rows) return;
-#pragma unroll 1
-    for (int k = 1; k < 32; ++k) join(s, all[k][r]);
+    if (warp > 0) return;
+    // the eight warps' parts: lane ROWS k + r holds warp k's of row r, two for eight rows
+    constexpr int kWarps = kHeadThreads / 32, kHeld = 32 / ROWS < kWarps ? 32 / ROWS : kWarps;
+    const int k0 = lane / ROWS;
+    s = TileStat{0.0f, 0.0f, 0.0f, 0.0f};
+    if (k0 < kHeld)
+        for (int k = k0; k < kWarps; k += kHeld) join(s, all[k][r]);
+#pragma unroll
+    for (int by = ROWS; by < 32 && by < ROWS * kHeld; by *= 2) join_lanes(s, by);
+    if (lane >= ROWS || row >= a.rows) return;
     // log(a + c) from its small part where one token leads
     const double sum = double(s.a) + double(s.c);
     const double log_s = log1p(double(s.a) + (double(s.c) - 1.0));
@@ -181,32 +214,61 @@ struct JoinArgs {
     int64_t stride;
 };
 
-// Sums of partials in the order of their ranges, in eight runs: a block of 32 x 8 threads
-// takes 32 columns of a row.
-template <typename T>
+// Sums of partials in the order of their ranges: a block of 32 x RUNS threads takes 128
+// columns of 8 / RUNS rows, RUNS threads the ranges of one column in as many runs (one for few
+// ranges, eight where there are many and few columns).
+template <typename T, int RUNS>
 __global__ void __launch_bounds__(kHeadThreads) join_kernel(const JoinArgs a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    __shared__ float runs[8][33];
-    const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-    const int64_t across = (a.cols + 31) / 32, tiles = across * a.rows;
-    for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-        const int64_t row = t / across, col = (t - row * across) * 32 + x;
-        const int32_t per = (a.splits + 7) / 8, s0 = y * per, s1 = min(a.splits, s0 + per);
-        float sum = 0.0f;
-        if (col < a.cols) {
+    constexpr int kRowsEach = 8 / RUNS;
+    __shared__ float4 runs[8][32];
+    const int x = threadIdx.x & 31, warp = threadIdx.x >> 5, run = warp % RUNS;
+    const int64_t across = (a.ld + 127) / 128, groups = (a.rows + kRowsEach - 1) / kRowsEach;
+    const int32_t per = (a.splits + RUNS - 1) / RUNS, s0 = run * per, s1 = min(a.splits, s0 + per);
+    for (int64_t t = blockIdx.x; t < across * groups; t += gridDim.x) {
+        const int64_t group = t / across, col = (t - group * across) * 128 + 4 * x;
+        const int64_t row = group * kRowsEach + warp / RUNS;
+        const bool in = row < a.rows && col < a.ld;  // (ld is a multiple of eight)
+        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (in) {
             const float* p = a.part + row * a.ld + col;
-#pragma unroll 4
-            for (int32_t s = s0; s < s1; ++s) sum += p[int64_t(s) * a.rows * a.ld];
+#pragma unroll 8
+            for (int32_t s = s0; s < s1; ++s) {
+                const float4 v = *reinterpret_cast<const float4*>(p + int64_t(s) * a.rows * a.ld);
+                sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+            }
         }
-        runs[y][x] = sum;
-        __syncthreads();
-        if (y == 0 && col < a.cols) {
+        if constexpr (RUNS > 1) {
+            runs[warp][x] = sum;
+            __syncthreads();
+            if (run == 0) {
 #pragma unroll
-            for (int k = 1; k < 8; ++k) sum += runs[k][x];
-            static_cast<T*>(a.out)[row * a.stride + col] = T(sum);
+                for (int k = 1; k < RUNS; ++k) {
+                    const float4 v = runs[warp + k][x];
+                    sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+                }
+            }
+            __syncthreads();
         }
-        __syncthreads();
+        if (in && run == 0) {
+            T* out = static_cast<T*>(a.out) + row * a.stride + col;
+            const float v[4] = {sum.x, sum.y, sum.z, sum.w};
+            if (col + 4 <= a.cols && reinterpret_cast<uintptr_t>(out) % (4 * sizeof(T)) == 0) {
+                if constexpr (sizeof(T) == 4) {
+                    *reinterpret_cast<float4*>(out) = sum;
+                } else {
+                    const __nv_bfloat162 lo = __floats2bfloat162_rn(v[0], v[1]);
+                    const __nv_bfloat162 hi = __floats2bfloat162_rn(v[2], v[3]);
+                    *reinterpret_cast<uint2*>(out) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                                                                *reinterpret_cast<const uint32_t*>(&hi));
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (col + k < a.cols) out[k] = T(v[k]);
+            }
+        }
     }
 }
 
@@ -368,11 +430,12 @@ BackwardPlan backward_plan(const HeadCall& c, int sms, bool want_hidden, bool wa
     const int64_t across = (c.width + kTileCols - 1) / kTileCols;
     const int64_t pairs = c.terms == 3 ? 6 : c.grad_terms;
     p.part_ld = c.ld;
-    // both products share a launch: units of one length, so that its last round is full
+    // both products share a launch: units of like length, the longer ones first, so that its
+    // last round is nearly full
     const int64_t head_steps = (c.rows + 63) / 64 * pairs, hidden_steps = (piece + 63) / 64 * pairs;
     p.head_splits = splits_for((piece + tile - 1) / tile * across, head_steps, grid, INT64_MAX);
     p.hidden_splits = splits_for((c.rows + tile - 1) / tile * across, hidden_steps, 2 * grid,
-                                 std::max<int64_t>(64, head_steps));
+                                 std::max<int64_t>(64, 2 * head_steps));
     int64_t at = 0;
     p.x = at;
     at += term_bytes(c, c.rows);
@@ -392,9 +455,14 @@ BackwardPlan backward_plan(const HeadCall& c, int sms, bool want_hidden, bool wa
 cudaError_t join_parts(const HeadCall& c, const float* part, int64_t rows, int32_t splits, void* out,
                        int64_t stride, int sms, cudaStream_t s) {
     JoinArgs a{part, rows, c.width, c.ld, splits, out, stride};
-    const int64_t blocks = std::min<int64_t>((c.width + 31) / 32 * rows, int64_t(sms) * 16);
-    return c.dtype == CAM_F32 ? launch(join_kernel<float>, blocks, a, s)
-                              : launch(join_kernel<__nv_bfloat16>, blocks, a, s);
+    const bool runs = splits > 16 && rows * c.ld < (int64_t(1) << 20);
+    const int64_t tiles = (c.ld + 127) / 128 * (runs ? rows : (rows + 7) / 8);
+    const int64_t blocks = std::min<int64_t>(tiles, int64_t(sms) * 16);
+    if (c.dtype == CAM_F32)
+        return runs ? launch(join_kernel<float, 8>, blocks, a, s)
+                    : launch(join_kernel<float, 1>, blocks, a, s);
+    return runs ? launch(join_kernel<__nv_bfloat16, 8>, blocks, a, s)
+                : launch(join_kernel<__nv_bfloat16, 1>, blocks, a, s);
 }
 
 int fail(const char* fn, cudaError_t ce) {
@@ -477,7 +545,8 @@ CAM_API int cam_head_logprobs(int64_t rows, int64_t vocab, int64_t width, const 
     }
     if (ce == cudaSuccess) {
         StatArgs a{stats, (vocab + 127) / 128, rows, vocab, mine, tokens, logp, entropy, lse, lse_lo};
-        ce = launch(stats_kernel, (rows + 7) / 8, a, s);
+        ce = rows <= 64 ? launch(stats_kernel<1>, rows, a, s)
+                        : launch(stats_kernel<8>, (rows + 7) / 8, a, s);
     }
     return ce == cudaSuccess ? CAM_OK : fail(fn, ce);
 }

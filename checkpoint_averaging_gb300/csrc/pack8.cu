@@ -4,8 +4,8 @@
 // q = e4m3(w * 2^-e), round to nearest even. The scale is a power of two so that w * 2^-e
 // is exact (the one rounding is e4m3's) and the tensor core can apply it (UE8M0).
 //
-// One pass over the matrix; HBM bounds it. A warp takes one row's block of 128 columns
-// at a time, four columns per lane, four rows in flight, and the largest magnitude is one
+// One pass over the matrix; HBM bounds it. A warp takes the same 128 columns of eight rows,
+// four columns per lane, all in flight at once, and the largest magnitude is one
 // integer warp reduction (of the bits without sign: NaN and infinity come out above
 // every number).
 #include <cuda_bf16.h>
@@ -22,16 +22,16 @@ namespace cam {
 namespace {
 
 constexpr int kThreads8 = 256;
-constexpr int kRowsAtOnce = 4;
+constexpr int kRowsAtOnce = 8;  // of a warp, in flight
 
 template <typename T>
 __device__ __forceinline__ void load4(const T* p, int n, bool vec, float* v) {
     if (vec && n >= 4) {
         if constexpr (sizeof(T) == 4) {
-            const float4 x = __ldg(reinterpret_cast<const float4*>(p));
+            const float4 x = *reinterpret_cast<const float4*>(p);
             v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
         } else {
-            const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
+            const uint2 x = *reinterpret_cast<const uint2*>(p);
             v[0] = __uint_as_float(x.x << 16), v[1] = __uint_as_float(x.x & 0xFFFF0000u);
             v[2] = __uint_as_float(x.y << 16), v[3] = __uint_as_float(x.y & 0xFFFF0000u);
         }
@@ -66,8 +66,13 @@ __device__ __forceinline__ uint32_t quantise(float* v, uint32_t* scale) {
     return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
 }
 
-// Warp w of the grid takes 32 rows of one block of columns: their scales are 128 bytes
-// that lie 16 bytes apart, written by the lanes in the end.
+// The word of a row's scale: lane r % 32 of the block of 128 rows, column r / 32 % 4.
+__device__ __forceinline__ int64_t scale_at(int64_t row, int32_t kb, int64_t row_blocks) {
+    return (int64_t(kb) * row_blocks + row / 128) * 128 + (row % 32) * 4 + row / 32 % 4;
+}
+
+// Unit u of the grid's warps: eight rows of one block of columns; units of the same rows
+// are neighbours. Rows up to the next multiple of 128 have a scale, too.
 template <typename T>
 __global__ void __launch_bounds__(kThreads8) pack8_kernel(int64_t rows, int64_t cols, const T* w,
                                                           int64_t stride, bool vec, uint8_t* q,
@@ -79,33 +84,25 @@ __global__ void __launch_bounds__(kThreads8) pack8_kernel(int64_t rows, int64_t 
     const int64_t row_blocks = (rows + 127) / 128;
     for (int64_t u = (int64_t(blockIdx.x) * kThreads8 + threadIdx.x) >> 5; u < units;
          u += int64_t(gridDim.x) * (kThreads8 / 32)) {
-        // (units of one row group are neighbours: a row is read from one place)
         const int64_t group = u / col_blocks;
         const int32_t kb = static_cast<int32_t>(u - group * col_blocks);
-        const int64_t row0 = group * 32;
+        const int64_t row0 = group * kRowsAtOnce;
         const int64_t col = int64_t(kb) * kP8Block + 4 * lane;
         const int n = static_cast<int>(min(int64_t(4), max(int64_t(0), cols - col)));
         uint32_t mine = 127;
-        for (int r0 = 0; r0 < 32 && row0 + r0 < rows; r0 += kRowsAtOnce) {
-            float v[kRowsAtOnce][4];
+        float v[kRowsAtOnce][4];
 #pragma unroll
-            for (int r = 0; r < kRowsAtOnce; ++r) {
-                const int64_t row = row0 + r0 + r;
-                load4(w + row * stride + col, row < rows ? n : 0, vec, v[r]);
-            }
+        for (int r = 0; r < kRowsAtOnce; ++r)
+            load4(w + (row0 + r) * stride + col, row0 + r < rows ? n : 0, vec, v[r]);
 #pragma unroll
-            for (int r = 0; r < kRowsAtOnce; ++r) {
-                const int64_t row = row0 + r0 + r;
-                uint32_t scale;
-                const uint32_t four = quantise(v[r], &scale);
-                if (lane == r0 + r) mine = scale;
-                if (row < rows && col < ld)
-                    *reinterpret_cast<uint32_t*>(q + row * ld + col) = four;
-            }
+        for (int r = 0; r < kRowsAtOnce; ++r) {
+            uint32_t scale;
+            const uint32_t four = quantise(v[r], &scale);
+            if (lane == r && row0 + r < rows) mine = scale;
+            if (row0 + r < rows && col < ld)
+                *reinterpret_cast<uint32_t*>(q + (row0 + r) * ld + col) = four;
         }
-        // word of row r: lane r % 32 of the block, column r / 32
-        const int64_t block = int64_t(kb) * row_blocks + row0 / 128;
-        scales[block * 128 + lane * 4 + (row0 / 32) % 4] = mine * 0x01010101u;
+        if (lane < kRowsAtOnce) scales[scale_at(row0 + lane, kb, row_blocks)] = mine * 0x01010101u;
     }
 }
 
@@ -139,36 +136,31 @@ __global__ void __launch_bounds__(kThreads8) unpack8_kernel(int64_t rows, int64_
          u += int64_t(gridDim.x) * (kThreads8 / 32)) {
         const int64_t group = u / col_blocks;
         const int32_t kb = static_cast<int32_t>(u - group * col_blocks);
-        const int64_t row0 = group * 32;
+        const int64_t row0 = group * kRowsAtOnce;
         const int64_t col = int64_t(kb) * kP8Block + 4 * lane;
         const int n = static_cast<int>(min(int64_t(4), max(int64_t(0), cols - col)));
-        const int64_t block = int64_t(kb) * row_blocks + row0 / 128;
-        const uint32_t mine = __ldg(scales + block * 128 + lane * 4 + (row0 / 32) % 4) & 0xFFu;
-        for (int r0 = 0; r0 < 32 && row0 + r0 < rows; r0 += kRowsAtOnce) {
-            uint32_t four[kRowsAtOnce];
+        const uint32_t mine =
+            lane < kRowsAtOnce ? scales[scale_at(row0 + lane, kb, row_blocks)] & 0xFFu : 0u;
+        uint32_t four[kRowsAtOnce];
 #pragma unroll
-            for (int r = 0; r < kRowsAtOnce; ++r) {
-                const int64_t row = row0 + r0 + r;
-                four[r] = row < rows && n > 0
-                              ? __ldg(reinterpret_cast<const uint32_t*>(q + row * ld + col))
-                              : 0u;
+        for (int r = 0; r < kRowsAtOnce; ++r)
+            four[r] = row0 + r < rows && n > 0
+                          ? *reinterpret_cast<const uint32_t*>(q + (row0 + r) * ld + col)
+                          : 0u;
+#pragma unroll
+        for (int r = 0; r < kRowsAtOnce; ++r) {
+            // 2^e, e in [-126, 120]
+            const float s = __uint_as_float(__shfl_sync(0xFFFFFFFFu, mine, r) << 23);
+            float v[4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+                    static_cast<__nv_fp8x2_storage_t>(four[r] >> (16 * i)), __NV_E4M3);
+                const float2 f = __half22float2(__half2(h));
+                v[2 * i] = f.x * s;
+                v[2 * i + 1] = f.y * s;
             }
-#pragma unroll
-            for (int r = 0; r < kRowsAtOnce; ++r) {
-                const int64_t row = row0 + r0 + r;
-                // 2^e, e in [-126, 120]
-                const float s = __uint_as_float(__shfl_sync(0xFFFFFFFFu, mine, r0 + r) << 23);
-                float v[4];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
-                        static_cast<__nv_fp8x2_storage_t>(four[r] >> (16 * i)), __NV_E4M3);
-                    const float2 f = __half22float2(__half2(h));
-                    v[2 * i] = f.x * s;
-                    v[2 * i + 1] = f.y * s;
-                }
-                if (row < rows) store4(out + row * stride + col, n, vec, v);
-            }
+            if (row0 + r < rows) store4(out + (row0 + r) * stride + col, n, vec, v);
         }
     }
 }
@@ -177,13 +169,13 @@ bool vec_aligned(const void* p, int64_t stride, int64_t bytes, int64_t size) {
     return reinterpret_cast<uintptr_t>(p) % bytes == 0 && stride * size % bytes == 0;
 }
 
-// Blocks for `units` warps: enough to fill the GPU, a few warps each beyond that.
+// Blocks for `units` warps, one each.
 cudaError_t grid_for(int64_t units, int* blocks) {
     int dev = 0, sms = 0;
     const cudaError_t ce = current_device(&dev, &sms);
     *blocks = static_cast<int>(
         std::max<int64_t>(1, std::min<int64_t>((units + kThreads8 / 32 - 1) / (kThreads8 / 32),
-                                               int64_t(sms) * 64)));
+                                               int64_t(1) << 30)));
     return ce;
 }
 
@@ -210,7 +202,7 @@ int p8_pack(const char* fn, int64_t rows, int64_t cols, const void* w, int64_t s
     const int size = dtype == CAM_F32 ? 4 : 2;
     int32_t col_blocks = static_cast<int32_t>((cols + kP8Block - 1) / kP8Block);
     // (whole blocks of 128 rows, so that every scale of the form is written)
-    int64_t units = (rows + 127) / 128 * 4 * col_blocks;
+    int64_t units = (rows + 127) / 128 * (128 / kRowsAtOnce) * col_blocks;
     int64_t ld = p8_ld(cols);
     bool vec = vec_aligned(w, stride, 4 * size, size);
     uint8_t* q = static_cast<uint8_t*>(packed);
@@ -265,7 +257,7 @@ CAM_API int cam_unpack8(int64_t rows, int64_t cols, const void* packed, void* va
     if (rows == 0 || cols == 0) return CAM_OK;
     const int size = dtype == CAM_F32 ? 4 : 2;
     int32_t col_blocks = static_cast<int32_t>((cols + cam::kP8Block - 1) / cam::kP8Block);
-    int64_t units = (rows + 31) / 32 * col_blocks;
+    int64_t units = (rows + cam::kRowsAtOnce - 1) / cam::kRowsAtOnce * col_blocks;
     int64_t ld = cam::p8_ld(cols);
     bool vec = cam::vec_aligned(values, stride, 4 * size, size);
     const uint8_t* q = static_cast<const uint8_t*>(packed);

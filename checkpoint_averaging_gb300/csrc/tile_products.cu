@@ -54,7 +54,11 @@ constexpr int kThreads = 320;    // ten warps
 constexpr int kEpilogueWarps = 8;
 constexpr int kStepBytes = 128;  // bytes of K per stage
 constexpr int kMnBox = 64 * kStepBytes;  // MN-major box: 64 K rows of 64 elements
-constexpr int kRing = 222 * 1024;
+constexpr int kRing = 208 * 1024;
+// A warp's buffer for storing rows that do not start on 32 bytes: 32 rows of 16 columns, and
+// a word between rows so that a column's words lie in as many banks.
+constexpr int kTurn = 17;
+constexpr int kTurnBytes = kEpilogueWarps * 32 * kTurn * 4;
 
 struct alignas(128) Prob {
     CUtensorMap ta, tb;    // operands
@@ -65,6 +69,7 @@ struct alignas(128) Prob {
     int32_t main0, run;    // from step main0 on, accumulated in runs of `run` steps
     int32_t a_mn, b_mn;
     int32_t unit0;
+    int32_t wide;          // rows of o.y start on 32 bytes
     uint32_t terms_a, terms_b;  // the terms of each pair, four bits each
     int64_t M, N;
     TileOut o;
@@ -87,7 +92,9 @@ struct Geo {
     static constexpr int kStage = (kTx + 1023) / 1024 * 1024;
     static constexpr int kStages = kRing / kStage < 8 ? kRing / kStage : 8;
     static constexpr int kBars = 2 * kStages + 5;
-    static constexpr int kSmem = kStages * kStage + 8 * kBars + 16 + 1024;
+    static constexpr int kTurnAt = kStages * kStage;
+    static constexpr int kBarsAt = kTurnAt + kTurnBytes;
+    static constexpr int kSmem = kBarsAt + 8 * kBars + 16 + 1024;
     static_assert(kSmem <= kMaxSharedBytes, "over the per-block shared memory limit");
 };
 
@@ -267,36 +274,43 @@ __device__ __forceinline__ void store8(void* p, const uint32_t* w) {
                  : "memory");
 }
 
-// 32 columns of a row as bf16, `n` of them inside the matrix.
-__device__ __forceinline__ void store_bf16(__nv_bfloat16* y, const float* v, int n) {
-    if (n >= 32 && (reinterpret_cast<uintptr_t>(y) & 31) == 0) {
+// 32 columns of a row as bf16 to a 32-byte aligned address.
+__device__ __forceinline__ void store_bf16(__nv_bfloat16* y, const float* v) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            uint32_t w[8];
+    for (int k = 0; k < 2; ++k) {
+        uint32_t w[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = bf16x2(v[16 * k + 2 * i], v[16 * k + 2 * i + 1]);
-            store8(y + 16 * k, w);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (i < n) y[i] = __float2bfloat16_rn(v[i]);
+        for (int i = 0; i < 8; ++i) w[i] = bf16x2(v[16 * k + 2 * i], v[16 * k + 2 * i + 1]);
+        store8(y + 16 * k, w);
     }
 }
 
-__device__ __forceinline__ void store_f32(float* y, const float* v, int n) {
-    if (n >= 32 && (reinterpret_cast<uintptr_t>(y) & 31) == 0) {
+// Eight columns of a row to a 32-byte aligned address.
+__device__ __forceinline__ void store_f32(float* y, const float* v) {
+    uint32_t w[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t w[8];
+    for (int k = 0; k < 8; ++k) w[k] = __float_as_uint(v[k]);
+    store8(y, w);
+}
+
+// 32 columns of 32 rows, this lane's row in v, to addresses of any alignment: turned in shared
+// memory so that half a warp writes 16 columns of one row (5,003 fp32 columns: a warp's store
+// takes 4 sectors of memory instead of 32).
+template <typename T>
+__device__ __forceinline__ void store_turned(float* buf, T* y, int64_t ldy, const float* v, int rows,
+                                             int n, int lane) {
+    const int c = lane & 15, odd = lane >> 4;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) w[k] = __float_as_uint(v[8 * i + k]);
-            store8(y + 8 * i, w);
+    for (int h = 0; h < 2; ++h) {
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) buf[lane * kTurn + i] = v[16 * h + i];
+        __syncwarp();
+        if (16 * h + c < n) {
+#pragma unroll 8
+            for (int r = odd; r < 32; r += 2)
+                if (r < rows) y[r * ldy + 16 * h + c] = T(buf[r * kTurn + c]);
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (i < n) y[i] = v[i];
     }
 }
 
@@ -365,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + G::kStages * G::kStage);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + G::kBarsAt);
     const uint32_t full0 = su32(bars);
     const uint32_t empty0 = full0 + 8 * G::kStages;
     const uint32_t tfull0 = empty0 + 8 * G::kStages;
@@ -561,6 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     } else if (warp >= 2) {
         // ---- epilogue ----
         const int quarter = warp & 3, half = (warp - 2) >> 2;
+        float* turn = reinterpret_cast<float*>(smem + G::kTurnAt) + (warp - 2) * 32 * kTurn;
         constexpr int kHalf = G::kCols / 2, kGroups = kHalf / 32;
         int acc = 0;
         uint32_t acc_phase = 0;
@@ -578,17 +593,17 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
             float lse = 0, lo = 0, H = 0, g = 0, h = 0;
             int64_t token = -1;
             if constexpr (EPI != kTileOut) {
-                if (in && o.tokens) token = __ldg(o.tokens + row);
+                if (in && o.tokens) token = o.tokens[row];
             }
             bool skip = false;  // kTileGrad: a row without a gradient gets zeros
             if constexpr (EPI == kTileGrad) {
                 if (in) {
-                    lse = __ldg(o.lse + row);
-                    if (o.lse_lo) lo = __ldg(o.lse_lo + row);
-                    if (o.g && token >= 0) g = __ldg(o.g + row);
+                    lse = o.lse[row];
+                    if (o.lse_lo) lo = o.lse_lo[row];
+                    if (o.g && token >= 0) g = o.g[row];
                     if (o.h) {
-                        h = __ldg(o.h + row);
-                        H = __ldg(o.entropy + row);
+                        h = o.h[row];
+                        H = o.entropy[row];
                     }
                 }
                 skip = g == 0.0f && h == 0.0f;
@@ -672,8 +687,9 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                     }
                     if (in) {
                         __nv_bfloat16* y = static_cast<__nv_bfloat16*>(o.y) + row * o.ldy + col;
+                        // (rows of whole tiles: columns past the matrix have room)
                         for (int k = 0; k < o.planes; ++k) {
-                            store_bf16(y + k * o.plane_stride, v, n);
+                            store_bf16(y + k * o.plane_stride, v);
                             if (k + 1 < o.planes) {
 #pragma unroll
                                 for (int i = 0; i < 32; ++i)
@@ -681,22 +697,37 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                             }
                         }
                     }
-                } else {
-                    if (in) {
-                        if (o.part) {
-                            float* y = o.part + (int64_t(t.split) * P.M + row) * o.part_ld + col;
+                } else if (o.part) {
+                    if (in) {  // (rows of whole groups of eight columns)
+                        float* y = o.part + (int64_t(t.split) * P.M + row) * o.part_ld + col;
+#pragma unroll
+                        for (int k = 0; k < 32; k += 8) {
+                            if (k >= n) break;
                             if (o.add) {
 #pragma unroll
-                                for (int i = 0; i < 32; ++i)
-                                    if (i < n) v[i] += y[i];
+                                for (int i = k; i < k + 8; i += 4) {
+                                    const float4 x = *reinterpret_cast<const float4*>(y + i);
+                                    v[i] += x.x, v[i + 1] += x.y, v[i + 2] += x.z, v[i + 3] += x.w;
+                                }
                             }
-                            store_f32(y, v, n);
-                        } else if (o.y_bf16) {
-                            store_bf16(static_cast<__nv_bfloat16*>(o.y) + row * o.ldy + col, v, n);
-                        } else {
-                            store_f32(static_cast<float*>(o.y) + row * o.ldy + col, v, n);
+                            store_f32(y + k, v + k);
                         }
                     }
+                } else if (P.wide && n == 32) {
+                    if (in && o.y_bf16) {
+                        store_bf16(static_cast<__nv_bfloat16*>(o.y) + row * o.ldy + col, v);
+                    } else if (in) {
+                        float* y = static_cast<float*>(o.y) + row * o.ldy + col;
+#pragma unroll
+                        for (int k = 0; k < 32; k += 8) store_f32(y + k, v + k);
+                    }
+                } else {
+                    const int rows = P.M - row0 < 32 ? int(P.M - row0) : 32;
+                    const int64_t at = row0 * o.ldy + col;
+                    if (o.y_bf16)
+                        store_turned(turn, static_cast<__nv_bfloat16*>(o.y) + at, o.ldy, v, rows, n, lane);
+                    else
+                        store_turned(turn, static_cast<float*>(o.y) + at, o.ldy, v, rows, n, lane);
                 }
             }
             if constexpr (EPI == kTileStats) {
@@ -838,6 +869,8 @@ int tile_products(const char* fn, const TileProduct* ps, int n, bool e4m3, bool 
         const int splits = std::max(1, std::min(p.splits, P.all_steps));
         P.per_split = (P.all_steps + splits - 1) / splits;
         P.unit0 = units;
+        const int64_t size = p.out.y_bf16 ? 2 : 4;
+        P.wide = reinterpret_cast<uintptr_t>(p.out.y) % 32 == 0 && p.out.ldy * size % 32 == 0;
         P.o = p.out;
         units += P.m_tiles * P.n_tiles * ((P.all_steps + P.per_split - 1) / P.per_split);
     }
