@@ -24,6 +24,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <utility>
 
 #include "cam_internal.h"
 #include "op_launch.h"
@@ -302,6 +303,7 @@ struct HeadCall {
     int64_t ld;      // of a matrix in terms
     bool x_direct, w_direct;  // read where they are
     bool pair;
+    bool few;        // few rows of logits: as columns, the vocabulary along the tiles' rows
 };
 
 int64_t padded(int64_t bytes) { return (bytes + 511) / 512 * 512; }
@@ -339,6 +341,8 @@ int check_head(const char* fn, HeadCall& c) {
     c.grad_terms = c.terms == 3 ? 3 : c.rows > 256 ? 1 : 2;
     // a pair of SMs takes 256 rows, one SM 128
     c.pair = c.rows > 128;
+    // (16 rows of 73,760 logits: a tile of 128 rows of logits has work for one warp in eight)
+    c.few = c.rows <= kTileFew;
     return CAM_OK;
 }
 
@@ -386,6 +390,9 @@ int64_t piece_rows(const HeadCall& c, int64_t per, int64_t budget) {
 constexpr int64_t kForwardBudget = int64_t(1) << 29;   // a piece of the head in terms
 constexpr int64_t kBackwardBudget = int64_t(1) << 29;  // a piece of G, and of the head in terms
 
+// Parts of the vocabulary with statistics of their own.
+int64_t stat_parts(const HeadCall& c) { return c.few ? (c.vocab + 31) / 32 : (c.vocab + 127) / 128; }
+
 struct ForwardPlan {
     int64_t piece, x, w, stats, mine, bytes;  // offsets in the workspace
 };
@@ -399,7 +406,7 @@ ForwardPlan forward_plan(const HeadCall& c) {
     p.w = at;
     if (!c.w_direct) at += term_bytes(c, p.piece);
     p.stats = at;
-    at += padded((c.vocab + 127) / 128 * c.rows * int64_t(sizeof(TileStat)));
+    at += padded(stat_parts(c) * c.rows * int64_t(sizeof(TileStat)));
     p.mine = at;
     at += padded(c.rows * 4);
     p.bytes = at;
@@ -409,7 +416,7 @@ ForwardPlan forward_plan(const HeadCall& c) {
 struct BackwardPlan {
     int64_t piece, x, w, grad, hidden, head, bytes;
     int32_t hidden_splits, head_splits;
-    int64_t part_ld;
+    int64_t part_ld, grad_ld, grad_stride;
 };
 
 // Ranges of K for a product of `tiles` tiles of `steps` steps: enough units for `want`, and
@@ -442,7 +449,10 @@ BackwardPlan backward_plan(const HeadCall& c, int sms, bool want_hidden, bool wa
     p.w = at;
     if (!c.w_direct) at += term_bytes(c, piece);
     p.grad = at;
-    at += padded(c.grad_terms * c.rows * p.piece * 2);
+    // G [rows][piece], or of few rows G^T [piece][rows, to a multiple of eight]
+    p.grad_ld = c.few ? (c.rows + 7) / 8 * 8 : p.piece;
+    p.grad_stride = p.grad_ld * (c.few ? p.piece : c.rows);
+    at += padded(c.grad_terms * p.grad_stride * 2);
     p.hidden = at;
     if (want_hidden && (p.hidden_splits > 1 || p.piece < c.vocab))
         at += padded(p.hidden_splits * c.rows * p.part_ld * 4);
@@ -535,16 +545,19 @@ CAM_API int cam_head_logprobs(int64_t rows, int64_t vocab, int64_t width, const 
         TileProduct t{};
         t.a = operand(c, c.hidden, rows, c.x_direct, ws + p.x, false);
         t.b = operand(c, piece, n, c.w_direct, ws + p.w, false);
+        if (c.few) std::swap(t.a, t.b);
         t.splits = 1;
-        t.out.stats = stats + at / 128 * rows;
+        t.out.stats = stats + at / (c.few ? 32 : 128) * rows;
         t.out.mine = mine;
         t.out.tokens = tokens;
         t.out.token0 = at;
         t.out.vocab = vocab;
-        if (const int rc = tile_products(fn, &t, 1, false, c.pair, kTileStats, sms, s)) return rc;
+        if (const int rc = tile_products(fn, &t, 1, false, c.pair, c.few ? kTileStatsFew : kTileStats,
+                                         sms, s))
+            return rc;
     }
     if (ce == cudaSuccess) {
-        StatArgs a{stats, (vocab + 127) / 128, rows, vocab, mine, tokens, logp, entropy, lse, lse_lo};
+        StatArgs a{stats, stat_parts(c), rows, vocab, mine, tokens, logp, entropy, lse, lse_lo};
         ce = rows <= 64 ? launch(stats_kernel<1>, rows, a, s)
                         : launch(stats_kernel<8>, (rows + 7) / 8, a, s);
     }
@@ -626,11 +639,12 @@ CAM_API int cam_head_logprobs_backward(int64_t rows, int64_t vocab, int64_t widt
         TileProduct t{};
         t.a = operand(c, c.hidden, rows, false, ws + p.x, false);
         t.b = operand(c, piece, n, c.w_direct, ws + p.w, false);
+        if (c.few) std::swap(t.a, t.b);
         t.splits = 1;
         t.out.y = ws + p.grad;
-        t.out.ldy = p.piece;
+        t.out.ldy = p.grad_ld;
         t.out.planes = c.grad_terms;
-        t.out.plane_stride = rows * p.piece;
+        t.out.plane_stride = p.grad_stride;
         t.out.tokens = tokens;
         t.out.token0 = at;
         t.out.vocab = vocab;
@@ -639,13 +653,15 @@ CAM_API int cam_head_logprobs_backward(int64_t rows, int64_t vocab, int64_t widt
         t.out.entropy = entropy;
         t.out.g = grad_logp;
         t.out.h = grad_entropy;
-        if (const int rc = tile_products(fn, &t, 1, false, c.pair, kTileGrad, sms, s)) return rc;
+        if (const int rc = tile_products(fn, &t, 1, false, c.pair, c.few ? kTileGradFew : kTileGrad, sms,
+                                         s))
+            return rc;
 
         TileOperand grad{};
         grad.base = ws + p.grad;
-        grad.ld = p.piece;
+        grad.ld = p.grad_ld;
         grad.planes = c.grad_terms;
-        grad.plane_stride = rows * p.piece;
+        grad.plane_stride = p.grad_stride;
         TileProduct both[2] = {};
         int count = 0;
         if (grad_hidden) {
@@ -653,6 +669,7 @@ CAM_API int cam_head_logprobs_backward(int64_t rows, int64_t vocab, int64_t widt
             q.a = grad;
             q.a.rows = rows;
             q.a.k = n;
+            q.a.mn_major = c.few;
             q.b = operand(c, piece, n, c.w_direct, ws + p.w, true);
             q.splits = p.hidden_splits;
             if (parts) {
@@ -670,7 +687,7 @@ CAM_API int cam_head_logprobs_backward(int64_t rows, int64_t vocab, int64_t widt
             q.a = grad;
             q.a.rows = n;
             q.a.k = rows;
-            q.a.mn_major = true;
+            q.a.mn_major = !c.few;
             q.b = operand(c, c.hidden, rows, false, ws + p.x, true);
             q.splits = p.head_splits;
             if (p.head_splits > 1) {

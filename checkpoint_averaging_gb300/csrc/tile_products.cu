@@ -80,9 +80,9 @@ struct alignas(128) Args {
     int32_t n_prob, n_units;
 };
 
-template <bool E4M3, bool PAIR>
+template <bool E4M3, bool PAIR, bool FEW = false>
 struct Geo {
-    static constexpr int kCols = E4M3 ? kTileCols8 : kTileCols;
+    static constexpr int kCols = E4M3 ? kTileCols8 : FEW ? kTileFew : kTileCols;
     static constexpr int kBCols = PAIR ? kCols / 2 : kCols;  // B rows an SM stages
     static constexpr int kABytes = kRows * kStepBytes;
     static constexpr int kBBytes = kBCols * kStepBytes;
@@ -161,9 +161,9 @@ __device__ __forceinline__ void commit(uint32_t bar) {
 // Instruction descriptors: fp32 accumulator; bf16 operands (formats 1, majorness in bits
 // 15 and 16), or e4m3 operands (formats 0) with one UE8M0 scale per 32 elements of K (bit
 // 23), scale bytes 0 of their words. N / 8 in bits 17-22, M / 16 in bits 24-28.
-template <bool E4M3, bool PAIR>
+template <bool E4M3, bool PAIR, bool FEW>
 __device__ __forceinline__ uint32_t instruction(uint32_t a_mn, uint32_t b_mn) {
-    constexpr uint32_t n = Geo<E4M3, PAIR>::kCols >> 3, m = (PAIR ? 256 : 128) >> 4;
+    constexpr uint32_t n = Geo<E4M3, PAIR, FEW>::kCols >> 3, m = (PAIR ? 256 : 128) >> 4;
     if constexpr (E4M3)
         return (n << 17) | (1u << 23) | (m << 24);
     else
@@ -331,12 +331,80 @@ __device__ __forceinline__ float exp_exact(float d, float rest) {
     return fmaf(e, c * 0.69314718f, e);
 }
 
+// 1 - exp(d) for d near 0 and below, p = exp(d): the Taylor series of exp(d) - 1 where the
+// difference would cancel (its next term is below 2^-30 of the sum there).
+__device__ __forceinline__ float one_minus_exp(float d, float p) {
+    if (!(d > -0.35f)) return 1.0f - p;
+    float s = fmaf(d, 1.0f / 8, 1.0f);
+    s = fmaf(d * (1.0f / 7), s, 1.0f);
+    s = fmaf(d * (1.0f / 6), s, 1.0f);
+    s = fmaf(d * (1.0f / 5), s, 1.0f);
+    s = fmaf(d * (1.0f / 4), s, 1.0f);
+    s = fmaf(d * (1.0f / 3), s, 1.0f);
+    s = fmaf(d * (1.0f / 2), s, 1.0f);
+    return -d * s;
+}
+
+// What a row of logits brings to its gradient g (1[j = token] - p_j) - h p_j (log p_j + H).
+struct GradRow {
+    float lse, lo;  // log p = (x - lse) - lo
+    float g, h, H;
+    float shift;    // the quick form: p = 2^(x log2(e) - shift), G = p (base - h x)
+    float base;
+    int32_t token;  // its column (the row of D for few rows), or -1
+};
+
+__device__ __forceinline__ GradRow grad_row(const TileOut& o, int64_t row, int64_t n) {
+    GradRow r;
+    const int64_t token = o.tokens ? o.tokens[row] : -1;
+    r.lse = o.lse[row];
+    r.lo = o.lse_lo ? o.lse_lo[row] : 0.0f;
+    r.g = o.g && token >= 0 ? o.g[row] : 0.0f;
+    r.h = o.h ? o.h[row] : 0.0f;
+    r.H = o.h ? o.entropy[row] : 0.0f;
+    // (a token that the vocabulary does not have)
+    if (r.g != 0.0f && token >= o.vocab) r.lse = __int_as_float(0x7FC00000);
+    // no gradient: zeros, whatever lse is (the row's logits are zeros: head.cu)
+    if (r.g == 0.0f && r.h == 0.0f) r.lse = r.lo = r.H = 0.0f;
+    r.shift = (r.lse + r.lo) * kLog2e;
+    r.base = r.h * (r.lse - r.H) - r.g;
+    const int64_t at = token - o.token0;
+    r.token = at >= 0 && at < n ? static_cast<int32_t>(at) : -1;
+    return r;
+}
+
+// The gradient of the logit of the row's own token.
+__device__ __forceinline__ float own_grad(float x, const GradRow& r) {
+    const float d = (x - r.lse) - r.lo, p = exp_exact(d, 0.0f);
+    return r.g * one_minus_exp(d, p) - r.h * p * (d + r.H);
+}
+
+// That of another's. FINE: for fp32 results, with all that matters there of d's rounding.
+// Otherwise p is off by 2^-24 of lse log2(e), a hundredth of what rounding G to bf16 costs.
+template <bool FINE>
+__device__ __forceinline__ float other_grad(float x, const GradRow& r) {
+    if constexpr (FINE) {
+        float d = x - r.lse;
+        const float b = x - d;  // (x - lse) - d, exactly: two-sum
+        const float rest = ((x - (d + b)) + (b - r.lse)) - r.lo;
+        const float p = exp_exact(d, rest);
+        return -p * fmaf(r.h, (d + rest) + r.H, r.g);
+    } else {
+        return exp2_fast(fmaf(x, kLog2e, -r.shift)) * fmaf(-r.h, x, r.base);
+    }
+}
+
 // The element of 32 at a place known at run time.
 __device__ __forceinline__ float pick(const float* v, int64_t at) {
     float x = v[0];
 #pragma unroll
     for (int i = 1; i < 32; ++i) x = at == i ? v[i] : x;
     return x;
+}
+
+__device__ __forceinline__ void put(float* v, int at, float x) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = at == i ? x : v[i];
 }
 
 // A row's statistics over a tile's columns, 32 at a time. The exponentials are relative to
@@ -371,11 +439,110 @@ struct RowStat {
     }
 };
 
+// ---- few rows: the vocabulary along the lanes, the rows along the columns ----------------
+
+// Sums of 32 values over the lanes, value i's in lane i: at each step a lane keeps half of
+// its values and adds the other lane's of those.
+__device__ __forceinline__ float sums_to_lanes(float* v, int lane) {
+#pragma unroll
+    for (int by = 16; by >= 1; by /= 2) {
+        const bool upper = lane & by;
+#pragma unroll
+        for (int j = 0; j < by; ++j) {
+            const float away = upper ? v[j] : v[j + by], keep = upper ? v[j + by] : v[j];
+            v[j] = keep + __shfl_xor_sync(0xFFFFFFFFu, away, by);
+        }
+    }
+    return v[0];
+}
+
+// Statistics of up to 32 rows of logits (v: this lane's logit of each) over 32 tokens of the
+// vocabulary.
+__device__ __forceinline__ void few_stats(const TileOut& o, const Prob& P, float* v, int64_t row0,
+                                          int64_t col0, bool in, int lane) {
+    const int n = P.N - col0 < 32 ? int(P.N - col0) : 32;
+    // the logits of the rows' tokens: each is met by one warp
+    const int64_t token = lane < n && o.tokens ? o.tokens[col0 + lane] - o.token0 - row0 : -1;
+    uint32_t here = __ballot_sync(0xFFFFFFFFu, token >= 0 && token < 32 && row0 + token < P.M);
+    while (here) {
+        const int i = __ffs(here) - 1;
+        here &= here - 1;
+        const int at = __shfl_sync(0xFFFFFFFFu, static_cast<int>(token), i);
+        const float x = pick(v, i);
+        if (lane == at) o.mine[col0 + i] = x;
+    }
+    float t[32], m = 0.0f, c = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        t[i] = 0.0f;
+        if (i < n) {
+            // the largest, by an order of the bits as whole numbers
+            const int bits = __float_as_int(v[i]);
+            const int key = in ? bits ^ ((bits >> 31) & 0x7FFFFFFF) : INT_MIN;
+            const int top_key = __reduce_max_sync(0xFFFFFFFFu, key);
+            const float top = __int_as_float(top_key ^ ((top_key >> 31) & 0x7FFFFFFF));
+            const float d = v[i] - top, e = exp2_fast(d * kLog2e);
+            const bool below = d < 0.0f;
+            const uint32_t equal = __ballot_sync(0xFFFFFFFFu, in && !below);
+            if (lane == i) {
+                m = top;
+                c = static_cast<float>(__popc(equal));
+            }
+            t[i] = in ? e * d : 0.0f;
+            v[i] = in && below ? e : 0.0f;
+        } else {
+            v[i] = 0.0f;
+        }
+    }
+    const float a = sums_to_lanes(v, lane), s = sums_to_lanes(t, lane);
+    if (lane < n) o.stats[row0 / 32 * P.N + col0 + lane] = TileStat{m, a, c, s};
+}
+
+// The gradient of one token's logits in up to 32 rows.
+__device__ __forceinline__ void few_grad(const TileOut& o, const Prob& P, const GradRow* rows, float* v,
+                                         int64_t token, int64_t col0, bool in) {
+    const int n = P.N - col0 < 32 ? int(P.N - col0) : 32;
+    uint32_t own = 0;  // the rows whose token this is
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        if (i < n && rows[i].token == int(token)) own |= 1u << i;
+    for (uint32_t left = own; left; left &= left - 1) {
+        const int i = __ffs(left) - 1;
+        put(v, i, own_grad(pick(v, i), rows[i]));
+    }
+    const bool fine = o.planes == 3;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        if (i >= n) {
+            v[i] = 0.0f;
+        } else {
+            const GradRow r = rows[i];
+            const float w = fine ? other_grad<true>(v[i], r) : other_grad<false>(v[i], r);
+            v[i] = own >> i & 1 ? v[i] : w;
+        }
+    }
+    if (!in) return;
+    __nv_bfloat16* y = static_cast<__nv_bfloat16*>(o.y) + token * o.ldy + col0;
+    for (int k = 0; k < o.planes; ++k) {
+#pragma unroll
+        for (int j = 0; j < 32; j += 8) {
+            if (j >= n) break;
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = bf16x2(v[j + 2 * i], v[j + 2 * i + 1]);
+            *reinterpret_cast<uint4*>(y + k * o.plane_stride + j) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] -= __bfloat162float(__float2bfloat16_rn(v[i]));
+    }
+}
+
 // ---- the kernel ------------------------------------------------------------------------
 
 template <bool E4M3, bool PAIR, int EPI>
 __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant__ Args a) {
-    using G = Geo<E4M3, PAIR>;
+    constexpr bool kFew = EPI == kTileStatsFew || EPI == kTileGradFew;
+    using G = Geo<E4M3, PAIR, kFew>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -509,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         for (int u = worker; u < a.n_units && ok; u += workers) {
             const Unit t = unit_of(a, u);
             const Prob& P = a.prob[t.p];
-            const uint32_t idesc = instruction<E4M3, PAIR>(P.a_mn, P.b_mn);
+            const uint32_t idesc = instruction<E4M3, PAIR, kFew>(P.a_mn, P.b_mn);
             // 32 bytes further along a K-major row, or 16 rows further down an MN-major box
             const uint64_t step_a = P.a_mn ? 16 * kStepBytes / 16 : 2;
             const uint64_t step_b = P.b_mn ? 16 * kStepBytes / 16 : 2;
@@ -580,6 +747,12 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         int acc = 0;
         uint32_t acc_phase = 0;
         bool ok = true;
+        GradRow* few_rows = reinterpret_cast<GradRow*>(smem + G::kTurnAt);
+        if constexpr (EPI == kTileGradFew) {  // the rows' data, for every thread of the epilogue
+            const int i = threadIdx.x - 64;
+            if (i < a.prob[0].N) few_rows[i] = grad_row(a.prob[0].o, i, a.prob[0].M);
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+        }
         for (int u = worker; u < a.n_units && ok; u += workers) {
             const Unit t = unit_of(a, u);
             const Prob& P = a.prob[t.p];
@@ -590,27 +763,14 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
             const int64_t col0 = int64_t(t.nt) * G::kCols + half * kHalf;
             const bool in = row < P.M;
             // what a row brings, asked for before its tile is done
-            float lse = 0, lo = 0, H = 0, g = 0, h = 0;
-            int64_t token = -1;
-            if constexpr (EPI != kTileOut) {
-                if (in && o.tokens) token = o.tokens[row];
+            int64_t token = -1;  // its column in this product
+            GradRow mine;
+            if constexpr (EPI == kTileStats) {
+                if (in && o.tokens) token = o.tokens[row] - o.token0;
             }
-            bool skip = false;  // kTileGrad: a row without a gradient gets zeros
             if constexpr (EPI == kTileGrad) {
-                if (in) {
-                    lse = o.lse[row];
-                    if (o.lse_lo) lo = o.lse_lo[row];
-                    if (o.g && token >= 0) g = o.g[row];
-                    if (o.h) {
-                        h = o.h[row];
-                        H = o.entropy[row];
-                    }
-                }
-                skip = g == 0.0f && h == 0.0f;
-                // (a token that the vocabulary does not have)
-                if (g != 0.0f && token >= o.vocab) lse = __int_as_float(0x7FC00000);
+                if (in) mine = grad_row(o, row, P.N);
             }
-            if constexpr (EPI != kTileOut) token -= o.token0;  // its column in this product
             const bool work = row0 < P.M && col0 < P.N;  // (of the warp)
             // the thread's part of the row, summed over the runs of K
             float sum[kHalf];
@@ -651,6 +811,14 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
             }
             if (!ok) break;
             if (!work) continue;
+            if constexpr (EPI == kTileStatsFew) {
+                few_stats(o, P, sum, row0, col0, in, lane);
+                continue;
+            }
+            if constexpr (EPI == kTileGradFew) {
+                few_grad(o, P, few_rows + col0, sum, row, col0, in);
+                continue;
+            }
             RowStat stat;
             stat.m = stat.a = stat.c = stat.t = 0.0f;
 #pragma unroll
@@ -665,25 +833,19 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                     const int64_t at = token - col;
                     if (in && at >= 0 && at < n) o.mine[row] = pick(v, at);
                 } else if constexpr (EPI == kTileGrad) {
-                    const int64_t at = token - col;
-                    float hit = 0.0f;  // g (1 - p) of the row's token, without cancellation
-                    if (at >= 0 && at < n) hit = -g * expm1f((pick(v, at) - lse) - lo);
-                    const bool fine = o.planes == 3;
+                    int own = -1;  // the row's token, if it is among these
+                    if (mine.token >= 0 && mine.token - int(col) >= 0 && mine.token - int(col) < 32) {
+                        own = mine.token - int(col);
+                        put(v, own, own_grad(pick(v, own), mine));
+                    }
+                    if (o.planes == 3) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        float d = v[i] - lse, p;
-                        if (fine) {
-                            const float b = v[i] - d;  // (v - lse) - d, exactly: two-sum
-                            const float rest = ((v[i] - (d + b)) + (b - lse)) - lo;
-                            p = exp_exact(d, rest);
-                            d += rest;
-                        } else {
-                            d -= lo;
-                            p = exp2_fast(d * kLog2e);
-                        }
-                        float w = at == i ? hit : -g * p;
-                        if (o.h) w -= h * p * (d + H);
-                        v[i] = skip ? 0.0f : w;
+                        for (int i = 0; i < 32; ++i)
+                            v[i] = own == i ? v[i] : other_grad<true>(v[i], mine);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            v[i] = own == i ? v[i] : other_grad<false>(v[i], mine);
                     }
                     if (in) {
                         __nv_bfloat16* y = static_cast<__nv_bfloat16*>(o.y) + row * o.ldy + col;
@@ -789,7 +951,7 @@ bool operand_map8(CUtensorMap* map, CUtensorMap* scales, const TileOperand& o, i
 
 template <bool E4M3, bool PAIR, int EPI>
 cudaError_t launch(const Args& a, int sms, cudaStream_t s) {
-    using G = Geo<E4M3, PAIR>;
+    using G = Geo<E4M3, PAIR, EPI == kTileStatsFew || EPI == kTileGradFew>;
     static std::atomic<uint64_t> allowed{0};
     auto* kernel = tile_kernel<E4M3, PAIR, EPI>;
     int dev = 0;
@@ -819,7 +981,9 @@ cudaError_t launch_any(const Args& a, bool e4m3, TileEpilogue epi, int sms, cuda
     switch (epi) {
         case kTileOut: return launch<false, PAIR, kTileOut>(a, sms, s);
         case kTileStats: return launch<false, PAIR, kTileStats>(a, sms, s);
-        default: return launch<false, PAIR, kTileGrad>(a, sms, s);
+        case kTileGrad: return launch<false, PAIR, kTileGrad>(a, sms, s);
+        case kTileStatsFew: return launch<false, false, kTileStatsFew>(a, sms, s);
+        default: return launch<false, false, kTileGradFew>(a, sms, s);
     }
 }
 
@@ -831,7 +995,9 @@ int tile_products(const char* fn, const TileProduct* ps, int n, bool e4m3, bool 
     using namespace tc;
     Args a;
     std::memset(&a, 0, sizeof a);
-    const int cols = e4m3 ? kTileCols8 : kTileCols, rows = tile_rows(pair);
+    const bool few = epilogue == kTileStatsFew || epilogue == kTileGradFew;
+    if (few) pair = false;
+    const int cols = e4m3 ? kTileCols8 : few ? kTileFew : kTileCols, rows = tile_rows(pair);
     const int b_rows = pair ? cols / 2 : cols;
     int32_t units = 0;
     for (int i = 0; i < n; ++i) {
@@ -865,7 +1031,8 @@ int tile_products(const char* fn, const TileProduct* ps, int n, bool e4m3, bool 
         // (of 512: 3 % slower), e4m3 ones' of 2,048 (their steps add twice as many terms); bf16
         // results of bf16 inputs hide what a long run loses.
         P.main0 = P.steps * (pairs - 1);
-        P.run = pairs > 1 ? 4 : e4m3 ? 16 : epilogue == kTileStats ? 12 : INT_MAX;
+        P.run = pairs > 1 ? 4 : e4m3 ? 16 : epilogue == kTileStats || epilogue == kTileStatsFew ? 12
+                                                                                   : INT_MAX;
         const int splits = std::max(1, std::min(p.splits, P.all_steps));
         P.per_split = (P.all_steps + splits - 1) / splits;
         P.unit0 = units;

@@ -29,6 +29,10 @@ enum TileEpilogue : int {
     kTileOut = 0,    // D stored in fp32 or bf16, or added into fp32 partials
     kTileStats = 1,  // softmax statistics of D's rows (logits)
     kTileGrad = 2,   // the logits' gradient, in bf16 terms
+    // The same for few rows of logits, which are D's columns (at most kTileFew), the
+    // vocabulary its rows: D^T's statistics by 32 tokens of the vocabulary, and G^T.
+    kTileStatsFew = 3,
+    kTileGradFew = 4,
 };
 
 // What kTileStats leaves of a row and half a tile of columns: the largest logit m,
@@ -48,7 +52,8 @@ struct TileOut {
     float* part;
     int64_t part_ld;
     // kTileStats: stats[tile of columns * 2 + half][M]; `mine` [M] takes the logit of each
-    // row's token. kTileGrad: G into `planes` terms of y (bf16, row stride ldy).
+    // row's token. kTileGrad: G into `planes` terms of y (bf16, row stride ldy). Few rows:
+    // stats[row of D / 32][N], and G^T (rows of a multiple of eight elements).
     TileStat* stats;
     float* mine;
     const int64_t* tokens;
@@ -67,6 +72,7 @@ struct TileProduct {
 
 constexpr int kTileCols = 256;   // columns of a bf16 tile
 constexpr int kTileCols8 = 192;  // of an e4m3 tile
+constexpr int kTileFew = 64;     // rows of logits that take the forms for few rows
 
 // Rows of a tile: a pair of SMs takes 256, one SM 128 (for few rows).
 inline int tile_rows(bool pair) { return pair ? 256 : 128; }
