@@ -20,11 +20,25 @@ import torch
 from . import binding as _b
 from . import operators as _o
 
-_CODES, _empty, _FLOAT = _o._CODES, torch.empty, torch.float32
+_CODES, _empty, _FLOAT, _BYTE = _o._CODES, torch.empty, torch.float32, torch.uint8
 _L = _b.lib()
 _current_device, _current_stream = _o._current_device, _o._current_stream
 _pack8, _unpack8, _matmul8 = _L.cam_pack8, _L.cam_unpack8, _L.cam_matmul8
 _head, _head_backward = _L.cam_head_logprobs, _L.cam_head_logprobs_backward
+
+
+# Workspaces by what decides their size (shapes, strides, dtypes, alignment): asking the library
+# takes as long as an allocation.
+_SIZES: dict = {}
+
+
+def _workspace(key, query, *args):
+    size = _SIZES.get(key)
+    if size is None:
+        if len(_SIZES) > 4096:
+            _SIZES.clear()
+        size = _SIZES[key] = _bytes(query, *args)
+    return size
 
 
 def _bytes(query, *args) -> int:
@@ -86,9 +100,11 @@ def pack8(weight, *, stream=None) -> Packed8:
     if device != _current_device():
         with torch.cuda.device(device):
             return pack8(weight)
-    data = _empty(pack8_bytes(rows, cols), dtype=torch.uint8, device=weight.device)
-    _b._check(_pack8(rows, cols, weight.data_ptr(), ld, code, data.data_ptr(),
-                     _current_stream(device)))
+    size = _workspace((rows, cols), _L.cam_pack8_bytes, rows, cols)
+    data = _empty(size, dtype=_BYTE, device=weight.device)
+    rc = _pack8(rows, cols, weight.data_ptr(), ld, code, data.data_ptr(), _current_stream(device))
+    if rc:
+        _b._check(rc)
     return Packed8.__new__(Packed8)._set(data, rows, cols, device)
 
 
@@ -120,7 +136,25 @@ def matmul8(x, packed: Packed8, *, out=None, out_dtype=None, stream=None):
     [tokens, rows] in x's dtype (or `out_dtype`, or into `out`). There is no
     gradient, and an x that requires one is refused while gradients are
     recorded."""
-    _no_gradient("matmul8", "detach it", x)
+    if x.requires_grad:
+        _no_gradient("matmul8", "detach it", x)
+    if out is None and out_dtype is None and stream is None:
+        # the common call, with every check of the general one below
+        code, shape, device = _CODES.get(x.dtype), x.shape, packed._device
+        if code is not None and len(shape) == 2 and x.get_device() == device == _current_device():
+            tokens, cols = shape
+            ld, step = x.stride()
+            if cols == packed._cols and step == 1 and ld >= cols:
+                rows, place = packed._rows, packed._place
+                size = _workspace((tokens, rows, cols), _L.cam_matmul8_workspace, tokens, rows, cols)
+                y = _empty((tokens, rows), dtype=x.dtype, device=place)
+                space = _empty(size, dtype=_BYTE, device=place)
+                rc = _matmul8(tokens, rows, cols, x.data_ptr(), ld, code, packed._data.data_ptr(),
+                              y.data_ptr(), rows, code, space.data_ptr(), size,
+                              _current_stream(device))
+                if rc:
+                    _b._check(rc)
+                return y
     if x.dim() == 1:
         if out is not None:
             matmul8(x.unsqueeze(0), packed, out=out.unsqueeze(0) if out.dim() == 1 else out,
@@ -148,7 +182,7 @@ def matmul8(x, packed: Packed8, *, out=None, out_dtype=None, stream=None):
         raise ValueError("out must match x and the matrix")
     _, _, ld_y, code_y = _o._matrix(y, "out")
     _o._same_device(device, y)
-    size = _bytes(_L.cam_matmul8_workspace, tokens, rows, cols)
+    size = _workspace((tokens, rows, cols), _L.cam_matmul8_workspace, tokens, rows, cols)
     space = _empty(size, dtype=torch.uint8, device=x.device)
     _b._check(_matmul8(tokens, rows, cols, x.data_ptr(), ld, code, packed._data.data_ptr(),
                        y.data_ptr(), ld_y, code_y, space.data_ptr(), size,
@@ -178,22 +212,26 @@ def head_logprobs(hidden, head, tokens=None, *, stream=None) -> _o.TokenLogprobs
     (`top`) are looked for. There is no gradient: inputs that require one are
     refused while gradients are recorded (probe.differentiable_head_logprobs)."""
     rows, vocab, width, ld_x, ld_w, code, device = _head_inputs(hidden, head, tokens)
-    _no_gradient("head_logprobs", "take probe.differentiable_head_logprobs", hidden, head)
+    if hidden.requires_grad or head.requires_grad:
+        _no_gradient("head_logprobs", "take probe.differentiable_head_logprobs", hidden, head)
     if stream is not None:
         return _o._on_stream(stream, device, lambda: head_logprobs(hidden, head, tokens),
                              (hidden, head, tokens), lambda r: (r._stats,))
     if device != _current_device():
         with torch.cuda.device(device):
             return head_logprobs(hidden, head, tokens)
-    x, w = hidden.data_ptr(), head.data_ptr()
-    stats = _empty((4, rows), dtype=_FLOAT, device=hidden.device)  # logp, entropy, lse, lse_lo
+    x, w, place = hidden.data_ptr(), head.data_ptr(), hidden.device
+    stats = _empty((4, rows), dtype=_FLOAT, device=place)  # logp, entropy, lse, lse_lo
     at = stats.data_ptr()
-    size = _bytes(_L.cam_head_logprobs_workspace, rows, vocab, width, x, ld_x, w, ld_w, code)
-    space = _empty(size, dtype=torch.uint8, device=hidden.device)
-    _b._check(_head(rows, vocab, width, x, ld_x, w, ld_w, code,
-                    None if tokens is None else tokens.data_ptr(), None if tokens is None else at,
-                    at + 4 * rows, at + 8 * rows, at + 12 * rows, space.data_ptr(), size,
-                    _current_stream(device)))
+    size = _workspace((rows, vocab, width, x % 16, ld_x, w % 16, ld_w, code),
+                      _L.cam_head_logprobs_workspace, rows, vocab, width, x, ld_x, w, ld_w, code)
+    space = _empty(size, dtype=_BYTE, device=place)
+    at_token = None if tokens is None else tokens.data_ptr()
+    rc = _head(rows, vocab, width, x, ld_x, w, ld_w, code, at_token,
+               None if at_token is None else at, at + 4 * rows, at + 8 * rows, at + 12 * rows,
+               space.data_ptr(), size, _current_stream(device))
+    if rc:
+        _b._check(rc)
     return _o.TokenLogprobs(stats, tokens is not None, None, None)
 
 
@@ -224,19 +262,23 @@ def head_logprobs_backward(hidden, head, tokens, lse, entropy, grad_logp=None, g
     at_entropy = _o._row_value(entropy, shape, device)
     at_g, at_h = _o._row_value(grad_logp, shape, device), _o._row_value(grad_entropy, shape, device)
     grad_hidden = grad_head = at_hidden = at_head = None
+    place = hidden.device
     if need_hidden:
-        grad_hidden = _empty((rows, width), dtype=hidden.dtype, device=hidden.device)
+        grad_hidden = _empty((rows, width), dtype=hidden.dtype, device=place)
         at_hidden = grad_hidden.data_ptr()
     if need_head:
-        grad_head = _empty((vocab, width), dtype=head.dtype, device=hidden.device)
+        grad_head = _empty((vocab, width), dtype=head.dtype, device=place)
         at_head = grad_head.data_ptr()
-    size = _bytes(_L.cam_head_logprobs_backward_workspace, rows, vocab, width, head.data_ptr(), ld_w,
-                  code)
-    space = _empty(size, dtype=torch.uint8, device=hidden.device)
-    _b._check(_head_backward(rows, vocab, width, hidden.data_ptr(), ld_x, head.data_ptr(), ld_w, code,
-                             None if tokens is None else tokens.data_ptr(), at_lse, at_lo, at_entropy,
-                             at_g, at_h, at_hidden, width, at_head, width, space.data_ptr(), size,
-                             _current_stream(device)))
+    w = head.data_ptr()
+    size = _workspace((rows, vocab, width, w % 16, ld_w, code, device),
+                      _L.cam_head_logprobs_backward_workspace, rows, vocab, width, w, ld_w, code)
+    space = _empty(size, dtype=_BYTE, device=place)
+    rc = _head_backward(rows, vocab, width, hidden.data_ptr(), ld_x, w, ld_w, code,
+                        None if tokens is None else tokens.data_ptr(), at_lse, at_lo, at_entropy,
+                        at_g, at_h, at_hidden, width, at_head, width, space.data_ptr(), size,
+                        _current_stream(device))
+    if rc:
+        _b._check(rc)
     return grad_hidden, grad_head
 
 
