@@ -54,22 +54,26 @@ constexpr int kThreads = 320;    // ten warps
 constexpr int kEpilogueWarps = 8;
 constexpr int kStepBytes = 128;  // bytes of K per stage
 constexpr int kMnBox = 64 * kStepBytes;  // MN-major box: 64 K rows of 64 elements
-constexpr int kRing = 208 * 1024;
-// A warp's buffer for storing rows that do not start on 32 bytes: 32 rows of 16 columns, and
-// a word between rows so that a column's words lie in as many banks.
+constexpr int kRing = 192 * 1024;
+// A warp's buffer for results: two boxes of 32 rows of 64 bytes, which TMA stores; or, where
+// rows do not start on 16 bytes, 32 rows of 16 words and one more between rows, so that a
+// column's words lie in as many banks.
+constexpr int kBox = 32 * 64;
 constexpr int kTurn = 17;
-constexpr int kTurnBytes = kEpilogueWarps * 32 * kTurn * 4;
+constexpr int kOutBytes = kEpilogueWarps * 2 * kBox;
+static_assert(32 * kTurn * 4 <= 2 * kBox, "both forms share the buffer");
 
 struct alignas(128) Prob {
     CUtensorMap ta, tb;    // operands
     CUtensorMap tsa, tsb;  // e4m3: their scales
+    CUtensorMap ty;        // results: boxes of 64 bytes by 32 rows
     int32_t m_tiles, n_tiles, m_fast;
     int32_t steps;         // K steps of one pair of terms
     int32_t all_steps, per_split;
     int32_t main0, run;    // from step main0 on, accumulated in runs of `run` steps
     int32_t a_mn, b_mn;
     int32_t unit0;
-    int32_t wide;          // rows of o.y start on 32 bytes
+    int32_t boxes;         // results go through ty
     uint32_t terms_a, terms_b;  // the terms of each pair, four bits each
     int64_t M, N;
     TileOut o;
@@ -92,8 +96,8 @@ struct Geo {
     static constexpr int kStage = (kTx + 1023) / 1024 * 1024;
     static constexpr int kStages = kRing / kStage < 8 ? kRing / kStage : 8;
     static constexpr int kBars = 2 * kStages + 5;
-    static constexpr int kTurnAt = kStages * kStage;
-    static constexpr int kBarsAt = kTurnAt + kTurnBytes;
+    static constexpr int kOutAt = kStages * kStage;
+    static constexpr int kBarsAt = kOutAt + kOutBytes;
     static constexpr int kSmem = kBarsAt + 8 * kBars + 16 + 1024;
     static_assert(kSmem <= kMaxSharedBytes, "over the per-block shared memory limit");
 };
@@ -267,30 +271,54 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Eight 32-bit words to a 32-byte aligned address.
-__device__ __forceinline__ void store8(void* p, const uint32_t* w) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
-                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
-}
-
-// 32 columns of a row as bf16 to a 32-byte aligned address.
-__device__ __forceinline__ void store_bf16(__nv_bfloat16* y, const float* v) {
+// 64 bytes of each of 32 rows, this lane's in w, to the box at (x, y, z) by TMA: rows and
+// columns past the matrix are left out. (Stored by the threads themselves, a row each, a
+// 32-byte store of a warp is 32 passes of the load/store unit.)
+__device__ __forceinline__ void store_box(const CUtensorMap* map, uint32_t buf, int& which,
+                                          const uint32_t* w, int lane, int x, int y, int z, bool add) {
+    if (elect_one()) bulk_wait_read1();  // the box before the last has been read
+    __syncwarp();
+    const uint32_t box = buf + which * kBox, row = box + lane * 64;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        uint32_t w[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = bf16x2(v[16 * k + 2 * i], v[16 * k + 2 * i + 1]);
-        store8(y + 16 * k, w);
+    for (int q = 0; q < 4; ++q)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + 16 * (q ^ ((lane >> 1) & 3))),
+                     "r"(w[4 * q]), "r"(w[4 * q + 1]), "r"(w[4 * q + 2]), "r"(w[4 * q + 3])
+                     : "memory");
+    fence_async_smem();
+    __syncwarp();
+    if (elect_one()) {
+        if (add)
+            asm volatile(
+                "cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group "
+                "[%0, {%2, %3, %4}], [%1];" ::"l"(reinterpret_cast<uint64_t>(map)),
+                "r"(box), "r"(x), "r"(y), "r"(z)
+                : "memory");
+        else
+            tma_store(map, box, x, y, z);
+        bulk_commit();
     }
+    which ^= 1;
 }
 
-// Eight columns of a row to a 32-byte aligned address.
-__device__ __forceinline__ void store_f32(float* y, const float* v) {
-    uint32_t w[8];
+// 32 columns of 32 rows, this lane's row in v, as bf16 or fp32.
+__device__ __forceinline__ void store_bf16(const CUtensorMap* map, uint32_t buf, int& which,
+                                           const float* v, int lane, int x, int y, int z) {
+    uint32_t w[16];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) w[k] = __float_as_uint(v[k]);
-    store8(y, w);
+    for (int i = 0; i < 16; ++i) w[i] = bf16x2(v[2 * i], v[2 * i + 1]);
+    store_box(map, buf, which, w, lane, x, y, z, false);
+}
+__device__ __forceinline__ void store_f32(const CUtensorMap* map, uint32_t buf, int& which,
+                                          const float* v, int n, int lane, int x, int y, int z,
+                                          bool add) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if (16 * h >= n) break;
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(v[16 * h + i]);
+        store_box(map, buf, which, w, lane, x + 16 * h, y, z, add);
+    }
 }
 
 // 32 columns of 32 rows, this lane's row in v, to addresses of any alignment: turned in shared
@@ -742,12 +770,15 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     } else if (warp >= 2) {
         // ---- epilogue ----
         const int quarter = warp & 3, half = (warp - 2) >> 2;
-        float* turn = reinterpret_cast<float*>(smem + G::kTurnAt) + (warp - 2) * 32 * kTurn;
+        uint8_t* out_at = smem + G::kOutAt + (warp - 2) * 2 * kBox;
+        const uint32_t out_buf = su32(out_at);
+        float* turn = reinterpret_cast<float*>(out_at);
+        int which = 0;
         constexpr int kHalf = G::kCols / 2, kGroups = kHalf / 32;
         int acc = 0;
         uint32_t acc_phase = 0;
         bool ok = true;
-        GradRow* few_rows = reinterpret_cast<GradRow*>(smem + G::kTurnAt);
+        GradRow* few_rows = reinterpret_cast<GradRow*>(smem + G::kOutAt);
         if constexpr (EPI == kTileGradFew) {  // the rows' data, for every thread of the epilogue
             const int i = threadIdx.x - 64;
             if (i < a.prob[0].N) few_rows[i] = grad_row(a.prob[0].o, i, a.prob[0].M);
@@ -847,43 +878,22 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                         for (int i = 0; i < 32; ++i)
                             v[i] = own == i ? v[i] : other_grad<false>(v[i], mine);
                     }
-                    if (in) {
-                        __nv_bfloat16* y = static_cast<__nv_bfloat16*>(o.y) + row * o.ldy + col;
-                        // (rows of whole tiles: columns past the matrix have room)
-                        for (int k = 0; k < o.planes; ++k) {
-                            store_bf16(y + k * o.plane_stride, v);
-                            if (k + 1 < o.planes) {
+                    for (int k = 0; k < o.planes; ++k) {
+                        store_bf16(&P.ty, out_buf, which, v, lane, int(col), int(row0), k);
+                        if (k + 1 < o.planes) {
 #pragma unroll
-                                for (int i = 0; i < 32; ++i)
-                                    v[i] -= __bfloat162float(__float2bfloat16_rn(v[i]));
-                            }
+                            for (int i = 0; i < 32; ++i)
+                                v[i] -= __bfloat162float(__float2bfloat16_rn(v[i]));
                         }
                     }
-                } else if (o.part) {
-                    if (in) {  // (rows of whole groups of eight columns)
-                        float* y = o.part + (int64_t(t.split) * P.M + row) * o.part_ld + col;
-#pragma unroll
-                        for (int k = 0; k < 32; k += 8) {
-                            if (k >= n) break;
-                            if (o.add) {
-#pragma unroll
-                                for (int i = k; i < k + 8; i += 4) {
-                                    const float4 x = *reinterpret_cast<const float4*>(y + i);
-                                    v[i] += x.x, v[i + 1] += x.y, v[i + 2] += x.z, v[i + 3] += x.w;
-                                }
-                            }
-                            store_f32(y + k, v + k);
-                        }
-                    }
-                } else if (P.wide && n == 32) {
-                    if (in && o.y_bf16) {
-                        store_bf16(static_cast<__nv_bfloat16*>(o.y) + row * o.ldy + col, v);
-                    } else if (in) {
-                        float* y = static_cast<float*>(o.y) + row * o.ldy + col;
-#pragma unroll
-                        for (int k = 0; k < 32; k += 8) store_f32(y + k, v + k);
-                    }
+                } else if (P.boxes) {
+                    if (o.y_bf16)
+                        store_bf16(&P.ty, out_buf, which, v, lane, int(col), int(row0), 0);
+                    else
+                        store_f32(&P.ty, out_buf, which, v, n, lane, int(col), int(row0), t.split,
+                                  o.add != 0);
                 } else {
+                    if (elect_one()) bulk_wait_read0();  // (boxes of the launch's other product)
                     const int rows = P.M - row0 < 32 ? int(P.M - row0) : 32;
                     const int64_t at = row0 * o.ldy + col;
                     if (o.y_bf16)
@@ -898,6 +908,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                         TileStat{stat.m, stat.a, stat.c, stat.t};
             }
         }
+        if (elect_one()) bulk_wait_all();  // stores done before the block (and its buffers) goes
     }
     __syncwarp();
     tc_fence_before();
@@ -921,6 +932,7 @@ bool encode(CUtensorMap* map, CUtensorMapDataType type, const void* base, int64_
             CUtensorMapSwizzle swizzle) {
     const auto enc = encoder();
     if (!enc) return false;
+    if (z == 1) z_bytes = y_bytes;  // (of no use, but below the limit)
     const cuuint64_t dims[3] = {cuuint64_t(x), cuuint64_t(y), cuuint64_t(z)};
     const cuuint64_t strides[2] = {cuuint64_t(y_bytes), cuuint64_t(z_bytes)};
     const cuuint32_t box[3] = {cuuint32_t(box_x), cuuint32_t(box_y), 1};
@@ -1036,8 +1048,21 @@ int tile_products(const char* fn, const TileProduct* ps, int n, bool e4m3, bool 
         const int splits = std::max(1, std::min(p.splits, P.all_steps));
         P.per_split = (P.all_steps + splits - 1) / splits;
         P.unit0 = units;
-        const int64_t size = p.out.y_bf16 ? 2 : 4;
-        P.wide = reinterpret_cast<uintptr_t>(p.out.y) % 32 == 0 && p.out.ldy * size % 32 == 0;
+        if (epilogue == kTileOut || epilogue == kTileGrad) {
+            const bool part = p.out.part != nullptr, bf16 = epilogue == kTileGrad || p.out.y_bf16;
+            const int64_t size = bf16 ? 2 : 4, ld = part ? p.out.part_ld : p.out.ldy;
+            const void* y = part ? p.out.part : p.out.y;
+            const int64_t planes = part ? (P.all_steps + P.per_split - 1) / P.per_split
+                                        : epilogue == kTileGrad ? p.out.planes : 1;
+            const int64_t plane = epilogue == kTileGrad ? p.out.plane_stride : P.M * ld;
+            // (the tensor maps want rows that start on 16 bytes)
+            P.boxes = reinterpret_cast<uintptr_t>(y) % 16 == 0 && ld * size % 16 == 0;
+            if (P.boxes &&
+                !encode(&P.ty, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                        y, P.N, P.M, planes, ld * size, plane * size, static_cast<int>(64 / size), 32,
+                        CU_TENSOR_MAP_SWIZZLE_64B))
+                return record_error(CAM_E_CUDA, "%s: cuTensorMapEncodeTiled failed", fn);
+        }
         P.o = p.out;
         units += P.m_tiles * P.n_tiles * ((P.all_steps + P.per_split - 1) / P.per_split);
     }
