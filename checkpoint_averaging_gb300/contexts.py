@@ -138,7 +138,7 @@ def matmul8(x, packed: Packed8, *, out=None, out_dtype=None, stream=None):
     recorded."""
     if x.requires_grad:
         _no_gradient("matmul8", "detach it", x)
-    if out is None and out_dtype is None and stream is None:
+    if out is None and out_dtype is None and stream is None and x.is_cuda:
         # the common call, with every check of the general one below
         code, shape, device = _CODES.get(x.dtype), x.shape, packed._device
         if code is not None and len(shape) == 2 and x.get_device() == device == _current_device():

@@ -46,36 +46,45 @@ __device__ __forceinline__ __nv_bfloat16 term(float x) {
     return h;
 }
 
-struct TermArgs {
+struct TermMatrix {
     const void* src;
     int64_t stride, rows, cols;
     __nv_bfloat16* out;  // [planes][rows][ld]
     int64_t ld, plane_stride;
-    // rows without a gradient are taken as zeros (all three null: every row as it is)
+    bool masked;  // rows without a gradient are taken as zeros
+};
+
+struct TermArgs {
+    TermMatrix m[2];
+    int64_t first;  // threads of the first matrix (a multiple of a block's)
+    int64_t all;
     const int64_t* tokens;
     const float *g, *h;
 };
 
-// A matrix in one (bf16) or three (fp32) bf16 terms, eight columns per thread.
+// One or two matrices in one (bf16) or three (fp32) bf16 terms, eight columns per thread.
 template <typename T>
 __global__ void __launch_bounds__(kHeadThreads) terms_kernel(const TermArgs a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     constexpr int kTerms = sizeof(T) == 4 ? 3 : 1;
-    const int64_t across = a.ld / 8, all = across * a.rows;
-    const T* src = static_cast<const T*>(a.src);
-    const bool vec = reinterpret_cast<uintptr_t>(src) % 16 == 0 && a.stride * sizeof(T) % 16 == 0;
-    for (int64_t i = int64_t(blockIdx.x) * kHeadThreads + threadIdx.x; i < all;
-         i += int64_t(gridDim.x) * kHeadThreads) {
+    for (int64_t k = int64_t(blockIdx.x) * kHeadThreads + threadIdx.x; k < a.all;
+         k += int64_t(gridDim.x) * kHeadThreads) {
+        const bool second = k >= a.first;
+        const TermMatrix& m = a.m[second];
+        const int64_t i = second ? k - a.first : k, across = (m.cols + 7) / 8;
         const int64_t row = i / across, col = (i - row * across) * 8;
+        if (row >= m.rows) continue;
+        const T* src = static_cast<const T*>(m.src);
+        const bool vec = reinterpret_cast<uintptr_t>(src) % 16 == 0 && m.stride * sizeof(T) % 16 == 0;
         bool keep = true;
-        if (a.g || a.h)
+        if (m.masked)
             keep = (a.g && a.tokens[row] >= 0 && a.g[row] != 0.0f) || (a.h && a.h[row] != 0.0f);
         float v[8];
-        const T* at = src + row * a.stride + col;
-        if (keep && vec && col + 8 <= a.cols) {
+        const T* at = src + row * m.stride + col;
+        if (keep && vec && col + 8 <= m.cols) {
             if constexpr (sizeof(T) == 4) {
-                const float4 x = *reinterpret_cast<const float4*>(at);
+                const float4 x = reinterpret_cast<const float4*>(at)[0];
                 const float4 y = reinterpret_cast<const float4*>(at)[1];
                 v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
                 v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
@@ -83,27 +92,27 @@ __global__ void __launch_bounds__(kHeadThreads) terms_kernel(const TermArgs a) {
                 const uint4 x = *reinterpret_cast<const uint4*>(at);
                 const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    v[2 * k] = __uint_as_float(w[k] << 16);
-                    v[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+                for (int j = 0; j < 4; ++j) {
+                    v[2 * j] = __uint_as_float(w[j] << 16);
+                    v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
                 }
             }
         } else {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                v[k] = keep && col + k < a.cols ? static_cast<float>(at[k]) : 0.0f;
+            for (int j = 0; j < 8; ++j)
+                v[j] = keep && col + j < m.cols ? static_cast<float>(at[j]) : 0.0f;
         }
 #pragma unroll
         for (int t = 0; t < kTerms; ++t) {
             uint32_t w[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const __nv_bfloat16 lo = term(v[2 * k]), hi = term(v[2 * k + 1]);
-                w[k] = __bfloat16_as_ushort(lo) | (uint32_t(__bfloat16_as_ushort(hi)) << 16);
-                v[2 * k] -= __bfloat162float(lo);
-                v[2 * k + 1] -= __bfloat162float(hi);
+            for (int j = 0; j < 4; ++j) {
+                const __nv_bfloat16 lo = term(v[2 * j]), hi = term(v[2 * j + 1]);
+                w[j] = __bfloat16_as_ushort(lo) | (uint32_t(__bfloat16_as_ushort(hi)) << 16);
+                v[2 * j] -= __bfloat162float(lo);
+                v[2 * j + 1] -= __bfloat162float(hi);
             }
-            *reinterpret_cast<uint4*>(a.out + t * a.plane_stride + row * a.ld + col) =
+            *reinterpret_cast<uint4*>(m.out + t * m.plane_stride + row * m.ld + col) =
                 make_uint4(w[0], w[1], w[2], w[3]);
         }
     }
@@ -119,29 +128,12 @@ struct StatArgs {
     float *logp, *entropy, *lse, *lse_lo;
 };
 
-__device__ __forceinline__ void join(TileStat& s, const TileStat& o) {
-    if (o.a + o.c == 0.0f) return;  // (a thread without a part)
-    if (s.a + s.c == 0.0f) {
-        s = o;
-        return;
-    }
-    const bool mine = s.m >= o.m;
-    const TileStat hi = mine ? s : o, lo = mine ? o : s;
-    const float d = lo.m - hi.m;
-    if (d == 0.0f) {
-        s = TileStat{hi.m, hi.a + lo.a, hi.c + lo.c, hi.t + lo.t};
-    } else {
-        const float f = exp2f(d * 1.4426950408889634f), sum = lo.a + lo.c;
-        s = TileStat{hi.m, fmaf(f, sum, hi.a), hi.c, fmaf(f, fmaf(d, sum, lo.t), hi.t)};
-    }
-}
-
 __device__ __forceinline__ void join_lanes(TileStat& s, int by) {
     TileStat o;
     o.m = __shfl_xor_sync(0xFFFFFFFFu, s.m, by);
     o.a = __shfl_xor_sync(0xFFFFFFFFu, s.a, by);
-    o.c = __shfl_xor_sync(0xFFFFFFFFu, s.c, by);
     o.t = __shfl_xor_sync(0xFFFFFFFFu, s.t, by);
+    o.any = __shfl_xor_sync(0xFFFFFFFFu, s.any, by);
     join(s, o);
 }
 
@@ -186,9 +178,8 @@ __global__ void __launch_bounds__(kHeadThreads) stats_kernel(const StatArgs a) {
 #pragma unroll
     for (int by = ROWS; by < 32 && by < ROWS * kHeld; by *= 2) join_lanes(s, by);
     if (lane >= ROWS || row >= a.rows) return;
-    // log(a + c) from its small part where one token leads
-    const double sum = double(s.a) + double(s.c);
-    const double log_s = log1p(double(s.a) + (double(s.c) - 1.0));
+    const double sum = 1.0 + double(s.a);
+    const double log_s = log1p(double(s.a));
     const bool broken = isnan(s.t);
     const float nan = __int_as_float(0x7FC00000);
     const float top = static_cast<float>(double(s.m) + log_s);
@@ -328,7 +319,8 @@ int check_head(const char* fn, HeadCall& c) {
         }
     }
     c.terms = c.dtype == CAM_F32 ? 3 : 1;
-    c.ld = (c.width + 7) / 8 * 8;
+    // (rows of whole 128-byte lines: a box of 128 bytes of each row is then one line of it)
+    c.ld = (c.width + 63) / 64 * 64;
     // (the tensor maps want rows that start on 16 bytes)
     auto direct = [&](const Matrix& m) {
         return c.dtype == CAM_BF16 && reinterpret_cast<uintptr_t>(m.base) % 16 == 0 && m.stride % 8 == 0;
@@ -362,13 +354,23 @@ TileOperand operand(const HeadCall& c, const Matrix& m, int64_t rows, bool direc
     return o;
 }
 
-cudaError_t make_terms(const HeadCall& c, const Matrix& m, int64_t rows, void* out,
-                       const int64_t* tokens, const float* g, const float* h, int sms,
-                       cudaStream_t s) {
-    TermArgs a{m.base, m.stride, rows, c.width, static_cast<__nv_bfloat16*>(out), c.ld, rows * c.ld,
-               tokens, g, h};
-    const int64_t blocks = std::min<int64_t>((rows * (c.ld / 8) + kHeadThreads - 1) / kHeadThreads,
-                                             int64_t(sms) * 32);
+// Queues the terms of up to two matrices (rows 0: none).
+cudaError_t make_terms(const HeadCall& c, const Matrix& m0, int64_t rows0, void* out0, bool masked,
+                       const Matrix& m1, int64_t rows1, void* out1, const int64_t* tokens,
+                       const float* g, const float* h, int sms, cudaStream_t s) {
+    const int64_t across = (c.width + 7) / 8;
+    TermArgs a{};
+    a.m[0] = {m0.base, m0.stride, rows0, c.width, static_cast<__nv_bfloat16*>(out0), c.ld, rows0 * c.ld,
+              masked};
+    a.m[1] = {m1.base, m1.stride, rows1, c.width, static_cast<__nv_bfloat16*>(out1), c.ld, rows1 * c.ld,
+              false};
+    a.first = (rows0 * across + kHeadThreads - 1) / kHeadThreads * kHeadThreads;
+    a.all = a.first + rows1 * across;
+    a.tokens = tokens;
+    a.g = g;
+    a.h = h;
+    if (a.all == 0) return cudaSuccess;
+    const int64_t blocks = std::min<int64_t>((a.all + kHeadThreads - 1) / kHeadThreads, int64_t(sms) * 32);
     return c.dtype == CAM_F32 ? launch(terms_kernel<float>, blocks, a, s)
                               : launch(terms_kernel<__nv_bfloat16>, blocks, a, s);
 }
@@ -391,7 +393,9 @@ constexpr int64_t kForwardBudget = int64_t(1) << 29;   // a piece of the head in
 constexpr int64_t kBackwardBudget = int64_t(1) << 29;  // a piece of G, and of the head in terms
 
 // Parts of the vocabulary with statistics of their own.
-int64_t stat_parts(const HeadCall& c) { return c.few ? (c.vocab + 31) / 32 : (c.vocab + 127) / 128; }
+int64_t stat_parts(const HeadCall& c) {
+    return c.few ? (c.vocab + 31) / 32 : (c.vocab + kTileCols - 1) / kTileCols;
+}
 
 struct ForwardPlan {
     int64_t piece, x, w, stats, mine, bytes;  // offsets in the workspace
@@ -434,9 +438,10 @@ BackwardPlan backward_plan(const HeadCall& c, int sms, bool want_hidden, bool wa
     p.piece = piece_rows(c, per, kBackwardBudget);
     const int64_t piece = std::min(p.piece, c.vocab);
     const int64_t grid = c.pair ? sms / 2 : sms, tile = tile_rows(c.pair);
-    const int64_t across = (c.width + kTileCols - 1) / kTileCols;
+    const int64_t cols = c.width <= kTileNarrow ? kTileNarrow : kTileCols;
+    const int64_t across = (c.width + cols - 1) / cols;
     const int64_t pairs = c.terms == 3 ? 6 : c.grad_terms;
-    p.part_ld = c.ld;
+    p.part_ld = (c.width + 7) / 8 * 8;
     // both products share a launch: units of like length, the longer ones first, so that its
     // last round is nearly full
     const int64_t head_steps = (c.rows + 63) / 64 * pairs, hidden_steps = (piece + 63) / 64 * pairs;
@@ -464,9 +469,10 @@ BackwardPlan backward_plan(const HeadCall& c, int sms, bool want_hidden, bool wa
 
 cudaError_t join_parts(const HeadCall& c, const float* part, int64_t rows, int32_t splits, void* out,
                        int64_t stride, int sms, cudaStream_t s) {
-    JoinArgs a{part, rows, c.width, c.ld, splits, out, stride};
-    const bool runs = splits > 16 && rows * c.ld < (int64_t(1) << 20);
-    const int64_t tiles = (c.ld + 127) / 128 * (runs ? rows : (rows + 7) / 8);
+    const int64_t ld = (c.width + 7) / 8 * 8;
+    JoinArgs a{part, rows, c.width, ld, splits, out, stride};
+    const bool runs = splits > 16 && rows * ld < (int64_t(1) << 20);
+    const int64_t tiles = (ld + 127) / 128 * (runs ? rows : (rows + 7) / 8);
     const int64_t blocks = std::min<int64_t>(tiles, int64_t(sms) * 16);
     if (c.dtype == CAM_F32)
         return runs ? launch(join_kernel<float, 8>, blocks, a, s)
@@ -535,19 +541,18 @@ CAM_API int cam_head_logprobs(int64_t rows, int64_t vocab, int64_t width, const 
     TileStat* stats = reinterpret_cast<TileStat*>(ws + p.stats);
     float* mine = reinterpret_cast<float*>(ws + p.mine);
     cudaError_t ce = cudaSuccess;
-    if (!c.x_direct)
-        ce = make_terms(c, c.hidden, rows, ws + p.x, nullptr, nullptr, nullptr, sms, s);
     for (int64_t at = 0; at < vocab && ce == cudaSuccess; at += p.piece) {
         const int64_t n = std::min(p.piece, vocab - at);
         const Matrix piece = piece_of(c, at);
-        if (!c.w_direct) ce = make_terms(c, piece, n, ws + p.w, nullptr, nullptr, nullptr, sms, s);
+        ce = make_terms(c, c.hidden, c.x_direct || at > 0 ? 0 : rows, ws + p.x, false, piece,
+                        c.w_direct ? 0 : n, ws + p.w, nullptr, nullptr, nullptr, sms, s);
         if (ce != cudaSuccess) break;
         TileProduct t{};
         t.a = operand(c, c.hidden, rows, c.x_direct, ws + p.x, false);
         t.b = operand(c, piece, n, c.w_direct, ws + p.w, false);
         if (c.few) std::swap(t.a, t.b);
         t.splits = 1;
-        t.out.stats = stats + at / (c.few ? 32 : 128) * rows;
+        t.out.stats = stats + at / (c.few ? 32 : kTileCols) * rows;
         t.out.mine = mine;
         t.out.tokens = tokens;
         t.out.token0 = at;
@@ -627,14 +632,15 @@ CAM_API int cam_head_logprobs_backward(int64_t rows, int64_t vocab, int64_t widt
     const BackwardPlan p = backward_plan(c, sms, grad_hidden != nullptr, grad_head != nullptr);
     if (const int rc = check_workspace(fn, workspace, workspace_bytes, p.bytes)) return rc;
     char* ws = static_cast<char*>(workspace);
-    // hidden states in terms, rows without a gradient as zeros: what they hold, NaN say, then
-    // reaches nothing
-    cudaError_t ce = make_terms(c, c.hidden, rows, ws + p.x, tokens, grad_logp, grad_entropy, sms, s);
+    cudaError_t ce = cudaSuccess;
     const bool parts = p.hidden_splits > 1 || p.piece < vocab;
     for (int64_t at = 0; at < vocab && ce == cudaSuccess; at += p.piece) {
         const int64_t n = std::min(p.piece, vocab - at);
         const Matrix piece = piece_of(c, at);
-        if (!c.w_direct) ce = make_terms(c, piece, n, ws + p.w, nullptr, nullptr, nullptr, sms, s);
+        // hidden states in terms, rows without a gradient as zeros: what they hold, NaN say,
+        // then reaches nothing
+        ce = make_terms(c, c.hidden, at > 0 ? 0 : rows, ws + p.x, true, piece, c.w_direct ? 0 : n,
+                        ws + p.w, tokens, grad_logp, grad_entropy, sms, s);
         if (ce != cudaSuccess) break;
         TileProduct t{};
         t.a = operand(c, c.hidden, rows, false, ws + p.x, false);

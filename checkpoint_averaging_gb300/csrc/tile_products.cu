@@ -2,7 +2,7 @@
 //
 // A persistent grid, one block per SM or one pair of blocks (a cluster of two) per pair of
 // SMs; unit u of the launch (a tile of one product, or one K range of it) goes to block
-// (pair) u, u + grid, ... Ten warps with fixed roles:
+// (pair) u, u + grid, ... Warps with fixed roles:
 //
 //   warp 0 (one lane)  TMA producer: per K step of 128 bytes, this SM's 128 rows of A
 //                    and its share of B (the tile's columns, or half of them in a
@@ -11,9 +11,9 @@
 //                    of 32 bytes of K per stage into one of two TMEM accumulators;
 //                    e4m3 operands' scales go from the stage into TMEM first
 //                    (tcgen05.cp) and are applied by the tensor core;
-//   warps 2..9       epilogue: TMEM lanes 32 (warp % 4) .. + 31, warps 2..5 the left
-//                    half of the columns and 6..9 the right one. A thread holds its half
-//                    of one row of the tile in registers.
+//   warps 2..        epilogue, 16 or 8: TMEM lanes 32 (warp % 4) .. + 31, each four of
+//                    them a part of the columns. A thread holds its part of one row of the
+//                    tile in registers.
 //
 // A pair of SMs works on one 256-row tile (cta_group::2): each stages its own rows of A
 // and half of B's columns, so an SM fetches 32 KB per 128 x 256 x 64 products
@@ -50,17 +50,14 @@ namespace {
 __device__ int32_t g_operators_status;
 
 constexpr int kRows = 128;       // TMEM lanes: rows of an SM's tile
-constexpr int kThreads = 320;    // ten warps
-constexpr int kEpilogueWarps = 8;
 constexpr int kStepBytes = 128;  // bytes of K per stage
 constexpr int kMnBox = 64 * kStepBytes;  // MN-major box: 64 K rows of 64 elements
-constexpr int kRing = 192 * 1024;
+constexpr int kShared = 226 * 1024;  // for the ring and the epilogue's buffers
 // A warp's buffer for results: two boxes of 32 rows of 64 bytes, which TMA stores; or, where
 // rows do not start on 16 bytes, 32 rows of 16 words and one more between rows, so that a
 // column's words lie in as many banks.
 constexpr int kBox = 32 * 64;
 constexpr int kTurn = 17;
-constexpr int kOutBytes = kEpilogueWarps * 2 * kBox;
 static_assert(32 * kTurn * 4 <= 2 * kBox, "both forms share the buffer");
 
 struct alignas(128) Prob {
@@ -69,6 +66,7 @@ struct alignas(128) Prob {
     CUtensorMap ty;        // results: boxes of 64 bytes by 32 rows
     int32_t m_tiles, n_tiles, m_fast;
     int32_t steps;         // K steps of one pair of terms
+    int32_t tail;          // 32-byte pieces of the last of them
     int32_t all_steps, per_split;
     int32_t main0, run;    // from step main0 on, accumulated in runs of `run` steps
     int32_t a_mn, b_mn;
@@ -84,9 +82,21 @@ struct alignas(128) Args {
     int32_t n_prob, n_units;
 };
 
-template <bool E4M3, bool PAIR, bool FEW = false>
+template <bool E4M3, bool PAIR, int EPI, int COLS>
 struct Geo {
-    static constexpr int kCols = E4M3 ? kTileCols8 : FEW ? kTileFew : kTileCols;
+    static constexpr int kCols = COLS;
+    // Warps of the epilogue: 16 where each has 64 columns of a quarter of the rows then
+    // (two per scheduler do not cover their own latencies), 8 for narrower tiles.
+    static constexpr int kWarps = COLS == kTileCols ? 16 : 8;
+    static constexpr int kThreads = 64 + 32 * kWarps;
+    static constexpr int kParts = kWarps / 4;      // of a tile's columns
+    static constexpr int kPart = COLS / kParts;
+    // buffers: results, the parts' statistics of three tiles, few rows' data
+    static constexpr int kOutBytes = EPI == kTileStats   ? 3 * 32 * kWarps * 16
+                                     : EPI == kTileStatsFew ? 0
+                                     : EPI == kTileGradFew  ? 4096
+                                                            : kWarps * 2 * kBox;
+    static constexpr int kRing = kShared - kOutBytes - 1024;
     static constexpr int kBCols = PAIR ? kCols / 2 : kCols;  // B rows an SM stages
     static constexpr int kABytes = kRows * kStepBytes;
     static constexpr int kBBytes = kBCols * kStepBytes;
@@ -95,7 +105,7 @@ struct Geo {
     static constexpr int kTx = kABytes + kBBytes + kScaleA + kScaleB;
     static constexpr int kStage = (kTx + 1023) / 1024 * 1024;
     static constexpr int kStages = kRing / kStage < 8 ? kRing / kStage : 8;
-    static constexpr int kBars = 2 * kStages + 5;
+    static constexpr int kBars = 2 * kStages + 5 + 12;
     static constexpr int kOutAt = kStages * kStage;
     static constexpr int kBarsAt = kOutAt + kOutBytes;
     static constexpr int kSmem = kBarsAt + 8 * kBars + 16 + 1024;
@@ -165,9 +175,9 @@ __device__ __forceinline__ void commit(uint32_t bar) {
 // Instruction descriptors: fp32 accumulator; bf16 operands (formats 1, majorness in bits
 // 15 and 16), or e4m3 operands (formats 0) with one UE8M0 scale per 32 elements of K (bit
 // 23), scale bytes 0 of their words. N / 8 in bits 17-22, M / 16 in bits 24-28.
-template <bool E4M3, bool PAIR, bool FEW>
+template <bool E4M3, bool PAIR, int COLS>
 __device__ __forceinline__ uint32_t instruction(uint32_t a_mn, uint32_t b_mn) {
-    constexpr uint32_t n = Geo<E4M3, PAIR, FEW>::kCols >> 3, m = (PAIR ? 256 : 128) >> 4;
+    constexpr uint32_t n = COLS >> 3, m = (PAIR ? 256 : 128) >> 4;
     if constexpr (E4M3)
         return (n << 17) | (1u << 23) | (m << 24);
     else
@@ -435,35 +445,99 @@ __device__ __forceinline__ void put(float* v, int at, float x) {
     for (int i = 0; i < 32; ++i) v[i] = at == i ? x : v[i];
 }
 
+// Two fp32 values in one register pair: one instruction adds or multiplies both.
+__device__ __forceinline__ uint64_t two(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ void halves(uint64_t v, float& x, float& y) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t y) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+    return r;
+}
+
 // A row's statistics over a tile's columns, 32 at a time. The exponentials are relative to
-// the largest logit so far; those equal to it are counted, not summed, so that a row whose
-// leading token has nearly all the probability keeps the others' share to full precision.
+// the largest logit so far, whose own is left out of their sum: where it has nearly all of the
+// probability (less than 2^-8 of it elsewhere in its 32) the others are summed again without
+// it, so that their share keeps its precision; elsewhere it is subtracted.
 struct RowStat {
-    float m, a, c, t;
+    float m, a, t;
     __device__ __forceinline__ void add(const float* v, int n, bool first) {
         float top = v[0];
 #pragma unroll
         for (int i = 1; i < 32; ++i) top = i < n ? fmaxf(top, v[i]) : top;
-        if (first) {
-            m = top;
-            a = c = t = 0.0f;
-        } else if (top > m) {
-            const float d = m - top, f = exp2_fast(d * kLog2e), s = a + c;
-            t = f * fmaf(d, s, t);
-            a = s * f;
-            c = 0.0f;
-            m = top;
+        const bool leads = first || top > m;
+        float before = 0.0f, t_before = 0.0f;  // what there was, relative to the new largest
+        if (!first) {
+            before = a;
+            t_before = t;
+            if (leads) {
+                const float d = m - top, f = exp2_fast(d * kLog2e);
+                t_before = f * fmaf(d, 1.0f + a, t);
+                before = (1.0f + a) * f;
+            }
         }
+        if (leads) m = top;
+        float sum, ts;
+        if (n == 32) {
+            const uint64_t back = two(-m, -m), scale = two(kLog2e, kLog2e);
+            uint64_t s2[2] = {0, 0}, t2[2] = {0, 0};
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            if (i >= n) break;
-            const float d = v[i] - m;
-            const float e = exp2_fast(d * kLog2e);
-            // (NaN wherever a logit is NaN or infinite: through t)
-            t = fmaf(e, d, t);
-            if (d < 0.0f) a += e;
-            else c += 1.0f;
+            for (int i = 0; i < 32; i += 2) {
+                const uint64_t d = add2(two(v[i], v[i + 1]), back), p = mul2(d, scale);
+                float x, y;
+                halves(p, x, y);
+                const uint64_t e = two(exp2_fast(x), exp2_fast(y));
+                s2[i >> 1 & 1] = add2(s2[i >> 1 & 1], e);
+                // (NaN wherever a logit is NaN or infinite: through t)
+                t2[i >> 1 & 1] = fma2(e, d, t2[i >> 1 & 1]);
+            }
+            float x, y;
+            halves(add2(s2[0], s2[1]), x, y);
+            sum = x + y;
+            halves(add2(t2[0], t2[1]), x, y);
+            ts = x + y;
+        } else {
+            sum = ts = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                if (i >= n) break;
+                const float d = v[i] - m, e = exp2_fast(d * kLog2e);
+                sum += e;
+                ts = fmaf(e, d, ts);
+            }
         }
+        if (leads) {
+            sum -= 1.0f;
+            if (sum < 0x1p-8f) {
+                sum = 0.0f;
+                bool seen = false;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    if (i >= n) break;
+                    const float d = v[i] - m;
+                    const bool own = !seen && d == 0.0f;
+                    seen = seen || own;
+                    sum += own ? 0.0f : exp2_fast(d * kLog2e);
+                }
+            }
+        }
+        a = before + sum;
+        t = t_before + ts;
     }
 };
 
@@ -514,7 +588,7 @@ __device__ __forceinline__ void few_stats(const TileOut& o, const Prob& P, float
             const uint32_t equal = __ballot_sync(0xFFFFFFFFu, in && !below);
             if (lane == i) {
                 m = top;
-                c = static_cast<float>(__popc(equal));
+                c = static_cast<float>(__popc(equal)) - 1.0f;
             }
             t[i] = in ? e * d : 0.0f;
             v[i] = in && below ? e : 0.0f;
@@ -523,7 +597,7 @@ __device__ __forceinline__ void few_stats(const TileOut& o, const Prob& P, float
         }
     }
     const float a = sums_to_lanes(v, lane), s = sums_to_lanes(t, lane);
-    if (lane < n) o.stats[row0 / 32 * P.N + col0 + lane] = TileStat{m, a, c, s};
+    if (lane < n) o.stats[row0 / 32 * P.N + col0 + lane] = TileStat{m, a + c, s, 1.0f};
 }
 
 // The gradient of one token's logits in up to 32 rows.
@@ -567,10 +641,10 @@ __device__ __forceinline__ void few_grad(const TileOut& o, const Prob& P, const 
 
 // ---- the kernel ------------------------------------------------------------------------
 
-template <bool E4M3, bool PAIR, int EPI>
-__global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant__ Args a) {
-    constexpr bool kFew = EPI == kTileStatsFew || EPI == kTileGradFew;
-    using G = Geo<E4M3, PAIR, kFew>;
+template <bool E4M3, bool PAIR, int EPI, int COLS>
+__global__ void __launch_bounds__(Geo<E4M3, PAIR, EPI, COLS>::kThreads, 1)
+    tile_kernel(const __grid_constant__ Args a) {
+    using G = Geo<E4M3, PAIR, EPI, COLS>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -580,6 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     const uint32_t tfull0 = empty0 + 8 * G::kStages;
     const uint32_t tempty0 = tfull0 + 16;
     const uint32_t drain = tempty0 + 16;
+    const uint32_t parts0 = drain + 8;  // kTileStats: of each quarter of rows, of three tiles
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + G::kBars);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int32_t* status = &g_operators_status;
@@ -595,9 +670,10 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         }
         for (int i = 0; i < 2; ++i) {
             bar_init(tfull0 + 8 * i, 1);
-            bar_init(tempty0 + 8 * i, (PAIR ? 2 : 1) * kEpilogueWarps);
+            bar_init(tempty0 + 8 * i, (PAIR ? 2 : 1) * G::kWarps);
         }
         bar_init(drain, 1);
+        for (int i = 0; i < 12; ++i) bar_init(parts0 + 8 * i, G::kParts > 1 ? G::kParts - 1 : 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -704,12 +780,14 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         for (int u = worker; u < a.n_units && ok; u += workers) {
             const Unit t = unit_of(a, u);
             const Prob& P = a.prob[t.p];
-            const uint32_t idesc = instruction<E4M3, PAIR, kFew>(P.a_mn, P.b_mn);
+            const uint32_t idesc = instruction<E4M3, PAIR, COLS>(P.a_mn, P.b_mn);
             // 32 bytes further along a K-major row, or 16 rows further down an MN-major box
             const uint64_t step_a = P.a_mn ? 16 * kStepBytes / 16 : 2;
             const uint64_t step_b = P.b_mn ? 16 * kStepBytes / 16 : 2;
             const uint64_t desc_a = P.a_mn ? smem_desc_mn(ring, kMnBox) : smem_desc(ring);
             const uint64_t desc_b = P.b_mn ? smem_desc_mn(ring, kMnBox) : smem_desc(ring);
+            const int steps = P.steps, tail = P.tail;
+            int left = steps - t.s0 % steps;  // of this pair of terms
             for (int s = t.s0; s < t.s1 && ok;) {
                 const int end = run_end(P, s, t.s1);
                 if (!bar_wait(tempty0 + 8 * acc, acc_phase ^ 1, abort_flag, status)) {
@@ -741,8 +819,14 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                         tb += (t.nt & 1) ? 2 : 0;
                         scale_at ^= 16;
                     }
+                    int pieces = kStepBytes / 32;
+                    if (--left == 0) {
+                        left = steps;
+                        pieces = tail;
+                    }
 #pragma unroll
                     for (int k = 0; k < kStepBytes / 32; ++k) {
+                        if (k >= pieces) break;
                         multiply<E4M3, PAIR>(d, da + step_a * k, db + step_b * k,
                                              idesc, accumulate, ta, tb);
                         accumulate = 1;
@@ -769,12 +853,13 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         }
     } else if (warp >= 2) {
         // ---- epilogue ----
-        const int quarter = warp & 3, half = (warp - 2) >> 2;
+        const int quarter = warp & 3, part = (warp - 2) >> 2;
         uint8_t* out_at = smem + G::kOutAt + (warp - 2) * 2 * kBox;
         const uint32_t out_buf = su32(out_at);
         float* turn = reinterpret_cast<float*>(out_at);
-        int which = 0;
-        constexpr int kHalf = G::kCols / 2, kGroups = kHalf / 32;
+        int which = 0, turn_of = 0;
+        uint32_t turn_phase = 0;
+        constexpr int kPart = G::kPart, kGroups = kPart / 32;
         int acc = 0;
         uint32_t acc_phase = 0;
         bool ok = true;
@@ -791,7 +876,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
             const int64_t row0 =
                 int64_t(t.mt * (PAIR ? 2 : 1) + int(rank)) * kRows + quarter * 32;
             const int64_t row = row0 + lane;
-            const int64_t col0 = int64_t(t.nt) * G::kCols + half * kHalf;
+            const int64_t col0 = int64_t(t.nt) * G::kCols + part * kPart;
             const bool in = row < P.M;
             // what a row brings, asked for before its tile is done
             int64_t token = -1;  // its column in this product
@@ -804,7 +889,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
             }
             const bool work = row0 < P.M && col0 < P.N;  // (of the warp)
             // the thread's part of the row, summed over the runs of K
-            float sum[kHalf];
+            float sum[kPart];
             for (int s = t.s0; s < t.s1;) {
                 const bool first = s == t.s0;
                 s = run_end(P, s, t.s1);
@@ -814,13 +899,13 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                 tc_fence_after();
                 if (work) {
                     const uint32_t tbase = tmem + (uint32_t(quarter * 32) << 16) +
-                                           uint32_t(acc * G::kCols + half * kHalf);
+                                           uint32_t(acc * G::kCols + part * kPart);
                     if (first) {
 #pragma unroll
                         for (int c = 0; c < kGroups; ++c) tmem_ld32(tbase + uint32_t(c * 32), sum + 32 * c);
                     } else {
 #pragma unroll
-                        for (int c = 0; c < kHalf / 16; ++c) {
+                        for (int c = 0; c < kPart / 16; ++c) {
                             float v[16];
                             tmem_ld16(tbase + uint32_t(c * 16), v);
 #pragma unroll
@@ -841,6 +926,48 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                 }
             }
             if (!ok) break;
+            if constexpr (EPI == kTileStats) {
+                // Joined with the other parts' of these rows by the first. A part may be two
+                // tiles ahead of it (the accumulators are handed back before this), hence three
+                // buffers in turn with a barrier each.
+                if (row0 >= P.M) continue;
+                const uint32_t joined = parts0 + 8 * (3 * quarter + turn_of);
+                TileStat* parts = reinterpret_cast<TileStat*>(smem + G::kOutAt) +
+                                  turn_of * 32 * G::kWarps + quarter * 32 + lane;
+                RowStat stat;
+                stat.m = stat.a = stat.t = 0.0f;
+                if (work) {
+#pragma unroll
+                    for (int c = 0; c < kGroups; ++c) {
+                        const int64_t col = col0 + 32 * c;
+                        if (col >= P.N) break;
+                        const float* v = sum + 32 * c;
+                        const int n = P.N - col < 32 ? int(P.N - col) : 32;
+                        if (n == 32) stat.add(v, 32, c == 0);
+                        else stat.add(v, n, c == 0);
+                        const int64_t at = token - col;
+                        if (in && at >= 0 && at < n) o.mine[row] = pick(v, at);
+                    }
+                }
+                TileStat all{stat.m, stat.a, stat.t, work ? 1.0f : 0.0f};
+                if (part > 0) {
+                    parts[part * 128] = all;
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(joined);
+                } else {
+                    ok = bar_wait(joined, turn_phase, abort_flag, status);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+#pragma unroll
+                    for (int k = 1; k < G::kParts; ++k) join(all, parts[k * 128]);
+                    if (in) o.stats[int64_t(t.nt) * P.M + row] = all;
+                }
+                if (++turn_of == 3) {
+                    turn_of = 0;
+                    turn_phase ^= 1;
+                }
+                continue;
+            }
             if (!work) continue;
             if constexpr (EPI == kTileStatsFew) {
                 few_stats(o, P, sum, row0, col0, in, lane);
@@ -850,20 +977,14 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                 few_grad(o, P, few_rows + col0, sum, row, col0, in);
                 continue;
             }
-            RowStat stat;
-            stat.m = stat.a = stat.c = stat.t = 0.0f;
+            if constexpr (EPI == kTileOut || EPI == kTileGrad)
 #pragma unroll
             for (int c = 0; c < kGroups; ++c) {
                 const int64_t col = col0 + 32 * c;
                 if (col >= P.N) break;
                 float* v = sum + 32 * c;
                 const int n = P.N - col < 32 ? int(P.N - col) : 32;
-                if constexpr (EPI == kTileStats) {
-                    if (n == 32) stat.add(v, 32, c == 0);
-                    else stat.add(v, n, c == 0);
-                    const int64_t at = token - col;
-                    if (in && at >= 0 && at < n) o.mine[row] = pick(v, at);
-                } else if constexpr (EPI == kTileGrad) {
+                if constexpr (EPI == kTileGrad) {
                     int own = -1;  // the row's token, if it is among these
                     if (mine.token >= 0 && mine.token - int(col) >= 0 && mine.token - int(col) < 32) {
                         own = mine.token - int(col);
@@ -901,11 +1022,6 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                     else
                         store_turned(turn, static_cast<float*>(o.y) + at, o.ldy, v, rows, n, lane);
                 }
-            }
-            if constexpr (EPI == kTileStats) {
-                if (in)
-                    o.stats[(int64_t(t.nt) * 2 + half) * P.M + row] =
-                        TileStat{stat.m, stat.a, stat.c, stat.t};
             }
         }
         if (elect_one()) bulk_wait_all();  // stores done before the block (and its buffers) goes
@@ -961,11 +1077,11 @@ bool operand_map8(CUtensorMap* map, CUtensorMap* scales, const TileOperand& o, i
                   512 * row_blocks, 128, blocks, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
-template <bool E4M3, bool PAIR, int EPI>
+template <bool E4M3, bool PAIR, int EPI, int COLS>
 cudaError_t launch(const Args& a, int sms, cudaStream_t s) {
-    using G = Geo<E4M3, PAIR, EPI == kTileStatsFew || EPI == kTileGradFew>;
+    using G = Geo<E4M3, PAIR, EPI, COLS>;
     static std::atomic<uint64_t> allowed{0};
-    auto* kernel = tile_kernel<E4M3, PAIR, EPI>;
+    auto* kernel = tile_kernel<E4M3, PAIR, EPI, COLS>;
     int dev = 0;
     cudaError_t ce = cudaGetDevice(&dev);
     if (ce == cudaSuccess) ce = allow_shared(reinterpret_cast<const void*>(kernel), dev, allowed);
@@ -973,7 +1089,7 @@ cudaError_t launch(const Args& a, int sms, cudaStream_t s) {
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof cfg);
     cfg.gridDim = dim3(PAIR ? 2 * std::min(a.n_units, sms / 2) : std::min(a.n_units, sms));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(G::kThreads);
     cfg.dynamicSmemBytes = G::kSmem;
     cfg.stream = s;
     cudaLaunchAttribute at[2];
@@ -988,14 +1104,16 @@ cudaError_t launch(const Args& a, int sms, cudaStream_t s) {
 }
 
 template <bool PAIR>
-cudaError_t launch_any(const Args& a, bool e4m3, TileEpilogue epi, int sms, cudaStream_t s) {
-    if (e4m3) return epi == kTileOut ? launch<true, PAIR, kTileOut>(a, sms, s) : cudaErrorInvalidValue;
+cudaError_t launch_any(const Args& a, bool e4m3, TileEpilogue epi, int cols, int sms, cudaStream_t s) {
+    if (e4m3) return launch<true, PAIR, kTileOut, kTileCols8>(a, sms, s);
     switch (epi) {
-        case kTileOut: return launch<false, PAIR, kTileOut>(a, sms, s);
-        case kTileStats: return launch<false, PAIR, kTileStats>(a, sms, s);
-        case kTileGrad: return launch<false, PAIR, kTileGrad>(a, sms, s);
-        case kTileStatsFew: return launch<false, false, kTileStatsFew>(a, sms, s);
-        default: return launch<false, false, kTileGradFew>(a, sms, s);
+        case kTileOut:
+            return cols == kTileNarrow ? launch<false, PAIR, kTileOut, kTileNarrow>(a, sms, s)
+                                       : launch<false, PAIR, kTileOut, kTileCols>(a, sms, s);
+        case kTileStats: return launch<false, PAIR, kTileStats, kTileCols>(a, sms, s);
+        case kTileGrad: return launch<false, PAIR, kTileGrad, kTileCols>(a, sms, s);
+        case kTileStatsFew: return launch<false, false, kTileStatsFew, kTileFew>(a, sms, s);
+        default: return launch<false, false, kTileGradFew, kTileFew>(a, sms, s);
     }
 }
 
@@ -1009,7 +1127,11 @@ int tile_products(const char* fn, const TileProduct* ps, int n, bool e4m3, bool 
     std::memset(&a, 0, sizeof a);
     const bool few = epilogue == kTileStatsFew || epilogue == kTileGradFew;
     if (few) pair = false;
-    const int cols = e4m3 ? kTileCols8 : few ? kTileFew : kTileCols, rows = tile_rows(pair);
+    // (products of at most 128 columns: half of a wide tile would be of none)
+    bool narrow = epilogue == kTileOut && !e4m3;
+    for (int i = 0; i < n; ++i) narrow = narrow && ps[i].b.rows <= kTileNarrow;
+    const int cols = e4m3 ? kTileCols8 : few ? kTileFew : narrow ? kTileNarrow : kTileCols;
+    const int rows = tile_rows(pair);
     const int b_rows = pair ? cols / 2 : cols;
     int32_t units = 0;
     for (int i = 0; i < n; ++i) {
@@ -1038,6 +1160,7 @@ int tile_products(const char* fn, const TileProduct* ps, int n, bool e4m3, bool 
                 }
         const int step = e4m3 ? 128 : 64;
         P.steps = static_cast<int32_t>((p.a.k + step - 1) / step);
+        P.tail = static_cast<int32_t>((p.a.k - (P.steps - 1) * int64_t(step) + step / 4 - 1) / (step / 4));
         P.all_steps = P.steps * pairs;
         // Runs of the leading products: fp32 inputs' of 256 terms, logits of bf16 ones of 768
         // (of 512: 3 % slower), e4m3 ones' of 2,048 (their steps add twice as many terms); bf16
@@ -1068,8 +1191,8 @@ int tile_products(const char* fn, const TileProduct* ps, int n, bool e4m3, bool 
     }
     a.n_prob = n;
     a.n_units = units;
-    const cudaError_t ce = pair ? launch_any<true>(a, e4m3, epilogue, sms, stream)
-                                : launch_any<false>(a, e4m3, epilogue, sms, stream);
+    const cudaError_t ce = pair ? launch_any<true>(a, e4m3, epilogue, cols, sms, stream)
+                                : launch_any<false>(a, e4m3, epilogue, cols, sms, stream);
     if (ce != cudaSuccess)
         return record_error(CAM_E_CUDA, "%s: launch: %s", fn, cudaGetErrorString(ce));
     return CAM_OK;

@@ -35,12 +35,25 @@ enum TileEpilogue : int {
     kTileGradFew = 4,
 };
 
-// What kTileStats leaves of a row and half a tile of columns: the largest logit m,
-// the sum a of exp(x - m) over logits below it, the number c of logits equal to it, and
-// t = sum exp(x - m) (x - m).
+// What kTileStats leaves of a row and a tile of columns: the largest logit m,
+// the sum a of exp(x - m) over the others, and t = sum exp(x - m) (x - m). `any` is 1 (0: of no
+// logits at all).
 struct alignas(16) TileStat {
-    float m, a, c, t;
+    float m, a, t, any;
 };
+
+// The statistics of both's logits.
+__device__ __forceinline__ void join(TileStat& s, const TileStat& o) {
+    if (o.any == 0.0f) return;
+    if (s.any == 0.0f) {
+        s = o;
+        return;
+    }
+    const bool mine = s.m >= o.m;
+    const TileStat hi = mine ? s : o, lo = mine ? o : s;
+    const float d = lo.m - hi.m, f = exp2f(d * 1.4426950408889634f), sum = 1.0f + lo.a;
+    s = TileStat{hi.m, fmaf(f, sum, hi.a), fmaf(f, fmaf(d, sum, lo.t), hi.t), 1.0f};
+}
 
 struct TileOut {
     // kTileOut: y, or (part != null) fp32 partials, part[split][M][part_ld], written or,
@@ -51,7 +64,7 @@ struct TileOut {
     int32_t add;
     float* part;
     int64_t part_ld;
-    // kTileStats: stats[tile of columns * 2 + half][M]; `mine` [M] takes the logit of each
+    // kTileStats: stats[tile of columns][M]; `mine` [M] takes the logit of each
     // row's token. kTileGrad: G into `planes` terms of y (bf16, row stride ldy). Few rows:
     // stats[row of D / 32][N], and G^T (rows of a multiple of eight elements).
     TileStat* stats;
@@ -71,6 +84,7 @@ struct TileProduct {
 };
 
 constexpr int kTileCols = 256;   // columns of a bf16 tile
+constexpr int kTileNarrow = 128;  // of products with so few columns
 constexpr int kTileCols8 = 192;  // of an e4m3 tile
 constexpr int kTileFew = 64;     // rows of logits that take the forms for few rows
 
