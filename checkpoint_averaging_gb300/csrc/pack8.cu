@@ -35,6 +35,16 @@ __device__ __forceinline__ void load4(const T* p, int n, bool vec, float* v) {
             v[0] = __uint_as_float(x.x << 16), v[1] = __uint_as_float(x.x & 0xFFFF0000u);
             v[2] = __uint_as_float(x.y << 16), v[3] = __uint_as_float(x.y & 0xFFFF0000u);
         }
+    } else if (sizeof(T) == 2 && n >= 4) {
+        // rows of any alignment: the two or three aligned words that hold the four columns
+        // (31,661 x 1,510 bf16: 84 us column by column)
+        const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(at & ~uintptr_t(3));
+        const bool odd = at & 2;
+        const uint32_t a = w[0], b = w[1], c = odd ? w[2] : 0u;
+        const uint32_t x = odd ? __funnelshift_r(a, b, 16) : a, y = odd ? __funnelshift_r(b, c, 16) : b;
+        v[0] = __uint_as_float(x << 16), v[1] = __uint_as_float(x & 0xFFFF0000u);
+        v[2] = __uint_as_float(y << 16), v[3] = __uint_as_float(y & 0xFFFF0000u);
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = i < n ? static_cast<float>(p[i]) : 0.0f;
@@ -117,6 +127,11 @@ __device__ __forceinline__ void store4(T* p, int n, bool vec, const float* v) {
             *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
                                                       *reinterpret_cast<const uint32_t*>(&b));
         }
+    } else if (sizeof(T) == 2 && n >= 4 && reinterpret_cast<uintptr_t>(p) % 4 == 0) {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]);
+        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2], v[3]);
+        reinterpret_cast<uint32_t*>(p)[0] = *reinterpret_cast<const uint32_t*>(&a);
+        reinterpret_cast<uint32_t*>(p)[1] = *reinterpret_cast<const uint32_t*>(&b);
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)

@@ -1,5 +1,5 @@
-"""A merged global after its round: published in 4 bits, answered from for a
-few tokens, probed on given tokens, and trained on from there.
+"""A merged global after its round: published in 4 or 8 bits, answered from for
+a few tokens or whole contexts, probed on given tokens, and trained on from there.
 
 The DiffuRefill-1B run probed every published global on held-out tokens and
 chose between the global, its EMA and running averages by their losses
@@ -12,7 +12,8 @@ module runs the operators together as such a user would:
 merges a round of synthetic workers, publishes the tied embedding of the new
 global and of its EMA, computes the logits of a few positions from the 4-bit
 form, and reports each head's loss, entropy and alternatives, then takes one
-gradient step of the positions' hidden states.
+gradient step of the positions' hidden states; after that it does the same with
+whole contexts: the 8-bit form, and losses and gradients without the logits.
 """
 from __future__ import annotations
 
@@ -63,6 +64,48 @@ def differentiable_logprobs(logits, tokens):
     return _TokenLogprobs.apply(logits, tokens)
 
 
+class _HeadLogprobsGrad(torch.autograd.Function):
+    """The gradients, as a step of the graph under create_graph=True, so that a second
+    derivative is refused (see _TokenLogprobsGrad)."""
+
+    @staticmethod
+    def forward(ctx, hidden, head, tokens, lse, lse_lo, entropy, g, h, need_hidden, need_head):
+        return B.head_logprobs_backward(hidden, head, tokens, lse, entropy, g, h, lse_lo=lse_lo,
+                                        need_hidden=need_hidden, need_head=need_head)
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("token log probabilities have no second derivative")
+
+
+class _HeadLogprobs(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, hidden, head, tokens):
+        r = B.head_logprobs(hidden, head, tokens)
+        ctx.save_for_backward(hidden, head, tokens, r.lse, r.lse_lo, r.entropy)
+        ctx.set_materialize_grads(False)
+        return r.logp.clone(), r.entropy.clone()
+
+    @staticmethod
+    def backward(ctx, grad_logp, grad_entropy):
+        if grad_logp is None and grad_entropy is None:
+            return None, None, None
+        g = None if grad_logp is None else grad_logp.contiguous()
+        h = None if grad_entropy is None else grad_entropy.contiguous()
+        hidden, head, tokens, lse, lse_lo, entropy = ctx.saved_tensors
+        grads = _HeadLogprobsGrad.apply(hidden, head, tokens, lse, lse_lo, entropy, g, h,
+                                        *ctx.needs_input_grad[:2])
+        return *grads, None
+
+
+def differentiable_head_logprobs(hidden, head, tokens):
+    """(log probabilities of the tokens, entropies) of the logits hidden head^T, which are
+    not stored, for a loss: gradients reach hidden and head through
+    cam_head_logprobs_backward, the one that requires none is not computed. A second
+    derivative is refused."""
+    return _HeadLogprobs.apply(hidden, head, tokens)
+
+
 class Probe(NamedTuple):
     """What probe found of a head on given tokens."""
     loss: torch.Tensor        # mean of -log p over the rows with a token
@@ -74,10 +117,13 @@ class Probe(NamedTuple):
 
 def head_logits(hidden, head):
     """The logits of hidden states [rows, width]: `head` is a [vocab, width]
-    matrix, or its 4-bit form (Packed4) for the few rows of a decoding step,
-    through which no gradient flows (hidden states that require one are refused)."""
+    matrix, or its 4-bit form (Packed4) for the few rows of a decoding step, or its
+    8-bit form (Packed8) for whole contexts; no gradient flows through those
+    (hidden states that require one are refused)."""
     if isinstance(head, B.Packed4):
         return B.gemv4(hidden, head)
+    if isinstance(head, B.Packed8):
+        return B.matmul8(hidden, head)
     return hidden @ head.to(hidden.dtype).t()
 
 
@@ -87,6 +133,22 @@ def probe(hidden, head, tokens, top: int = 5) -> Probe:
     r = B.token_logprobs(head_logits(hidden, head), tokens, top=top)
     known = (tokens >= 0).sum().clamp(min=1)
     return Probe(-r.logp.sum() / known, r.entropy.mean(), r.logp, r.top_logp, r.top_ids)
+
+
+class ContextLoss(NamedTuple):
+    """What context_loss found of a head on given tokens."""
+    loss: torch.Tensor        # mean of -log p over the rows with a token
+    entropy: torch.Tensor     # mean over all rows
+    logp: torch.Tensor        # [rows]
+
+
+def context_loss(hidden, head, tokens) -> ContextLoss:
+    """probe's loss and entropy of whole contexts, for a [vocab, width] head of
+    hidden's dtype: the logits are neither stored nor rounded to it (and there are no
+    alternatives)."""
+    r = B.head_logprobs(hidden, head, tokens)
+    known = (tokens >= 0).sum().clamp(min=1)
+    return ContextLoss(-r.logp.sum() / known, r.entropy.mean(), r.logp)
 
 
 def main(vocab: int = 8192, width: int = 512, rows: int = 16, workers: int = 3, seed: int = 0):
@@ -133,9 +195,42 @@ def main(vocab: int = 8192, width: int = 512, rows: int = 16, workers: int = 3, 
     return found, losses
 
 
+def main_contexts(vocab: int = 8192, width: int = 512, rows: int = 1000, seed: int = 0):
+    """A head probed on a whole context and trained with it: the loss by the 8-bit
+    form's logits and without any, in bf16, and the losses before and after one gradient
+    step of the hidden states and the head in fp32."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+
+    def normal(*shape, scale):
+        return torch.empty(*shape, device="cuda").normal_(0.0, scale, generator=gen)
+
+    head = normal(vocab, width, scale=0.05)
+    tokens = torch.randint(0, vocab, (rows,), device="cuda", generator=gen)
+    hidden = head[tokens] * 3.0 + normal(rows, width, scale=0.3)
+    tokens[::10] = -1
+    short, short_head = hidden.bfloat16(), head.bfloat16()
+    eight = probe(short, B.pack8(head), tokens, top=1)
+    full = context_loss(short, short_head, tokens)
+
+    state, weight = hidden.clone().requires_grad_(True), head.clone().requires_grad_(True)
+    losses = []
+    for _ in range(2):
+        logp, entropy = differentiable_head_logprobs(state, weight, tokens)
+        loss = -logp.sum() / (tokens >= 0).sum() + 0.01 * entropy.mean()
+        losses.append(float(loss.detach()))
+        if len(losses) == 1:
+            loss.backward()
+            state = (state - 0.5 * state.grad).detach()
+            weight = (weight - 0.5 * weight.grad).detach()
+    return eight, full, losses
+
+
 if __name__ == "__main__":
     probes, steps = main()
     for name, p in probes.items():
         print(f"{name:15s} loss {float(p.loss):.4f}  entropy {float(p.entropy):.4f}  "
               f"first row's alternatives {p.top_ids[0].tolist()}")
     print(f"loss with entropy term: {steps[0]:.4f}, after one step {steps[1]:.4f}")
+    eight, full, steps = main_contexts()
+    print(f"a context: loss {float(full.loss):.4f} without logits, {float(eight.loss):.4f} in 8 bits; "
+          f"with entropy term {steps[0]:.4f}, after one step of hidden states and head {steps[1]:.4f}")
