@@ -24,31 +24,62 @@ namespace {
 constexpr int kThreads8 = 256;
 constexpr int kRowsAtOnce = 8;  // of a warp, in flight
 
+// Four columns of a row as they lie in memory: loaded first, widened when all of a warp's rows
+// are on their way (a load that is widened at once is waited for at once: 55,668 x 2,704 bf16
+// took 248 us that way).
+struct Four {
+    uint32_t w[4];
+};
+
+// From rows that start on four columns' bytes (`vec`), or of any alignment: fp32 one by one,
+// bf16 as the two or three aligned words that hold them. n: columns inside the matrix.
 template <typename T>
-__device__ __forceinline__ void load4(const T* p, int n, bool vec, float* v) {
-    if (vec && n >= 4) {
-        if constexpr (sizeof(T) == 4) {
-            const float4 x = *reinterpret_cast<const float4*>(p);
-            v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+__device__ __forceinline__ Four load4(const T* p, int n, bool vec) {
+    Four f{{0, 0, 0, 0}};
+    if (n < 4) {
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+            if (i < n) {
+                if constexpr (sizeof(T) == 4) f.w[i] = __float_as_uint(p[i]);
+                else f.w[i / 2] |= uint32_t(__bfloat16_as_ushort(p[i])) << (16 * (i & 1));
+            }
+    } else if constexpr (sizeof(T) == 4) {
+        if (vec) {
+            const uint4 x = *reinterpret_cast<const uint4*>(p);
+            f.w[0] = x.x, f.w[1] = x.y, f.w[2] = x.z, f.w[3] = x.w;
         } else {
-            const uint2 x = *reinterpret_cast<const uint2*>(p);
-            v[0] = __uint_as_float(x.x << 16), v[1] = __uint_as_float(x.x & 0xFFFF0000u);
-            v[2] = __uint_as_float(x.y << 16), v[3] = __uint_as_float(x.y & 0xFFFF0000u);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f.w[i] = __float_as_uint(p[i]);
         }
-    } else if (sizeof(T) == 2 && n >= 4) {
-        // rows of any alignment: the two or three aligned words that hold the four columns
-        // (31,661 x 1,510 bf16: 84 us column by column)
+    } else if (vec) {
+        const uint2 x = *reinterpret_cast<const uint2*>(p);
+        f.w[0] = x.x, f.w[1] = x.y;
+    } else {
         const uintptr_t at = reinterpret_cast<uintptr_t>(p);
         const uint32_t* w = reinterpret_cast<const uint32_t*>(at & ~uintptr_t(3));
-        const bool odd = at & 2;
-        const uint32_t a = w[0], b = w[1], c = odd ? w[2] : 0u;
-        const uint32_t x = odd ? __funnelshift_r(a, b, 16) : a, y = odd ? __funnelshift_r(b, c, 16) : b;
+        f.w[0] = w[0], f.w[1] = w[1];
+        if (at & 2) f.w[2] = w[2];
+    }
+    return f;
+}
+
+template <typename T>
+__device__ __forceinline__ void widen4(const Four& f, const T* p, int n, float* v) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(f.w[i]);
+    } else {
+        const bool odd = n >= 4 && (reinterpret_cast<uintptr_t>(p) & 2);
+        const uint32_t x = odd ? __funnelshift_r(f.w[0], f.w[1], 16) : f.w[0];
+        const uint32_t y = odd ? __funnelshift_r(f.w[1], f.w[2], 16) : f.w[1];
         v[0] = __uint_as_float(x << 16), v[1] = __uint_as_float(x & 0xFFFF0000u);
         v[2] = __uint_as_float(y << 16), v[3] = __uint_as_float(y & 0xFFFF0000u);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = i < n ? static_cast<float>(p[i]) : 0.0f;
     }
+}
+
+// u / d, in 32 bits where they suffice.
+__device__ __forceinline__ int64_t quotient(int64_t u, int32_t d) {
+    return u >> 32 ? u / d : static_cast<int64_t>(static_cast<uint32_t>(u) / static_cast<uint32_t>(d));
 }
 
 // q and scale of a block, of which this lane holds four columns.
@@ -94,20 +125,22 @@ __global__ void __launch_bounds__(kThreads8) pack8_kernel(int64_t rows, int64_t 
     const int64_t row_blocks = (rows + 127) / 128;
     for (int64_t u = (int64_t(blockIdx.x) * kThreads8 + threadIdx.x) >> 5; u < units;
          u += int64_t(gridDim.x) * (kThreads8 / 32)) {
-        const int64_t group = u / col_blocks;
+        const int64_t group = quotient(u, col_blocks);
         const int32_t kb = static_cast<int32_t>(u - group * col_blocks);
         const int64_t row0 = group * kRowsAtOnce;
         const int64_t col = int64_t(kb) * kP8Block + 4 * lane;
         const int n = static_cast<int>(min(int64_t(4), max(int64_t(0), cols - col)));
         uint32_t mine = 127;
-        float v[kRowsAtOnce][4];
+        Four f[kRowsAtOnce];
 #pragma unroll
         for (int r = 0; r < kRowsAtOnce; ++r)
-            load4(w + (row0 + r) * stride + col, row0 + r < rows ? n : 0, vec, v[r]);
+            f[r] = load4(w + (row0 + r) * stride + col, row0 + r < rows ? n : 0, vec);
 #pragma unroll
         for (int r = 0; r < kRowsAtOnce; ++r) {
+            float v[4];
+            widen4(f[r], w + (row0 + r) * stride + col, n, v);
             uint32_t scale;
-            const uint32_t four = quantise(v[r], &scale);
+            const uint32_t four = quantise(v, &scale);
             if (lane == r && row0 + r < rows) mine = scale;
             if (row0 + r < rows && col < ld)
                 *reinterpret_cast<uint32_t*>(q + (row0 + r) * ld + col) = four;
@@ -149,7 +182,7 @@ __global__ void __launch_bounds__(kThreads8) unpack8_kernel(int64_t rows, int64_
     const int64_t row_blocks = (rows + 127) / 128;
     for (int64_t u = (int64_t(blockIdx.x) * kThreads8 + threadIdx.x) >> 5; u < units;
          u += int64_t(gridDim.x) * (kThreads8 / 32)) {
-        const int64_t group = u / col_blocks;
+        const int64_t group = quotient(u, col_blocks);
         const int32_t kb = static_cast<int32_t>(u - group * col_blocks);
         const int64_t row0 = group * kRowsAtOnce;
         const int64_t col = int64_t(kb) * kP8Block + 4 * lane;
