@@ -28,6 +28,7 @@
 
 #include "cam_internal.h"
 #include "op_launch.h"
+#include "tile_device.cuh"
 #include "tile_products.h"
 
 #define CAM_API extern "C" __attribute__((visibility("default")))
@@ -35,16 +36,11 @@
 namespace cam {
 namespace {
 
+using tc::term;
+
 constexpr int kHeadThreads = 256;
 
 // ---- terms ------------------------------------------------------------------------------
-
-// The nearest bf16, but the largest one where that would be an infinity.
-__device__ __forceinline__ __nv_bfloat16 term(float x) {
-    __nv_bfloat16 h = __float2bfloat16_rn(x);
-    if ((__bfloat16_as_ushort(h) & 0x7FFFu) == 0x7F80u && isfinite(x)) h = __float2bfloat16_rz(x);
-    return h;
-}
 
 struct TermMatrix {
     const void* src;
@@ -264,6 +260,35 @@ __global__ void __launch_bounds__(kHeadThreads) join_kernel(const JoinArgs a) {
     }
 }
 
+// Partials part[range][column][row] of few rows' sums, joined in the order of their ranges and
+// turned: a block takes four columns of 32 rows, its warps the ranges in eight runs.
+__global__ void __launch_bounds__(kHeadThreads) join_turned(const JoinArgs a) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    __shared__ float runs[8][4][32];
+    const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+    const int64_t across = (a.cols + 3) / 4;
+    const int64_t row = blockIdx.x / across * 32 + x, col0 = blockIdx.x % across * 4;
+    const int32_t per = (a.splits + 7) / 8, s0 = y * per, s1 = min(a.splits, s0 + per);
+    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (row < a.rows) {
+#pragma unroll 4
+        for (int32_t s = s0; s < s1; ++s)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (col0 + k < a.cols) sum[k] += a.part[(s * a.cols + col0 + k) * a.ld + row];
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) runs[y][k][x] = sum[k];
+    __syncthreads();
+    if (y < 4 && row < a.rows && col0 + y < a.cols) {
+        float all = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) all += runs[k][y][x];
+        static_cast<float*>(a.out)[row * a.stride + col0 + y] = all;
+    }
+}
+
 // ---- host side --------------------------------------------------------------------------
 
 template <typename A>
@@ -295,6 +320,7 @@ struct HeadCall {
     bool x_direct, w_direct;  // read where they are
     bool pair;
     bool few;        // few rows of logits: as columns, the vocabulary along the tiles' rows
+    bool few32;      // and in fp32: the head's terms made on the way (f32_products.cu)
 };
 
 int64_t padded(int64_t bytes) { return (bytes + 511) / 512 * 512; }
@@ -334,7 +360,9 @@ int check_head(const char* fn, HeadCall& c) {
     // a pair of SMs takes 256 rows, one SM 128
     c.pair = c.rows > 128;
     // (16 rows of 73,760 logits: a tile of 128 rows of logits has work for one warp in eight)
-    c.few = c.rows <= kTileFew;
+    c.few32 = c.terms == 3 && c.rows <= kFew32;
+    c.few = c.rows <= kTileFew || c.few32;
+    if (c.few32) c.w_direct = true;
     return CAM_OK;
 }
 
@@ -373,6 +401,19 @@ cudaError_t make_terms(const HeadCall& c, const Matrix& m0, int64_t rows0, void*
     const int64_t blocks = std::min<int64_t>((a.all + kHeadThreads - 1) / kHeadThreads, int64_t(sms) * 32);
     return c.dtype == CAM_F32 ? launch(terms_kernel<float>, blocks, a, s)
                               : launch(terms_kernel<__nv_bfloat16>, blocks, a, s);
+}
+
+// The product of `t` (the few rows as t.b) with a piece of an fp32 head.
+Few32Product head32(const HeadCall& c, const Matrix& piece, int64_t n, const TileProduct& t) {
+    Few32Product q{};
+    q.w = static_cast<const float*>(piece.base);
+    q.w_rows = n;
+    q.width = c.width;
+    q.w_stride = piece.stride;
+    q.b = t.b;
+    q.splits = 1;
+    q.out = t.out;
+    return q;
 }
 
 Matrix piece_of(const HeadCall& c, int64_t at) {
@@ -420,6 +461,7 @@ ForwardPlan forward_plan(const HeadCall& c) {
 struct BackwardPlan {
     int64_t piece, x, w, grad, hidden, head, bytes;
     int32_t hidden_splits, head_splits;
+    int32_t hidden_ranges;  // few32: of the largest piece
     int64_t part_ld, grad_ld, grad_stride;
 };
 
@@ -448,6 +490,10 @@ BackwardPlan backward_plan(const HeadCall& c, int sms, bool want_hidden, bool wa
     p.head_splits = splits_for((piece + tile - 1) / tile * across, head_steps, grid, INT64_MAX);
     p.hidden_splits = splits_for((c.rows + tile - 1) / tile * across, hidden_steps, 2 * grid,
                                  std::max<int64_t>(64, 2 * head_steps));
+    if (c.few32) {  // head^T G^T: tiles of 128 columns of the head, steps of 32 of its rows
+        const int64_t steps = (piece + 31) / 32, tiles = (c.width + 127) / 128;
+        p.hidden_splits = p.hidden_ranges = splits_for(tiles, steps, 2 * sms, INT64_MAX);
+    }
     int64_t at = 0;
     p.x = at;
     at += term_bytes(c, c.rows);
@@ -459,7 +505,9 @@ BackwardPlan backward_plan(const HeadCall& c, int sms, bool want_hidden, bool wa
     p.grad_stride = p.grad_ld * (c.few ? p.piece : c.rows);
     at += padded(c.grad_terms * p.grad_stride * 2);
     p.hidden = at;
-    if (want_hidden && (p.hidden_splits > 1 || p.piece < c.vocab))
+    if (want_hidden && c.few32)
+        at += padded(p.hidden_splits * c.width * p.grad_ld * 4);
+    else if (want_hidden && (p.hidden_splits > 1 || p.piece < c.vocab))
         at += padded(p.hidden_splits * c.rows * p.part_ld * 4);
     p.head = at;
     if (want_head && p.head_splits > 1) at += padded(p.head_splits * piece * p.part_ld * 4);
@@ -549,7 +597,7 @@ CAM_API int cam_head_logprobs(int64_t rows, int64_t vocab, int64_t width, const 
         if (ce != cudaSuccess) break;
         TileProduct t{};
         t.a = operand(c, c.hidden, rows, c.x_direct, ws + p.x, false);
-        t.b = operand(c, piece, n, c.w_direct, ws + p.w, false);
+        if (!c.few32) t.b = operand(c, piece, n, c.w_direct, ws + p.w, false);
         if (c.few) std::swap(t.a, t.b);
         t.splits = 1;
         t.out.stats = stats + at / (c.few ? 32 : kTileCols) * rows;
@@ -557,8 +605,9 @@ CAM_API int cam_head_logprobs(int64_t rows, int64_t vocab, int64_t width, const 
         t.out.tokens = tokens;
         t.out.token0 = at;
         t.out.vocab = vocab;
-        if (const int rc = tile_products(fn, &t, 1, false, c.pair, c.few ? kTileStatsFew : kTileStats,
-                                         sms, s))
+        if (const int rc = c.few32 ? few32_product(fn, head32(c, piece, n, t), kTileStatsFew, sms, s)
+                                   : tile_products(fn, &t, 1, false, c.pair,
+                                                   c.few ? kTileStatsFew : kTileStats, sms, s))
             return rc;
     }
     if (ce == cudaSuccess) {
@@ -644,7 +693,7 @@ CAM_API int cam_head_logprobs_backward(int64_t rows, int64_t vocab, int64_t widt
         if (ce != cudaSuccess) break;
         TileProduct t{};
         t.a = operand(c, c.hidden, rows, false, ws + p.x, false);
-        t.b = operand(c, piece, n, c.w_direct, ws + p.w, false);
+        if (!c.few32) t.b = operand(c, piece, n, c.w_direct, ws + p.w, false);
         if (c.few) std::swap(t.a, t.b);
         t.splits = 1;
         t.out.y = ws + p.grad;
@@ -659,8 +708,9 @@ CAM_API int cam_head_logprobs_backward(int64_t rows, int64_t vocab, int64_t widt
         t.out.entropy = entropy;
         t.out.g = grad_logp;
         t.out.h = grad_entropy;
-        if (const int rc = tile_products(fn, &t, 1, false, c.pair, c.few ? kTileGradFew : kTileGrad, sms,
-                                         s))
+        if (const int rc = c.few32 ? few32_product(fn, head32(c, piece, n, t), kTileGradFew, sms, s)
+                                   : tile_products(fn, &t, 1, false, c.pair,
+                                                   c.few ? kTileGradFew : kTileGrad, sms, s))
             return rc;
 
         TileOperand grad{};
@@ -670,7 +720,23 @@ CAM_API int cam_head_logprobs_backward(int64_t rows, int64_t vocab, int64_t widt
         grad.plane_stride = p.grad_stride;
         TileProduct both[2] = {};
         int count = 0;
-        if (grad_hidden) {
+        if (grad_hidden && c.few32) {  // head^T G^T, turned by join_turned
+            Few32Product q{};
+            q.w = static_cast<const float*>(piece.base);
+            q.w_rows = n;
+            q.width = width;
+            q.w_stride = piece.stride;
+            q.turned = true;
+            q.b = grad;
+            q.b.rows = rows;
+            q.b.k = n;
+            q.b.mn_major = true;
+            q.splits = p.hidden_splits;
+            q.out.part = reinterpret_cast<float*>(ws + p.hidden);
+            q.out.part_ld = p.grad_ld;
+            q.out.add = at > 0;
+            if (const int rc = few32_product(fn, q, kTileOut, sms, s)) return rc;
+        } else if (grad_hidden) {
             TileProduct& q = both[count++];
             q.a = grad;
             q.a.rows = rows;
@@ -705,13 +771,18 @@ CAM_API int cam_head_logprobs_backward(int64_t rows, int64_t vocab, int64_t widt
                 q.out.y_bf16 = dtype == CAM_BF16;
             }
         }
-        if (const int rc = tile_products(fn, both, count, false, c.pair, kTileOut, sms, s)) return rc;
+        if (count > 0)
+            if (const int rc = tile_products(fn, both, count, false, c.pair, kTileOut, sms, s)) return rc;
         if (grad_head && p.head_splits > 1)
             ce = join_parts(c, reinterpret_cast<const float*>(ws + p.head), n, p.head_splits,
                             static_cast<char*>(grad_head) + at * grad_head_stride * size,
                             grad_head_stride, sms, s);
     }
-    if (ce == cudaSuccess && grad_hidden && parts)
+    if (ce == cudaSuccess && grad_hidden && c.few32) {
+        JoinArgs a{reinterpret_cast<const float*>(ws + p.hidden), rows, width, p.grad_ld,
+                   p.hidden_ranges, grad_hidden, grad_hidden_stride};
+        ce = launch(join_turned, (width + 3) / 4 * ((rows + 31) / 32), a, s);
+    } else if (ce == cudaSuccess && grad_hidden && parts)
         ce = join_parts(c, reinterpret_cast<const float*>(ws + p.hidden), rows, p.hidden_splits,
                         grad_hidden, grad_hidden_stride, sms, s);
     return ce == cudaSuccess ? CAM_OK : fail(fn, ce);

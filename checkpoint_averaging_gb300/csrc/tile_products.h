@@ -96,4 +96,26 @@ inline int tile_rows(bool pair) { return pair ? 256 : 128; }
 int tile_products(const char* fn, const TileProduct* p, int n, bool e4m3, bool pair,
                   TileEpilogue epilogue, int sms, cudaStream_t stream);
 
+// A product of an fp32 matrix w [w_rows][width] with few rows (at most kFew32) in three
+// bf16 terms, whose own terms the kernel makes as it reads it:
+//     turned = false:  D[v][r] = sum_k w[v][k] b[r][k]    (b.rows = r, b.k = width)
+//     turned = true:   D[d][r] = sum_v w[v][d] b[r][v]    (b MN-major, b.k = w_rows)
+// with kTileStatsFew or kTileGradFew of the first, kTileOut into partials of the second.
+struct Few32Product {
+    const float* w;
+    int64_t w_rows, width, w_stride;
+    bool turned;
+    TileOperand b;
+    int32_t splits;
+    TileOut out;
+};
+constexpr int kFew32 = 128;
+
+// Enqueues it (f32_products.cu). Errors: CAM_E_CUDA.
+int few32_product(const char* fn, const Few32Product& p, TileEpilogue epilogue, int sms,
+                  cudaStream_t stream);
+
+// The status word of these kernels on device `dev`, the current one.
+cudaError_t operators_status(int dev, int32_t** at);
+
 }  // namespace cam

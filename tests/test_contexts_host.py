@@ -130,10 +130,11 @@ def test_head_workspaces():
     more = head_workspace(ldw=65) - head_workspace()
     assert more == 300 * 64 * 2
     assert head_workspace(x=P + 2) - head_workspace() == 512
-    assert head_workspace(dt=B.F32) - head_workspace() == 3 * 300 * 64 * 2 + 3 * 4 * 64 * 2
+    assert head_workspace(200, dt=B.F32) - head_workspace(200) == 3 * (300 + 200) * 64 * 2
+    assert head_workspace(dt=B.F32) - head_workspace() == 3 * 4 * 64 * 2  # (few rows: the head as it is)
     # a piece of the head, not all of it
-    assert head_workspace(vocab=1 << 24, width=1024, ldx=1024, ldw=1024, dt=B.F32) < (1 << 29) + (1 << 27) \
-        + (1 << 24) // 128 * 4 * 16
+    assert head_workspace(200, vocab=1 << 22, width=1024, ldx=1024, ldw=1024, dt=B.F32) < (1 << 29) + (1 << 20) \
+        + (1 << 22) // 256 * 200 * 16
 
 
 def test_head_backward_refusals():
