@@ -14,7 +14,8 @@
 // A persistent grid of one block per SM, 18 warps:
 //   warp 0 (one lane)  TMA producer of the few rows' terms
 //   warp 1 (one lane)  MMA issuer: D[128 rows of the matrix][64 or 128 few rows]
-//   warps 2..9         16 rows of the matrix's tile each (or 4 rows of K): copied, split
+//   warps 2..9         in two groups that take the steps in turn, 32 rows of the matrix's
+//                      tile (or 8 rows of K) each: copied, split
 //   warps 10..17       epilogue: a lane is a row of the matrix, its registers the few rows
 //
 // Waits are bounded as in tile_products.cu.
@@ -37,7 +38,8 @@ constexpr int kStep = 32;          // elements of K
 constexpr int kStages32 = 3;
 constexpr int kTermBytes = kRows32 * kStep * 2;  // one term of the matrix's tile
 constexpr int kSplitWarps = 8;
-constexpr int kSlot = 2048;        // a warp's share of a step, fp32
+constexpr int kGroup = 4;          // of them work on one step (all eight on each: 30 % slower)
+constexpr int kSlot = 4096;        // a warp's share of a step, fp32
 constexpr int kRun32 = 8;          // steps of a run
 
 struct alignas(128) Args32 {
@@ -55,7 +57,7 @@ template <int COLS>
 struct Geo32 {
     static constexpr int kXBytes = 3 * COLS * kStep * 2;
     static constexpr int kStage = 3 * kTermBytes + kXBytes;
-    static constexpr int kDepth = COLS == 64 ? 5 : 4;  // steps copied ahead
+    static constexpr int kDepth = COLS == 64 ? 3 : 2;  // steps that a group copies ahead
     static constexpr int kRawAt = kStages32 * kStage;
     static constexpr int kRowsAt = kRawAt + kSplitWarps * kDepth * kSlot;
     static constexpr int kBarsAt = kRowsAt + kFew32 * 32;
@@ -152,7 +154,7 @@ __global__ void __launch_bounds__(kF32Threads, 1) f32_kernel(const __grid_consta
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages32; ++s) {
             bar_init(xfull0 + 8 * s, 1);
-            bar_init(ready0 + 8 * s, kSplitWarps);
+            bar_init(ready0 + 8 * s, kGroup);
             bar_init(empty0 + 8 * s, 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -275,61 +277,74 @@ __global__ void __launch_bounds__(kF32Threads, 1) f32_kernel(const __grid_consta
         }
     } else if (warp >= 2 && warp < 2 + kSplitWarps) {
         // ---- the matrix, copied ahead and split into terms ----
-        const int mine = warp - 2;
-        const uint32_t raw = ring + G::kRawAt + mine * G::kDepth * kSlot;
+        const int group = (warp - 2) / kGroup, mine = (warp - 2) % kGroup;
+        const uint32_t raw = ring + G::kRawAt + (warp - 2) * G::kDepth * kSlot;
         auto fetch = [&](const Cursor& f, uint32_t slot) {
             if (f.u < a.units) {
-                if constexpr (TURNED) {  // four rows of K, 128 columns
-                    const int64_t row0 = int64_t(f.s) * kStep + 4 * mine, col0 = int64_t(f.mt) * kRows32;
+                if constexpr (TURNED) {  // eight rows of K, 128 columns
+                    const int64_t row0 = int64_t(f.s) * kStep + 8 * mine, col0 = int64_t(f.mt) * kRows32;
+                    const int rows = a.w_rows - row0 < 8 ? int(a.w_rows - row0) : 8;
+                    const float* src = a.w + row0 * a.stride + col0;
+                    const int cols = a.width - col0 < 128 ? int(a.width - col0) : 128;
+                    if (a.vec) {
+                        const int left = (cols - 4 * lane) * 4, most = max(0, min(left, 16));
+                        src += 4 * lane;
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const bool in = row0 + r < a.w_rows;
-                        const float* row = a.w + (in ? row0 + r : 0) * a.stride;
-                        if (a.vec) {
-                            const int64_t left = (a.width - col0 - 4 * lane) * 4;
-                            const int bytes = in && left > 0 ? int(min(left, int64_t(16))) : 0;
-                            copy16(slot + r * 512 + lane * 16, bytes ? row + col0 + 4 * lane : a.w, bytes);
-                        } else {
+                        for (int r = 0; r < 8; ++r, src += a.stride) {
+                            const int bytes = r < rows ? most : 0;
+                            copy16(slot + r * 512 + lane * 16, bytes ? src : a.w, bytes);
+                        }
+                    } else {
+                        src += lane;
+#pragma unroll
+                        for (int r = 0; r < 8; ++r, src += a.stride)
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
-                                const int64_t col = col0 + 32 * k + lane;
-                                const bool ok = in && col < a.width;
-                                copy4(slot + r * 512 + (32 * k + lane) * 4, ok ? row + col : a.w, ok ? 4 : 0);
+                                const bool ok = r < rows && 32 * k + lane < cols;
+                                copy4(slot + r * 512 + (32 * k + lane) * 4, ok ? src + 32 * k : a.w,
+                                      ok ? 4 : 0);
                             }
-                        }
                     }
-                } else {  // 16 rows of 32 elements of K, 16-byte pieces c at c ^ (row % 8)
-                    const int64_t row0 = int64_t(f.mt) * kRows32 + 16 * mine, col0 = int64_t(f.s) * kStep;
+                } else {  // 32 rows of 32 elements of K, 16-byte pieces c at c ^ (row % 8)
+                    const int64_t row0 = int64_t(f.mt) * kRows32 + 32 * mine, col0 = int64_t(f.s) * kStep;
+                    const int64_t left_rows = a.w_rows - row0;
+                    const int rows = left_rows < 32 ? int(left_rows) : 32;  // (may be none)
+                    const float* src = a.w + row0 * a.stride + col0;
                     if (a.vec) {
                         const int piece = lane & 7;
                         const int64_t left = (a.width - col0 - 4 * piece) * 4;
                         const int most = left > 0 ? int(min(left, int64_t(16))) : 0;
+                        src += (lane >> 3) * a.stride + 4 * piece;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
+                        for (int k = 0; k < 8; ++k, src += 4 * a.stride) {
                             const int r = (lane >> 3) + 4 * k;
-                            const int bytes = row0 + r < a.w_rows ? most : 0;
-                            copy16(slot + r * 128 + ((piece ^ (r & 7)) * 16),
-                                   bytes ? a.w + (row0 + r) * a.stride + col0 + 4 * piece : a.w, bytes);
+                            const int bytes = r < rows ? most : 0;
+                            copy16(slot + r * 128 + ((piece ^ (r & 7)) * 16), bytes ? src : a.w, bytes);
                         }
                     } else {
-                        const bool in = col0 + lane < a.width;
+                        const int most = col0 + lane < a.width ? rows : 0;
+                        src += lane;
 #pragma unroll
-                        for (int r = 0; r < 16; ++r) {
-                            const bool ok = in && row0 + r < a.w_rows;
-                            copy4(slot + r * 128 + (((lane >> 2) ^ (r & 7)) * 16) + (lane & 3) * 4,
-                                  ok ? a.w + (row0 + r) * a.stride + col0 + lane : a.w, ok ? 4 : 0);
+                        for (int r = 0; r < 32; ++r, src += a.stride) {
+                            const bool ok = r < most;
+                            copy4(slot + r * 128 + ((lane * 4) ^ ((r & 7) << 4)), ok ? src : a.w, ok ? 4 : 0);
                         }
                     }
                 }
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
+        auto skip = [&](Cursor& f) {  // the other group's step
+            if (f.u < a.units) advance(a, f);
+        };
+        if (group == 1) skip(c);
         Cursor ahead = c;
         for (int k = 0; k < G::kDepth; ++k) {
             fetch(ahead, raw + k * kSlot);
-            if (ahead.u < a.units) advance(a, ahead);
+            skip(ahead);
+            skip(ahead);
         }
-        int stage = 0, slot = 0;
+        int stage = group, slot = 0;
         uint32_t phase = 0;
         while (c.u < a.units) {
             asm volatile("cp.async.wait_group %0;" ::"n"(G::kDepth - 1) : "memory");
@@ -338,31 +353,34 @@ __global__ void __launch_bounds__(kF32Threads, 1) f32_kernel(const __grid_consta
             if (!__all_sync(0xffffffffu, ok)) break;
             const uint32_t from = raw + slot * kSlot, to = ring + stage * G::kStage;
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
+            for (int k = 0; k < 4; ++k) {
                 float v[8];
                 if constexpr (TURNED) {
-                    const int r = (lane >> 4) + 2 * k, octet = lane & 15, kr = 4 * mine + r;
+                    const int r = (lane >> 4) + 2 * k, octet = lane & 15, kr = 8 * mine + r;
                     lds4(from + r * 512 + octet * 32, v);
                     lds4(from + r * 512 + octet * 32 + 16, v + 4);
                     split8(v, to + (octet >> 3) * 64 * kStep * 2 + kr * 128 + (((octet & 7) ^ (kr & 7)) * 16));
                 } else {
-                    const int r = lane & 15, octet = (lane >> 4) + 2 * k, R = 16 * mine + r;
-                    lds4(from + r * 128 + (((2 * octet) ^ (r & 7)) * 16), v);
-                    lds4(from + r * 128 + (((2 * octet + 1) ^ (r & 7)) * 16), v + 4);
-                    split8(v, to + R * 64 + ((octet ^ ((R >> 1) & 3)) * 16));
+                    const int R = 32 * mine + lane;
+                    lds4(from + lane * 128 + (((2 * k) ^ (lane & 7)) * 16), v);
+                    lds4(from + lane * 128 + (((2 * k + 1) ^ (lane & 7)) * 16), v + 4);
+                    split8(v, to + R * 64 + ((k ^ ((R >> 1) & 3)) * 16));
                 }
             }
             fence_async_smem();
             __syncwarp();  // (and the slot is read: it may be filled again)
             if (lane == 0) bar_arrive(ready0 + 8 * stage);
             fetch(ahead, from);
-            if (ahead.u < a.units) advance(a, ahead);
+            skip(ahead);
+            skip(ahead);
             if (++slot == G::kDepth) slot = 0;
-            if (++stage == kStages32) {
-                stage = 0;
+            stage += 2;
+            if (stage >= kStages32) {
+                stage -= kStages32;
                 phase ^= 1;
             }
-            advance(a, c);
+            skip(c);
+            skip(c);
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp >= 2 + kSplitWarps) {
