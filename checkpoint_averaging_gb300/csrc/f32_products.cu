@@ -35,7 +35,6 @@ namespace {
 constexpr int kF32Threads = 576;
 constexpr int kRows32 = 128;       // of the matrix's tile
 constexpr int kStep = 32;          // elements of K
-constexpr int kStages32 = 3;
 constexpr int kTermBytes = kRows32 * kStep * 2;  // one term of the matrix's tile
 constexpr int kSplitWarps = 8;
 constexpr int kGroup = 4;          // of them work on one step (all eight on each: 30 % slower)
@@ -53,15 +52,21 @@ struct alignas(128) Args32 {
     int32_t* status;
 };
 
+// Rings of their own for the matrix's terms, which are made at once when a stage is free, and
+// the few rows', whose copies take longer to come (one ring of three stages: 20 rows over
+// 152,602 x 824 200 us instead of 193).
 template <int COLS>
 struct Geo32 {
     static constexpr int kXBytes = 3 * COLS * kStep * 2;
-    static constexpr int kStage = 3 * kTermBytes + kXBytes;
-    static constexpr int kDepth = COLS == 64 ? 3 : 2;  // steps that a group copies ahead
-    static constexpr int kRawAt = kStages32 * kStage;
+    static constexpr int kWBytes = 3 * kTermBytes;
+    static constexpr int kWStages = 3;
+    static constexpr int kXStages = COLS == 64 ? 6 : 3;
+    static constexpr int kDepth = 2;  // steps that a group copies ahead
+    static constexpr int kXAt = kWStages * kWBytes;
+    static constexpr int kRawAt = kXAt + kXStages * kXBytes;
     static constexpr int kRowsAt = kRawAt + kSplitWarps * kDepth * kSlot;
     static constexpr int kBarsAt = kRowsAt + kFew32 * 32;
-    static constexpr int kBars = 3 * kStages32 + 5;
+    static constexpr int kBars = 2 * kWStages + 2 * kXStages + 5;
     static constexpr int kSmem = kBarsAt + 8 * kBars + 16 + 1024;
     static_assert(kSmem <= kMaxSharedBytes, "over the per-block shared memory limit");
 };
@@ -142,9 +147,10 @@ __global__ void __launch_bounds__(kF32Threads, 1) f32_kernel(const __grid_consta
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + G::kBarsAt);
     const uint32_t ring = su32(smem);
     const uint32_t xfull0 = su32(bars);
-    const uint32_t ready0 = xfull0 + 8 * kStages32;
-    const uint32_t empty0 = ready0 + 8 * kStages32;
-    const uint32_t tfull0 = empty0 + 8 * kStages32;
+    const uint32_t xempty0 = xfull0 + 8 * G::kXStages;
+    const uint32_t ready0 = xempty0 + 8 * G::kXStages;
+    const uint32_t empty0 = ready0 + 8 * G::kWStages;
+    const uint32_t tfull0 = empty0 + 8 * G::kWStages;
     const uint32_t tempty0 = tfull0 + 16;
     const uint32_t drain = tempty0 + 16;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + G::kBars);
@@ -152,8 +158,8 @@ __global__ void __launch_bounds__(kF32Threads, 1) f32_kernel(const __grid_consta
     const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages32; ++s) {
-            bar_init(xfull0 + 8 * s, 1);
+        for (int s = 0; s < 2 * G::kXStages; ++s) bar_init(xfull0 + 8 * s, 1);  // (and xempty)
+        for (int s = 0; s < G::kWStages; ++s) {
             bar_init(ready0 + 8 * s, kGroup);
             bar_init(empty0 + 8 * s, 1);
         }
@@ -185,8 +191,8 @@ __global__ void __launch_bounds__(kF32Threads, 1) f32_kernel(const __grid_consta
         int stage = 0;
         uint32_t phase = 0, issued = 0, filled_parity = 0;
         while (c.u < a.units) {
-            if (!bar_wait(empty0 + 8 * stage, phase ^ 1, abort_flag, a.status)) break;
-            const uint32_t sx = ring + stage * G::kStage + 3 * kTermBytes, fb = xfull0 + 8 * stage;
+            if (!bar_wait(xempty0 + 8 * stage, phase ^ 1, abort_flag, a.status)) break;
+            const uint32_t sx = ring + G::kXAt + stage * G::kXBytes, fb = xfull0 + 8 * stage;
             bar_expect(fb, G::kXBytes);
             if constexpr (TURNED) {
 #pragma unroll
@@ -197,14 +203,14 @@ __global__ void __launch_bounds__(kF32Threads, 1) f32_kernel(const __grid_consta
             }
             issued |= 1u << stage;
             filled_parity = (filled_parity & ~(1u << stage)) | (phase << stage);
-            if (++stage == kStages32) {
+            if (++stage == G::kXStages) {
                 stage = 0;
                 phase ^= 1;
             }
             advance(a, c);
         }
         if (*abort_flag) {  // let the copies in flight land
-            for (int s = 0; s < kStages32; ++s)
+            for (int s = 0; s < G::kXStages; ++s)
                 if ((issued >> s) & 1) {
                     const unsigned long long t0 = now_ns();
                     while (!bar_test(xfull0 + 8 * s, (filled_parity >> s) & 1))
@@ -221,22 +227,22 @@ __global__ void __launch_bounds__(kF32Threads, 1) f32_kernel(const __grid_consta
         constexpr uint64_t kAdvance = TURNED ? 16 * 128 / 16 : 2;
         constexpr int kXTerm = TURNED ? 64 * kStep * 2 : COLS * kStep * 2;
         const uint64_t wdesc = TURNED ? smem_desc_mn(ring, 64 * kStep * 2) : smem_desc64(ring);
-        const uint64_t xdesc = TURNED ? smem_desc_mn(ring + 3 * kTermBytes, 3 * 64 * kStep * 2)
-                                      : smem_desc64(ring + 3 * kTermBytes);
-        int stage = 0, acc = 0, in_run = 0;
-        uint32_t phase = 0, acc_phase = 0;
+        const uint64_t xdesc = TURNED ? smem_desc_mn(ring + G::kXAt, 3 * 64 * kStep * 2)
+                                      : smem_desc64(ring + G::kXAt);
+        int stage = 0, xstage = 0, acc = 0, in_run = 0;
+        uint32_t phase = 0, xphase = 0, acc_phase = 0;
         while (c.u < a.units) {
             if (in_run == 0) {
                 if (!bar_wait(tempty0 + 8 * acc, acc_phase ^ 1, abort_flag, a.status)) break;
                 tc_fence_after();
             }
-            if (!bar_wait(xfull0 + 8 * stage, phase, abort_flag, a.status) ||
+            if (!bar_wait(xfull0 + 8 * xstage, xphase, abort_flag, a.status) ||
                 !bar_wait(ready0 + 8 * stage, phase, abort_flag, a.status))
                 break;
             tc_fence_after();
             const uint32_t d = tmem + uint32_t(acc * 2 * COLS);
-            const uint64_t w0 = wdesc + uint32_t(stage * G::kStage / 16);
-            const uint64_t x0 = xdesc + uint32_t(stage * G::kStage / 16);
+            const uint64_t w0 = wdesc + uint32_t(stage * G::kWBytes / 16);
+            const uint64_t x0 = xdesc + uint32_t(xstage * G::kXBytes / 16);
             const int pieces = c.s + 1 == a.steps ? a.tail : 2;
 #pragma unroll
             for (int i = 0; i < 3; ++i)
@@ -254,9 +260,14 @@ __global__ void __launch_bounds__(kF32Threads, 1) f32_kernel(const __grid_consta
                                   fresh ? 0u : 1u);
                     }
             mma_commit(empty0 + 8 * stage);
-            if (++stage == kStages32) {
+            mma_commit(xempty0 + 8 * xstage);
+            if (++stage == G::kWStages) {
                 stage = 0;
                 phase ^= 1;
+            }
+            if (++xstage == G::kXStages) {
+                xstage = 0;
+                xphase ^= 1;
             }
             const bool last = c.s + 1 == c.s1;
             if (++in_run == kRun32 || last) {
@@ -351,7 +362,7 @@ __global__ void __launch_bounds__(kF32Threads, 1) f32_kernel(const __grid_consta
             __syncwarp();
             const bool ok = bar_wait(empty0 + 8 * stage, phase ^ 1, abort_flag, a.status);
             if (!__all_sync(0xffffffffu, ok)) break;
-            const uint32_t from = raw + slot * kSlot, to = ring + stage * G::kStage;
+            const uint32_t from = raw + slot * kSlot, to = ring + stage * G::kWBytes;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 float v[8];
@@ -375,8 +386,8 @@ __global__ void __launch_bounds__(kF32Threads, 1) f32_kernel(const __grid_consta
             skip(ahead);
             if (++slot == G::kDepth) slot = 0;
             stage += 2;
-            if (stage >= kStages32) {
-                stage -= kStages32;
+            if (stage >= G::kWStages) {
+                stage -= G::kWStages;
                 phase ^= 1;
             }
             skip(c);

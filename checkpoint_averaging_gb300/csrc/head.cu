@@ -332,6 +332,9 @@ int check_head(const char* fn, HeadCall& c) {
         return record_error(CAM_E_ARG, "%s: vocab out of range", fn);
     if (c.width < 1 || c.width > CAM_HEAD_MAX_WIDTH)
         return record_error(CAM_E_ARG, "%s: width out of range", fn);
+    // (tiles are counted in 32 bits)
+    if ((c.rows + 127) / 128 * ((c.vocab + kTileCols - 1) / kTileCols) > (int64_t(1) << 30))
+        return record_error(CAM_E_ARG, "%s: rows and vocab out of range", fn);
     if (c.dtype != CAM_F32 && c.dtype != CAM_BF16)
         return record_error(CAM_E_ARG, "%s: unknown dtype %d", fn, static_cast<int>(c.dtype));
     const int64_t size = c.dtype == CAM_F32 ? 4 : 2;

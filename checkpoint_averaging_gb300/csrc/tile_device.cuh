@@ -202,7 +202,9 @@ __device__ __forceinline__ float own_grad(float x, const GradRow& r) {
 }
 
 // That of another's. FINE: for fp32 results, with all that matters there of d's rounding.
-// Otherwise p is off by 2^-24 of lse log2(e), a hundredth of what rounding G to bf16 costs.
+// Otherwise p is off by 2^-24 of lse log2(e), a hundredth of what rounding G to bf16 costs
+// as long as |lse| is below kQuick.
+constexpr float kQuick = 256.0f;
 template <bool FINE>
 __device__ __forceinline__ float other_grad(float x, const GradRow& r) {
     if constexpr (FINE) {
@@ -396,13 +398,14 @@ __device__ __forceinline__ void few_grad(const TileOut& o, int64_t N, const Grad
         const int i = __ffs(left) - 1;
         put(v, i, own_grad(pick(v, i), rows[i]));
     }
-    const bool fine = o.planes == 3;
+    const bool three = o.planes == 3;
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
         if (i >= n) {
             v[i] = 0.0f;
         } else {
             const GradRow r = rows[i];
+            const bool fine = three || fabsf(r.lse) > kQuick;  // (one row for every lane)
             const float w = fine ? other_grad<true>(v[i], r) : other_grad<false>(v[i], r);
             v[i] = own >> i & 1 ? v[i] : w;
         }

@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(Geo<E4M3, PAIR, EPI, COLS>::kThreads, 1)
             const bool in = row < P.M;
             // what a row brings, asked for before its tile is done
             int64_t token = -1;  // its column in this product
-            GradRow mine;
+            GradRow mine{};
             if constexpr (EPI == kTileStats) {
                 if (in && o.tokens) token = o.tokens[row] - o.token0;
             }
@@ -593,7 +593,7 @@ __global__ void __launch_bounds__(Geo<E4M3, PAIR, EPI, COLS>::kThreads, 1)
                         own = mine.token - int(col);
                         put(v, own, own_grad(pick(v, own), mine));
                     }
-                    if (o.planes == 3) {
+                    if (o.planes == 3 || __any_sync(0xffffffffu, fabsf(mine.lse) > kQuick)) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             v[i] = own == i ? v[i] : other_grad<true>(v[i], mine);

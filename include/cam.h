@@ -860,8 +860,9 @@ int cam_matmul8(int64_t tokens, int64_t rows, int64_t cols, const void* x, int64
  * throughout. A negative token id is no token (logp 0); one of `vocab` or more
  * gives a logp of NaN. vocab in [1, CAM_LOGPROBS_MAX_VOCAB], width in
  * [1, CAM_HEAD_MAX_WIDTH]; strides count elements between the starts of rows.
- * Matrices whose rows start on 16 bytes (bf16) are read where they are, others
- * and fp32 ones through the workspace, in pieces of the vocabulary. workspace:
+ * bf16 matrices whose rows start on 16 bytes are read where they are, and so is
+ * an fp32 head for at most 128 rows; others go through the workspace in bf16
+ * terms, in pieces of the vocabulary. workspace:
  * cam_head_logprobs_workspace bytes (for the same arguments) of device memory,
  * 256-byte aligned, the call's own until it has run.
  * Errors: CAM_E_ARG, CAM_E_CUDA.

@@ -107,6 +107,7 @@ def test_head_refusals():
     refused(f(rows=(1 << 24) + 1), "rows")
     refused(f(vocab=0), "vocab")
     refused(f(vocab=(1 << 24) + 1), "vocab")
+    refused(f(rows=1 << 24, vocab=1 << 24), "rows and vocab")
     refused(f(width=0), "width")
     refused(f(width=(1 << 17) + 1, ldx=1 << 18, ldw=1 << 18), "width")
     refused(f(dt=5), "dtype")

@@ -366,3 +366,31 @@ def test_other_streams_and_graphs(dtype):
     for got, ref in zip(outs, (want, want2)):
         for u, v in zip(got, ref):
             assert torch.equal(u, v)
+
+
+@pytest.mark.parametrize("rows", [9, 150])
+def test_logits_far_from_zero(rows):
+    """bf16 logits of 1e5 and more, all of a row near its largest: p keeps what the logits say."""
+    gen = torch.Generator().manual_seed(rows)
+    hidden = torch.zeros(rows, 64)
+    hidden[:, 0] = 2.0 ** 17
+    hidden[:, 1:4] = torch.randn(rows, 3, generator=gen)
+    head = torch.zeros(300, 64)
+    head[:, 0] = 1.0
+    head[:, 1:4] = torch.randn(300, 3, generator=gen)
+    tokens = torch.randint(0, 300, (rows,), generator=gen).to(DEV)
+    hidden, head = hidden.to(BF16).to(DEV), head.to(BF16).to(DEV)
+    x = hidden.double() @ head.double().t()
+    lse = torch.logsumexp(x, 1)
+    p = (x - lse[:, None]).exp()
+    top = lse.float()
+    g = torch.full((rows,), -1.0, device=DEV)
+    _, gw = B.head_logprobs_backward(hidden, head, tokens, top, torch.zeros_like(top), g,
+                                     lse_lo=(lse - top.double()).float())
+    # logits are sums rounded at 2^17: 64 / 16 steps and a sum of fp32 lose 2 * 2^-6 each at most
+    off = 10 * 2.0 ** -6
+    G = p.clone()
+    G.scatter_add_(1, tokens[:, None], torch.full((rows, 1), -1.0, device=DEV).double())
+    dG = p * (math.exp(off) - 1) + 2.0 ** -8 * G.abs()
+    assert ((gw.double() - G.t() @ hidden.double()).abs()
+            <= dG.t() @ hidden.double().abs() * 1.01 + 2.0 ** -8 * (G.t() @ hidden.double()).abs() + 1e-6).all()
