@@ -69,7 +69,10 @@ __global__ void __launch_bounds__(kHeadThreads) terms_kernel(const TermArgs a) {
         const bool second = k >= a.first;
         const TermMatrix& m = a.m[second];
         const int64_t i = second ? k - a.first : k, across = (m.cols + 7) / 8;
-        const int64_t row = i / across, col = (i - row * across) * 8;
+        const int64_t row = a.all >> 31 ? i / across
+                                        : static_cast<int64_t>(static_cast<uint32_t>(i) /
+                                                               static_cast<uint32_t>(across));
+        const int64_t col = (i - row * across) * 8;
         if (row >= m.rows) continue;
         const T* src = static_cast<const T*>(m.src);
         const bool vec = reinterpret_cast<uintptr_t>(src) % 16 == 0 && m.stride * sizeof(T) % 16 == 0;
@@ -468,11 +471,12 @@ struct BackwardPlan {
     int64_t part_ld, grad_ld, grad_stride;
 };
 
-// Ranges of K for a product of `tiles` tiles of `steps` steps: enough units for `want`, and
-// none longer than `most` steps, but none shorter than eight.
-int32_t splits_for(int64_t tiles, int64_t steps, int64_t want, int64_t most) {
-    const int64_t n = std::min(std::max((want + tiles - 1) / tiles, (steps + most - 1) / most),
-                               std::max<int64_t>(1, steps / 8));
+// Ranges of K for a product of `tiles` tiles of `steps` steps of K, `pairs` products of terms
+// each: enough units for `want`, and none longer than `most` products, but none shorter than
+// eight.
+int32_t splits_for(int64_t tiles, int64_t steps, int64_t pairs, int64_t want, int64_t most) {
+    const int64_t n = std::min(std::max((want + tiles - 1) / tiles, (steps * pairs + most - 1) / most),
+                               std::max<int64_t>(1, std::min(steps, steps * pairs / 8)));
     const int64_t per = (steps + n - 1) / n;
     return static_cast<int32_t>((steps + per - 1) / per);
 }
@@ -489,13 +493,13 @@ BackwardPlan backward_plan(const HeadCall& c, int sms, bool want_hidden, bool wa
     p.part_ld = (c.width + 7) / 8 * 8;
     // both products share a launch: units of like length, the longer ones first, so that its
     // last round is nearly full
-    const int64_t head_steps = (c.rows + 63) / 64 * pairs, hidden_steps = (piece + 63) / 64 * pairs;
-    p.head_splits = splits_for((piece + tile - 1) / tile * across, head_steps, grid, INT64_MAX);
-    p.hidden_splits = splits_for((c.rows + tile - 1) / tile * across, hidden_steps, 2 * grid,
-                                 std::max<int64_t>(64, 2 * head_steps));
+    const int64_t head_steps = (c.rows + 63) / 64, hidden_steps = (piece + 63) / 64;
+    p.head_splits = splits_for((piece + tile - 1) / tile * across, head_steps, pairs, grid, INT64_MAX / 2);
+    p.hidden_splits = splits_for((c.rows + tile - 1) / tile * across, hidden_steps, pairs, 2 * grid,
+                                 std::max<int64_t>(64, 2 * head_steps * pairs));
     if (c.few32) {  // head^T G^T: tiles of 128 columns of the head, steps of 32 of its rows
         const int64_t steps = (piece + 31) / 32, tiles = (c.width + 127) / 128;
-        p.hidden_splits = p.hidden_ranges = splits_for(tiles, steps, 2 * sms, INT64_MAX);
+        p.hidden_splits = p.hidden_ranges = splits_for(tiles, steps, 6, 2 * sms, INT64_MAX / 2);
     }
     int64_t at = 0;
     p.x = at;

@@ -61,8 +61,9 @@ struct alignas(128) Prob {
     int32_t m_tiles, n_tiles, m_fast;
     int32_t steps;         // K steps of one pair of terms
     int32_t tail;          // 32-byte pieces of the last of them
-    int32_t all_steps, per_split;
-    int32_t main0, run;    // from step main0 on, accumulated in runs of `run` steps
+    int32_t pairs;         // of terms
+    int32_t per_split;     // K steps of a unit's range
+    int32_t run;           // K steps that are accumulated in TMEM, every pair's
     int32_t a_mn, b_mn;
     int32_t unit0;
     int32_t boxes;         // results go through ty
@@ -213,7 +214,8 @@ __device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t smem) {
 // ---- units -----------------------------------------------------------------------------
 
 struct Unit {
-    int p, mt, nt, split, s0, s1;
+    int p, mt, nt, split;
+    int k0, k1;  // K steps
 };
 
 __device__ __forceinline__ Unit unit_of(const Args& a, int u) {
@@ -231,15 +233,9 @@ __device__ __forceinline__ Unit unit_of(const Args& a, int u) {
         t.mt = u / P.n_tiles;
         t.nt = u - t.mt * P.n_tiles;
     }
-    t.s0 = t.split * P.per_split;
-    t.s1 = min(P.all_steps, t.s0 + P.per_split);
+    t.k0 = t.split * P.per_split;
+    t.k1 = min(P.steps, t.k0 + P.per_split);
     return t;
-}
-
-// The end of the run of K steps that starts with s.
-__device__ __forceinline__ int run_end(const Prob& P, int s, int s1) {
-    if (s < P.main0) return min(s1, P.main0);
-    return min(int64_t(s1), int64_t(s) + P.run - (s - P.main0) % P.run);
 }
 
 // ---- the kernel ------------------------------------------------------------------------
@@ -314,12 +310,12 @@ __global__ void __launch_bounds__(Geo<E4M3, PAIR, EPI, COLS>::kThreads, 1)
             const Prob& P = a.prob[t.p];
             const int arow = (t.mt * (PAIR ? 2 : 1) + int(rank)) * kRows;
             const int bcol = t.nt * G::kCols, brow = bcol + int(rank) * G::kBCols;
-            const int steps = P.steps, s1 = t.s1;
+            const int k1 = t.k1, run = P.run, pairs = P.pairs;
             const bool a_mn = P.a_mn, b_mn = P.b_mn;
             const CUtensorMap *ta = &P.ta, *tb = &P.tb;
-            int pair = t.s0 / steps, ks = t.s0 - pair * steps;
-            int za = P.terms_a >> (4 * pair) & 15, zb = P.terms_b >> (4 * pair) & 15;
-            for (int s = t.s0; s < s1; ++s) {
+            int pair = 0, ks = t.k0, za = P.terms_a & 15, zb = P.terms_b & 15;
+            int from = ks, to = min(k1 - from, run) + from;  // the run
+            while (from < k1) {
                 if (!bar_wait(empty0 + 8 * stage, phase ^ 1, abort_flag, status)) {
                     ok = false;
                     break;
@@ -357,9 +353,13 @@ __global__ void __launch_bounds__(Geo<E4M3, PAIR, EPI, COLS>::kThreads, 1)
                     stage = 0;
                     phase ^= 1;
                 }
-                if (++ks == steps) {
-                    ks = 0;
-                    ++pair;
+                if (++ks == to) {
+                    if (++pair == pairs) {
+                        pair = 0;
+                        from = to;
+                        to = min(k1 - from, run) + from;
+                    }
+                    ks = from;
                     za = P.terms_a >> (4 * pair) & 15;
                     zb = P.terms_b >> (4 * pair) & 15;
                 }
@@ -389,10 +389,9 @@ __global__ void __launch_bounds__(Geo<E4M3, PAIR, EPI, COLS>::kThreads, 1)
             const uint64_t step_b = P.b_mn ? 16 * kStepBytes / 16 : 2;
             const uint64_t desc_a = P.a_mn ? smem_desc_mn(ring, kMnBox) : smem_desc(ring);
             const uint64_t desc_b = P.b_mn ? smem_desc_mn(ring, kMnBox) : smem_desc(ring);
-            const int steps = P.steps, tail = P.tail;
-            int left = steps - t.s0 % steps;  // of this pair of terms
-            for (int s = t.s0; s < t.s1 && ok;) {
-                const int end = run_end(P, s, t.s1);
+            const int last = P.steps - 1, tail = P.tail, k1 = t.k1, run = P.run, pairs = P.pairs;
+            for (int from = t.k0; from < k1 && ok;) {
+                const int to = min(k1 - from, run) + from;
                 if (!bar_wait(tempty0 + 8 * acc, acc_phase ^ 1, abort_flag, status)) {
                     ok = false;
                     break;
@@ -400,7 +399,8 @@ __global__ void __launch_bounds__(Geo<E4M3, PAIR, EPI, COLS>::kThreads, 1)
                 tc_fence_after();
                 const uint32_t d = tmem + uint32_t(acc * G::kCols);
                 uint32_t accumulate = 0;
-                for (; s < end; ++s) {
+                int ks = from;
+                for (int left = (to - from) * pairs; left > 0; --left) {
                     if (!bar_wait(full0 + 8 * stage, phase, abort_flag, status)) {
                         ok = false;
                         break;
@@ -422,11 +422,8 @@ __global__ void __launch_bounds__(Geo<E4M3, PAIR, EPI, COLS>::kThreads, 1)
                         tb += (t.nt & 1) ? 2 : 0;
                         scale_at ^= 16;
                     }
-                    int pieces = kStepBytes / 32;
-                    if (--left == 0) {
-                        left = steps;
-                        pieces = tail;
-                    }
+                    const int pieces = ks == last ? tail : kStepBytes / 32;
+                    if (++ks == to) ks = from;
 #pragma unroll
                     for (int k = 0; k < kStepBytes / 32; ++k) {
                         if (k >= pieces) break;
@@ -441,6 +438,7 @@ __global__ void __launch_bounds__(Geo<E4M3, PAIR, EPI, COLS>::kThreads, 1)
                     }
                 }
                 if (!ok) break;
+                from = to;
                 commit<PAIR>(tfull0 + 8 * acc);
                 if (++acc == 2) {
                     acc = 0;
@@ -493,9 +491,10 @@ __global__ void __launch_bounds__(Geo<E4M3, PAIR, EPI, COLS>::kThreads, 1)
             const bool work = row0 < P.M && col0 < P.N;  // (of the warp)
             // the thread's part of the row, summed over the runs of K
             float sum[kPart];
-            for (int s = t.s0; s < t.s1;) {
-                const bool first = s == t.s0;
-                s = run_end(P, s, t.s1);
+            const int k1 = t.k1, run = P.run;
+            for (int from = t.k0; from < k1;) {
+                const bool first = from == t.k0;
+                from += min(k1 - from, run);
                 ok = bar_wait(tfull0 + 8 * acc, acc_phase, abort_flag, status);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
@@ -749,21 +748,22 @@ int tile_products(const char* fn, const TileProduct* ps, int n, bool e4m3, bool 
         const int step = e4m3 ? 128 : 64;
         P.steps = static_cast<int32_t>((p.a.k + step - 1) / step);
         P.tail = static_cast<int32_t>((p.a.k - (P.steps - 1) * int64_t(step) + step / 4 - 1) / (step / 4));
-        P.all_steps = P.steps * pairs;
-        // Runs of the leading products: fp32 inputs' of 256 terms, logits of bf16 ones of 768
-        // (of 512: 3 % slower), e4m3 ones' of 2,048 (their steps add twice as many terms); bf16
+        P.pairs = pairs;
+        // Runs: of fp32 inputs 256 terms of each pair (all pairs of a run are close in time, so
+        // that the terms' second and third reads come from L2), of two-term G 512, of bf16 logits
+        // 768 (of 512: 3 % slower), of e4m3 2,048 (whose steps add twice as many terms); bf16
         // results of bf16 inputs hide what a long run loses.
-        P.main0 = P.steps * (pairs - 1);
-        P.run = pairs > 1 ? 4 : e4m3 ? 16 : epilogue == kTileStats || epilogue == kTileStatsFew ? 12
-                                                                                   : INT_MAX;
-        const int splits = std::max(1, std::min(p.splits, P.all_steps));
-        P.per_split = (P.all_steps + splits - 1) / splits;
+        const bool logits = epilogue == kTileStats || epilogue == kTileStatsFew;
+        P.run = pairs > 2 ? 4 : pairs == 2 ? 8 : e4m3 ? 16 : logits ? 12 : INT_MAX;
+        const int splits = std::max(1, std::min(p.splits, P.steps));
+        P.per_split = (P.steps + splits - 1) / splits;
+        const int ranges = (P.steps + P.per_split - 1) / P.per_split;
         P.unit0 = units;
         if (epilogue == kTileOut || epilogue == kTileGrad) {
             const bool part = p.out.part != nullptr, bf16 = epilogue == kTileGrad || p.out.y_bf16;
             const int64_t size = bf16 ? 2 : 4, ld = part ? p.out.part_ld : p.out.ldy;
             const void* y = part ? p.out.part : p.out.y;
-            const int64_t planes = part ? (P.all_steps + P.per_split - 1) / P.per_split
+            const int64_t planes = part ? ranges
                                         : epilogue == kTileGrad ? p.out.planes : 1;
             const int64_t plane = epilogue == kTileGrad ? p.out.plane_stride : P.M * ld;
             // (the tensor maps want rows that start on 16 bytes)
@@ -775,7 +775,7 @@ int tile_products(const char* fn, const TileProduct* ps, int n, bool e4m3, bool 
                 return record_error(CAM_E_CUDA, "%s: cuTensorMapEncodeTiled failed", fn);
         }
         P.o = p.out;
-        units += P.m_tiles * P.n_tiles * ((P.all_steps + P.per_split - 1) / P.per_split);
+        units += P.m_tiles * P.n_tiles * ranges;
     }
     a.n_prob = n;
     a.n_units = units;
