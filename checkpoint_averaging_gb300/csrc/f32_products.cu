@@ -65,7 +65,7 @@ struct Geo32 {
     static constexpr int kXAt = kWStages * kWBytes;
     static constexpr int kRawAt = kXAt + kXStages * kXBytes;
     static constexpr int kRowsAt = kRawAt + kSplitWarps * kDepth * kSlot;
-    static constexpr int kBarsAt = kRowsAt + kFew32 * 32;
+    static constexpr int kBarsAt = (kRowsAt + kFew32 * int(sizeof(GradRow)) + 15) / 16 * 16;
     static constexpr int kBars = 2 * kWStages + 2 * kXStages + 5;
     static constexpr int kSmem = kBarsAt + 8 * kBars + 16 + 1024;
     static_assert(kSmem <= kMaxSharedBytes, "over the per-block shared memory limit");
