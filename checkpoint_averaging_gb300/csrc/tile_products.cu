@@ -767,8 +767,12 @@ int tile_products(const char* fn, const TileProduct* ps, int n, bool e4m3, bool 
             const int64_t planes = part ? ranges
                                         : epilogue == kTileGrad ? p.out.planes : 1;
             const int64_t plane = epilogue == kTileGrad ? p.out.plane_stride : P.M * ld;
-            // (the tensor maps want rows that start on 16 bytes)
-            P.boxes = reinterpret_cast<uintptr_t>(y) % 16 == 0 && ld * size % 16 == 0;
+            // The tensor maps want rows that start on 16 bytes, and a box that a row ends in may
+            // be written past the row's end (a bf16 row of 223 columns: the 224th, too): into a
+            // workspace's padding, not into what a caller has beside the result.
+            const bool own = part || epilogue == kTileGrad;
+            P.boxes = reinterpret_cast<uintptr_t>(y) % 16 == 0 && ld * size % 16 == 0 &&
+                      (own || P.N * size % 16 == 0);
             if (P.boxes &&
                 !encode(&P.ty, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
                         y, P.N, P.M, planes, ld * size, plane * size, static_cast<int>(64 / size), 32,

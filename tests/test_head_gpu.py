@@ -18,6 +18,7 @@ The products with the head and with hidden pass that on, |dG| |head| and |dG|^T 
 and add (12 K / 16 + 64) 2^-23 of |G| |head| (K = vocab) and |G|^T |hidden| (K = rows);
 a bf16 result rounds by 2^-8 of itself.
 """
+import ctypes
 import math
 
 import pytest
@@ -394,3 +395,62 @@ def test_logits_far_from_zero(rows):
     dG = p * (math.exp(off) - 1) + 2.0 ** -8 * G.abs()
     assert ((gw.double() - G.t() @ hidden.double()).abs()
             <= dG.t() @ hidden.double().abs() * 1.01 + 2.0 ** -8 * (G.t() @ hidden.double()).abs() + 1e-6).all()
+
+
+def poison(size=1 << 27):
+    """Leaves NaN in the allocator's free memory, where workspaces come from."""
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    blocks = [torch.full((n // 4,), math.nan, device=DEV) for n in (size, 1 << 20, 1 << 16, 4096)]
+    torch.cuda.synchronize()
+    del blocks
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("rows", [7, 120, 200, 300])
+@pytest.mark.parametrize("more", range(1, 8))
+def test_what_lies_beside_the_rows_is_not_read(rows, more, dtype):
+    # rows that start on 16 bytes and end anywhere, NaN behind them and in the workspaces
+    width, vocab = 128 + more, 600 + more
+    hidden, head, tokens = inputs(rows, vocab, width, dtype)
+    want, grads = check(hidden, head, tokens), check_grad(hidden, head, tokens)
+    a = torch.full((rows + 1, 144), math.nan, dtype=dtype, device=DEV)
+    w = torch.full((vocab + 1, 144), math.nan, dtype=dtype, device=DEV)
+    a[:rows, :width], w[:vocab, :width] = hidden, head
+    a, w = a[:rows, :width], w[:vocab, :width]
+    poison()
+    for u, v in zip(want, B.head_logprobs(a, w, tokens)):
+        assert u is None or torch.equal(u, v)
+    poison()
+    got = check_grad(a, w, tokens)
+    assert torch.equal(got[0], grads[0]) and torch.equal(got[1], grads[1])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("rows", [7, 120, 200, 300])
+@pytest.mark.parametrize("width", range(129, 137))
+def test_what_lies_beside_the_gradients_stays(rows, width, dtype):
+    hidden, head, tokens = inputs(rows, 601, width, dtype)
+    e = Exact(hidden, head, tokens)
+    want = check_grad(hidden, head, tokens, with_h=False, e=e)
+    gen = torch.Generator().manual_seed(rows)
+    g = -(torch.rand(rows, generator=gen) + 0.5).to(DEV) / rows
+    L, code = B.lib(), B.F32 if dtype is F32 else B.BF16
+    lse, H = e.lse.float(), e.H.float()
+    lo = (e.lse - lse.double()).float()
+    size = ctypes.c_int64()
+    args = (rows, 601, width)
+    assert L.cam_head_logprobs_backward_workspace(*args, head.data_ptr(), width, code,
+                                                  ctypes.byref(size)) == 0
+    space = torch.empty(size.value, dtype=torch.uint8, device=DEV)
+    dx = torch.full((rows + 1, 144), 9.0, dtype=dtype, device=DEV)
+    dw = torch.full((602, 144), 9.0, dtype=dtype, device=DEV)
+    stream = torch.cuda.current_stream().cuda_stream
+    assert L.cam_head_logprobs_backward(
+        *args, hidden.data_ptr(), width, head.data_ptr(), width, code, tokens.data_ptr(),
+        lse.data_ptr(), lo.data_ptr(), H.data_ptr(), g.data_ptr(), None, dx.data_ptr(), 144,
+        dw.data_ptr(), 144, space.data_ptr(), size.value, stream) == 0
+    torch.cuda.synchronize()
+    for got, room, n in ((want[0], dx, rows), (want[1], dw, 601)):
+        assert torch.equal(room[:n, :width], got)
+        assert (room[:n, width:] == 9).all() and (room[n] == 9).all()

@@ -176,6 +176,30 @@ def test_strides_of_products(tokens, out):
     assert (y[tokens:] == 9).all()
 
 
+@pytest.mark.parametrize("tokens", [5, 200])
+@pytest.mark.parametrize("rows", [193, 222, 223, 224])
+@pytest.mark.parametrize("pad, offset", [(0, 0), (0, 1), (1, 0), (1, 1), (2, 2)])
+def test_results_that_start_between_words(tokens, rows, pad, offset):
+    # bf16 rows on even and odd elements, whose last part has 1, 30, 31 or 32 columns
+    x, w = rand(tokens, 300, 6), rand(rows, 300, 7)
+    ld = rows + pad + (rows & 1) + offset
+    room = torch.full((tokens + 1, ld), 9.0, dtype=BF16, device=DEV)
+    check(x, w, y=room[:tokens, offset:offset + rows])
+    assert (room[:tokens, :offset] == 9).all() and (room[:tokens, offset + rows:] == 9).all()
+    assert (room[tokens] == 9).all()
+
+
+@pytest.mark.parametrize("tokens", [5, 200])
+@pytest.mark.parametrize("out", [F32, BF16])
+@pytest.mark.parametrize("rows", range(217, 225))
+def test_columns_beside_a_result_stay(tokens, out, rows):
+    # rows that start on 16 bytes and end anywhere
+    x, w = rand(tokens, 300, 6), rand(rows, 300, 7)
+    room = torch.full((tokens + 1, 240), 9.0, dtype=out, device=DEV)
+    check(x, w, y=room[:tokens, :rows])
+    assert (room[:tokens, rows:] == 9).all() and (room[tokens] == 9).all()
+
+
 def test_broken_blocks_stay_visible():
     x, w = rand(200, 300, 8), rand(400, 300, 9)
     x[7, 290], x[150, 0] = math.nan, math.inf
