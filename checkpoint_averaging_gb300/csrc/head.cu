@@ -395,7 +395,13 @@ int check_head(const char* fn, HeadCall& c) {
     // a pair of SMs takes 256 rows, one SM 128
     c.pair = c.rows > 128;
     // (16 rows of 73,760 logits: a tile of 128 rows of logits has work for one warp in eight)
-    c.few32 = c.terms == 3 && c.rows <= kFew32;
+    // Terms on the way save writing the head's and reading them back, but a block takes 128 rows of
+    // the head, whose copies it waits for: where the head is small, or narrow for so many rows,
+    // its terms are written out. (Log probabilities and gradients, on the way / written out:
+    // 100 rows over 4,000 x 200 33 / 33 and 52 / 38 us, over 12,000 x 1,500 63 / 92 and 160 / 178,
+    // over 150,000 x 72 142 / 74 and 270 / 189; 30 over 150,000 x 72 65 / 89 and 155 / 180.)
+    c.few32 = c.terms == 3 && c.rows <= kFew32 && c.vocab * c.width >= (int64_t(1) << 23) &&
+              (c.rows <= kTileFew || c.width > 512);
     c.few = c.rows <= kTileFew || c.few32;
     if (c.few32) c.w_direct = true;
     return CAM_OK;
