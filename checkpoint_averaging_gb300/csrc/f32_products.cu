@@ -39,7 +39,7 @@ constexpr int kTermBytes = kRows32 * kStep * 2;  // one term of the matrix's til
 constexpr int kSplitWarps = 8;
 constexpr int kGroup = 4;          // of them work on one step (all eight on each: 30 % slower)
 constexpr int kSlot = 4096;        // a warp's share of a step, fp32
-// Steps of a run: 126 rows over 152,602 x 824 take 297 us, with eight 270; the entropy of one row
+// Steps of a run: 126 rows over 152,602 x 824 take 279 us, with eight 246; the entropy of one row
 // over 11,241 x 1,469 is off by 9.9e-7 of itself, with eight 1.8e-6.
 constexpr int kRun32 = 4;
 
@@ -56,13 +56,17 @@ struct alignas(128) Args32 {
 
 // Rings of their own for the matrix's terms, which are made at once when a stage is free, and
 // the few rows', whose copies take longer to come (one ring of three stages: 20 rows over
-// 152,602 x 824 200 us instead of 193).
+// 152,602 x 824 200 us instead of 193). No more of either than is needed: copies of 4 bytes hold
+// lines of L1 while they are under way, and L1 is what shared memory leaves. With six and three
+// stages of the few rows' terms for 64 and 128 columns, and with these four and two: 2 rows over
+// 18,495 x 3,934 174 and 142 us, 126 over 152,602 x 822 370 and 314; with rows that start on
+// 16 bytes (copied past L1) 2 over 18,495 x 3,932 108 and 113, 126 over 152,602 x 824 298 and 280.
 template <int COLS>
 struct Geo32 {
     static constexpr int kXBytes = 3 * COLS * kStep * 2;
     static constexpr int kWBytes = 3 * kTermBytes;
     static constexpr int kWStages = 3;
-    static constexpr int kXStages = COLS == 64 ? 6 : 3;
+    static constexpr int kXStages = COLS == 64 ? 4 : 2;
     static constexpr int kDepth = 2;  // steps that a group copies ahead
     static constexpr int kXAt = kWStages * kWBytes;
     static constexpr int kRawAt = kXAt + kXStages * kXBytes;

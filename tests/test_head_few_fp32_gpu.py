@@ -45,8 +45,8 @@ def test_sizes(rows, vocab, width):
 
 
 @pytest.mark.parametrize("rows", [7, 100])
-@pytest.mark.parametrize("width", [516, 519])
-@pytest.mark.parametrize("pad, offset", [(0, 1), (1, 0), (4, 0), (8, 4), (3, 2)])
+@pytest.mark.parametrize("width", [516, 518, 519])
+@pytest.mark.parametrize("pad, offset", [(0, 0), (0, 1), (1, 0), (2, 0), (4, 0), (4, 2), (8, 4), (3, 2)])
 def test_strides_and_what_lies_beside(rows, width, pad, offset):
     vocab = 16411
     hidden, head, tokens = inputs(rows, vocab, width, F32)
