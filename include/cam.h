@@ -861,8 +861,8 @@ int cam_matmul8(int64_t tokens, int64_t rows, int64_t cols, const void* x, int64
  * gives a logp of NaN. vocab in [1, CAM_LOGPROBS_MAX_VOCAB], width in
  * [1, CAM_HEAD_MAX_WIDTH]; strides count elements between the starts of rows.
  * bf16 matrices whose rows start on 16 bytes are read where they are, and so is
- * an fp32 head for at most 128 rows; others go through the workspace in bf16
- * terms, in pieces of the vocabulary. workspace:
+ * a large fp32 head for at most 128 rows; others go through the workspace in
+ * bf16 terms, in pieces of the vocabulary. workspace:
  * cam_head_logprobs_workspace bytes (for the same arguments) of device memory,
  * 256-byte aligned, the call's own until it has run.
  * Errors: CAM_E_ARG, CAM_E_CUDA.
@@ -887,7 +887,8 @@ int cam_head_logprobs(int64_t rows, int64_t vocab, int64_t width, const void* hi
  *
  * in the inputs' dtype, sums in binary32, rounded once. The logits are
  * computed again, and G is held for one piece of the vocabulary at a time,
- * in three bf16 terms for fp32 inputs and rounded to bf16 for bf16 ones.
+ * in three bf16 terms for fp32 inputs, rounded to bf16 for bf16 ones (in two
+ * terms for at most 256 rows).
  * Either of grad_hidden and grad_head may be NULL, not both, and either of
  * grad_logp (with tokens) and grad_entropy (with entropy). lse, lse_lo (may be
  * NULL) and entropy are as cam_head_logprobs wrote them. A negative token id
