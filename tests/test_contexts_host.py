@@ -132,7 +132,19 @@ def test_head_workspaces():
     assert more == 300 * 64 * 2
     assert head_workspace(x=P + 2) - head_workspace() == 512
     assert head_workspace(200, dt=B.F32) - head_workspace(200) == 3 * (300 + 200) * 64 * 2
-    assert head_workspace(dt=B.F32) - head_workspace() == 3 * 4 * 64 * 2  # (few rows: the head as it is)
+    assert head_workspace(dt=B.F32) - head_workspace() == 3 * (300 + 4) * 64 * 2
+    # few rows over 2^23 elements, above 64 rows of more than 512 each: the head as it is
+    for rows, vocab, width, direct in ((4, 1 << 17, 64, True), (4, (1 << 17) - 1, 64, False), (64, 1 << 17, 64, True),
+                                       (65, 1 << 17, 64, False), (65, 1 << 14, 512, False),
+                                       (128, 1 << 14, 576, True), (129, 1 << 14, 576, False)):
+        size = {"rows": rows, "vocab": vocab, "width": width, "ldx": width, "ldw": width}
+        # (the statistics of `few` rows' calls are for 32 tokens each, of others for 256)
+        parts = (vocab + 31) // 32 if direct or rows <= 64 else (vocab + 255) // 256
+        padded = lambda n: (n + 511) // 512 * 512
+        want = padded(3 * rows * width * 2) + padded(parts * rows * 16) + padded(rows * 4)
+        if not direct:
+            want += padded(3 * vocab * width * 2)
+        assert head_workspace(dt=B.F32, **size) == want
     # a piece of the head, not all of it
     assert head_workspace(200, vocab=1 << 22, width=1024, ldx=1024, ldw=1024, dt=B.F32) < (1 << 29) + (1 << 20) \
         + (1 << 22) // 256 * 200 * 16
