@@ -56,31 +56,7 @@ struct TermArgs {
     int64_t all;
     const int64_t* tokens;
     const float *g, *h;
-    // The logits of the rows' tokens, by fp32 sums (null: not wanted). The tensor core's lean to
-    // zero by some 2^-23 of themselves: for a token's logit of 20 that is 2e-6 of its
-    // probability, and the gradient of a row whose other entries are small.
-    float* mine;
-    const float *hidden, *head;
-    int64_t hidden_stride, head_stride, rows, width, vocab;
-    int64_t term_blocks;  // the blocks after these
 };
-
-// A warp's sum of a row's products with its token's row of the head: 32 runs of every 32nd
-// product, joined in 64 bits.
-__device__ __forceinline__ void own_logit(const TermArgs& a, int64_t row, int lane) {
-    const int64_t token = a.tokens[row];
-    const bool keep = (a.g && token >= 0 && a.g[row] != 0.0f) || (a.h && a.h[row] != 0.0f);
-    float sum = 0.0f;
-    if (keep && token >= 0 && token < a.vocab) {
-        const float *x = a.hidden + row * a.hidden_stride, *w = a.head + token * a.head_stride;
-#pragma unroll 4
-        for (int64_t k = lane; k < a.width; k += 32) sum = fmaf(x[k], w[k], sum);
-    }
-    double all = sum;
-#pragma unroll
-    for (int by = 16; by >= 1; by /= 2) all += __shfl_xor_sync(0xFFFFFFFFu, all, by);
-    if (lane == 0) a.mine[row] = static_cast<float>(all);
-}
 
 // One or two matrices in one (bf16) or three (fp32) bf16 terms, eight columns per thread.
 template <typename T>
@@ -88,13 +64,8 @@ __global__ void __launch_bounds__(kHeadThreads) terms_kernel(const TermArgs a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     constexpr int kTerms = sizeof(T) == 4 ? 3 : 1;
-    if (blockIdx.x >= a.term_blocks) {
-        const int64_t row = (blockIdx.x - a.term_blocks) * (kHeadThreads / 32) + (threadIdx.x >> 5);
-        if (row < a.rows) own_logit(a, row, threadIdx.x & 31);
-        return;
-    }
     for (int64_t k = int64_t(blockIdx.x) * kHeadThreads + threadIdx.x; k < a.all;
-         k += a.term_blocks * kHeadThreads) {
+         k += int64_t(gridDim.x) * kHeadThreads) {
         const bool second = k >= a.first;
         const TermMatrix& m = a.m[second];
         const int64_t i = second ? k - a.first : k, across = (m.cols + 7) / 8;
@@ -426,7 +397,7 @@ TileOperand operand(const HeadCall& c, const Matrix& m, int64_t rows, bool direc
 // Queues the terms of up to two matrices (rows 0: none).
 cudaError_t make_terms(const HeadCall& c, const Matrix& m0, int64_t rows0, void* out0, bool masked,
                        const Matrix& m1, int64_t rows1, void* out1, const int64_t* tokens,
-                       const float* g, const float* h, float* mine, int sms, cudaStream_t s) {
+                       const float* g, const float* h, int sms, cudaStream_t s) {
     const int64_t across = (c.width + 7) / 8;
     TermArgs a{};
     a.m[0] = {m0.base, m0.stride, rows0, c.width, static_cast<__nv_bfloat16*>(out0), c.ld, rows0 * c.ld,
@@ -439,19 +410,8 @@ cudaError_t make_terms(const HeadCall& c, const Matrix& m0, int64_t rows0, void*
     a.g = g;
     a.h = h;
     if (a.all == 0) return cudaSuccess;
-    a.term_blocks = std::min<int64_t>((a.all + kHeadThreads - 1) / kHeadThreads, int64_t(sms) * 32);
-    int64_t blocks = a.term_blocks;
-    if (mine) {
-        a.mine = mine;
-        a.hidden = static_cast<const float*>(c.hidden.base);
-        a.head = static_cast<const float*>(c.head.base);
-        a.hidden_stride = c.hidden.stride;
-        a.head_stride = c.head.stride;
-        a.rows = c.rows;
-        a.width = c.width;
-        a.vocab = c.vocab;
-        blocks += (c.rows + kHeadThreads / 32 - 1) / (kHeadThreads / 32);
-    }
+    const int64_t blocks =
+        std::min<int64_t>((a.all + kHeadThreads - 1) / kHeadThreads, int64_t(sms) * 32);
     return c.dtype == CAM_F32 ? launch(terms_kernel<float>, blocks, a, s)
                               : launch(terms_kernel<__nv_bfloat16>, blocks, a, s);
 }
@@ -512,7 +472,7 @@ ForwardPlan forward_plan(const HeadCall& c) {
 }
 
 struct BackwardPlan {
-    int64_t piece, x, w, mine, grad, hidden, head, bytes;
+    int64_t piece, x, w, grad, hidden, head, bytes;
     int32_t hidden_splits, head_splits;
     int32_t hidden_ranges;  // few32: of the largest piece
     int64_t part_ld, grad_ld, grad_stride;
@@ -553,8 +513,6 @@ BackwardPlan backward_plan(const HeadCall& c, int sms, bool want_hidden, bool wa
     at += term_bytes(c, c.rows);
     p.w = at;
     if (!c.w_direct) at += term_bytes(c, piece);
-    p.mine = at;
-    if (c.terms == 3) at += padded(c.rows * 4);
     p.grad = at;
     // G [rows][piece], or of few rows G^T [piece][rows, to a multiple of eight]
     p.grad_ld = c.few ? (c.rows + 7) / 8 * 8 : p.piece;
@@ -649,7 +607,7 @@ CAM_API int cam_head_logprobs(int64_t rows, int64_t vocab, int64_t width, const 
         const int64_t n = std::min(p.piece, vocab - at);
         const Matrix piece = piece_of(c, at);
         ce = make_terms(c, c.hidden, c.x_direct || at > 0 ? 0 : rows, ws + p.x, false, piece,
-                        c.w_direct ? 0 : n, ws + p.w, nullptr, nullptr, nullptr, nullptr, sms, s);
+                        c.w_direct ? 0 : n, ws + p.w, nullptr, nullptr, nullptr, sms, s);
         if (ce != cudaSuccess) break;
         TileProduct t{};
         t.a = operand(c, c.hidden, rows, c.x_direct, ws + p.x, false);
@@ -738,7 +696,6 @@ CAM_API int cam_head_logprobs_backward(int64_t rows, int64_t vocab, int64_t widt
     if (const int rc = check_workspace(fn, workspace, workspace_bytes, p.bytes)) return rc;
     char* ws = static_cast<char*>(workspace);
     cudaError_t ce = cudaSuccess;
-    float* mine = c.terms == 3 && tokens ? reinterpret_cast<float*>(ws + p.mine) : nullptr;
     const bool parts = p.hidden_splits > 1 || p.piece < vocab;
     for (int64_t at = 0; at < vocab && ce == cudaSuccess; at += p.piece) {
         const int64_t n = std::min(p.piece, vocab - at);
@@ -746,7 +703,7 @@ CAM_API int cam_head_logprobs_backward(int64_t rows, int64_t vocab, int64_t widt
         // hidden states in terms, rows without a gradient as zeros: what they hold, NaN say,
         // then reaches nothing
         ce = make_terms(c, c.hidden, at > 0 ? 0 : rows, ws + p.x, true, piece, c.w_direct ? 0 : n,
-                        ws + p.w, tokens, grad_logp, grad_entropy, at > 0 ? nullptr : mine, sms, s);
+                        ws + p.w, tokens, grad_logp, grad_entropy, sms, s);
         if (ce != cudaSuccess) break;
         TileProduct t{};
         t.a = operand(c, c.hidden, rows, false, ws + p.x, false);
@@ -765,7 +722,6 @@ CAM_API int cam_head_logprobs_backward(int64_t rows, int64_t vocab, int64_t widt
         t.out.entropy = entropy;
         t.out.g = grad_logp;
         t.out.h = grad_entropy;
-        t.out.mine = mine;
         if (const int rc = c.few32 ? few32_product(fn, head32(c, piece, n, t), kTileGradFew, sms, s)
                                    : tile_products(fn, &t, 1, false, c.pair,
                                                    c.few ? kTileGradFew : kTileGrad, sms, s))

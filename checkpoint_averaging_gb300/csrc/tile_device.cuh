@@ -173,7 +173,6 @@ struct GradRow {
     float g, h, H;
     float shift;    // the quick form: p = 2^(x log2(e) - shift), G = p (base - h x)
     float base;
-    float mine;     // the logit of the row's token, if known
     int32_t token;  // its column (the row of D for few rows), or -1
 };
 
@@ -191,13 +190,15 @@ __device__ __forceinline__ GradRow grad_row(const TileOut& o, int64_t row, int64
     if (r.g == 0.0f && r.h == 0.0f) r.lse = r.lo = r.H = 0.0f;
     r.shift = (r.lse + r.lo) * kLog2e;
     r.base = r.h * (r.lse - r.H) - r.g;
-    r.mine = o.mine && token >= 0 ? o.mine[row] : 0.0f;
     const int64_t at = token - o.token0;
     r.token = at >= 0 && at < n ? static_cast<int32_t>(at) : -1;
     return r;
 }
 
-// The gradient of the logit of the row's own token.
+// The gradient of the logit of the row's own token. Where p is near 1 it is what x and lse
+// differ by: x is the sum that lse was taken from, of the same terms in the same order, so that
+// what the tensor core lost of it is in both. (An exact x beside that lse: 1 - p of 1e-7 comes
+// out as -1e-5 for logits of 25.)
 __device__ __forceinline__ float own_grad(float x, const GradRow& r) {
     const float d = (x - r.lse) - r.lo, p = exp_exact(d, 0.0f);
     return r.g * one_minus_exp(d, p) - r.h * p * (d + r.H);
@@ -398,7 +399,7 @@ __device__ __forceinline__ void few_grad(const TileOut& o, int64_t N, const Grad
         if (i < n && rows[i].token == int(token)) own |= 1u << i;
     for (uint32_t left = own; left; left &= left - 1) {
         const int i = __ffs(left) - 1;
-        put(v, i, own_grad(o.mine ? rows[i].mine : pick(v, i), rows[i]));
+        put(v, i, own_grad(pick(v, i), rows[i]));
     }
     const bool three = o.planes == 3;
 #pragma unroll

@@ -590,7 +590,7 @@ __global__ void __launch_bounds__(Geo<E4M3, PAIR, EPI, COLS>::kThreads, 1)
                     int own = -1;  // the row's token, if it is among these
                     if (mine.token >= 0 && mine.token - int(col) >= 0 && mine.token - int(col) < 32) {
                         own = mine.token - int(col);
-                        put(v, own, own_grad(o.mine ? mine.mine : pick(v, own), mine));
+                        put(v, own, own_grad(pick(v, own), mine));
                     }
                     if (o.planes == 3 || __any_sync(0xffffffffu, fabsf(mine.lse) > kQuick)) {
 #pragma unroll

@@ -65,8 +65,7 @@ struct TileOut {
     float* part;
     int64_t part_ld;
     // kTileStats: stats[tile of columns][M]; `mine` [M] takes the logit of each
-    // row's token. kTileGrad: G into `planes` terms of y (bf16, row stride ldy); `mine`, if
-    // given, brings the logits of the rows' tokens. Few rows:
+    // row's token. kTileGrad: G into `planes` terms of y (bf16, row stride ldy). Few rows:
     // stats[row of D / 32][N], and G^T (rows of a multiple of eight elements).
     TileStat* stats;
     float* mine;
