@@ -752,9 +752,10 @@ int tile_products(const char* fn, const TileProduct* ps, int n, bool e4m3, bool 
         // Runs: of fp32 inputs 256 terms of each pair (all pairs of a run are close in time, so
         // that the terms' second and third reads come from L2; of 128 the logits' errors are 40 %
         // smaller and calls up to 5 % slower), of two-term G 512, of bf16 logits 768 (of 512: 3 %
-        // slower), of e4m3 2,048 (whose steps add twice as many terms); bf16 results of bf16
-        // inputs hide what a long run loses.
-        const bool logits = epilogue == kTileStats || epilogue == kTileStatsFew;
+        // slower; the gradients take the logits by the same sums as the statistics, as 1 - p of
+        // a row's token is a difference between the two), of e4m3 2,048 (whose steps add twice as
+        // many terms); bf16 results of bf16 inputs hide what a long run loses.
+        const bool logits = epilogue != kTileOut;
         P.run = pairs > 2 ? 4 : pairs == 2 ? 8 : e4m3 ? 16 : logits ? 12 : INT_MAX;
         const int splits = std::max(1, std::min(p.splits, P.steps));
         P.per_split = (P.steps + splits - 1) / splits;

@@ -82,7 +82,7 @@ class Exact:
 SIZES = [(9, 500, 2048), (9, 4200, 2048), (100, 4200, 2048), (100, 700, 4096), (300, 900, 4096), (300, 4200, 2048)]
 
 
-@pytest.mark.parametrize("dtype", [F32])
+@pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("rows,vocab,width", SIZES)
 @pytest.mark.parametrize("entropy", [False, True])
 def test_gradients_by_the_forward_calls_lse(rows, vocab, width, dtype, entropy):
@@ -107,7 +107,7 @@ def test_gradients_by_the_forward_calls_lse(rows, vocab, width, dtype, entropy):
         assert (off <= tol + 1e-37).all(), (float((off / (tol + 1e-37)).max()), int((off > tol).sum()))
 
 
-@pytest.mark.parametrize("dtype", [F32])
+@pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("rows,vocab,width", [(9, 4200, 2048), (300, 900, 4096)])
 def test_rows_push_along_their_token(rows, vocab, width, dtype):
     """Through autograd: a row's gradient pushes it along its token's row of the head, by
