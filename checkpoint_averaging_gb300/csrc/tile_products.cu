@@ -34,7 +34,6 @@
 
 #include <algorithm>
 #include <atomic>
-#include <climits>
 #include <cstring>
 
 #include "cam_internal.h"
@@ -754,9 +753,11 @@ int tile_products(const char* fn, const TileProduct* ps, int n, bool e4m3, bool 
         // smaller and calls up to 5 % slower), of two-term G 512, of bf16 logits 768 (of 512: 3 %
         // slower; the gradients take the logits by the same sums as the statistics, as 1 - p of
         // a row's token is a difference between the two), of e4m3 2,048 (whose steps add twice as
-        // many terms); bf16 results of bf16 inputs hide what a long run loses.
+        // many terms), of the gradients' one-term products 8,192: what 512 additions lose, 2^-15
+        // of a sum at most, is hidden in bf16 results, but not what a sum over 2^18 rows loses
+        // in one run.
         const bool logits = epilogue != kTileOut;
-        P.run = pairs > 2 ? 4 : pairs == 2 ? 8 : e4m3 ? 16 : logits ? 12 : INT_MAX;
+        P.run = pairs > 2 ? 4 : pairs == 2 ? 8 : e4m3 ? 16 : logits ? 12 : 128;
         const int splits = std::max(1, std::min(p.splits, P.steps));
         P.per_split = (P.steps + splits - 1) / splits;
         const int ranges = (P.steps + P.per_split - 1) / P.per_split;
