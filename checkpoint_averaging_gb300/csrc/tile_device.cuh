@@ -276,7 +276,7 @@ struct RowStat {
             t_before = t;
             if (leads) {
                 const float d = m - top, f = exp2_fast(d * kLog2e);
-                t_before = f * fmaf(d, 1.0f + a, t);
+                t_before = f * (f > 0.0f ? fmaf(d, 1.0f + a, t) : t);  // (as in join)
                 before = (1.0f + a) * f;
             }
         }

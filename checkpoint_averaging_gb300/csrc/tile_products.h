@@ -52,7 +52,10 @@ __device__ __forceinline__ void join(TileStat& s, const TileStat& o) {
     const bool mine = s.m >= o.m;
     const TileStat hi = mine ? s : o, lo = mine ? o : s;
     const float d = lo.m - hi.m, f = exp2f(d * 1.4426950408889634f), sum = 1.0f + lo.a;
-    s = TileStat{hi.m, fmaf(f, sum, hi.a), fmaf(f, fmaf(d, sum, lo.t), hi.t), 1.0f};
+    // (masks of the type's lowest value: d times their number is beyond binary32, and 0 times that
+    // a NaN; a part of NaN has it in t)
+    const float t = f > 0.0f ? fmaf(d, sum, lo.t) : lo.t;
+    s = TileStat{hi.m, fmaf(f, sum, hi.a), fmaf(f, t, hi.t), 1.0f};
 }
 
 struct TileOut {

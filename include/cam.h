@@ -856,10 +856,13 @@ int cam_matmul8(int64_t tokens, int64_t rows, int64_t cols, const void* x, int64
  * of their products those below 2^-23 of |hidden||head| are left out. logp (with
  * tokens), entropy, lse and lse_lo are as there; tokens and logp may both be
  * NULL, the others each. There are no alternatives: ask cam_token_logprobs.
- * A row with a logit that is NaN, infinite or beyond binary32 has NaN
- * throughout. A negative token id is no token (logp 0); one of `vocab` or more
- * gives a logp of NaN. vocab in [1, CAM_LOGPROBS_MAX_VOCAB], width in
- * [1, CAM_HEAD_MAX_WIDTH]; strides count elements between the starts of rows.
+ * A logit of the type's lowest value is a token that cannot occur (p = 0), by
+ * a column of the head for hidden states of 1 there, say. A row with a logit
+ * that is NaN, infinite or beyond binary32 has NaN throughout; one with logits
+ * further apart than binary32's largest number may. A negative token id is no
+ * token (logp 0); one of `vocab` or more gives a logp of NaN. vocab in
+ * [1, CAM_LOGPROBS_MAX_VOCAB], width in [1, CAM_HEAD_MAX_WIDTH]; strides count
+ * elements between the starts of rows.
  * bf16 matrices whose rows start on 16 bytes are read where they are, and so is
  * a large fp32 head for at most 128 rows; others go through the workspace in
  * bf16 terms, in pieces of the vocabulary. workspace:
