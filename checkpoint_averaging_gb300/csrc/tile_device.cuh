@@ -171,7 +171,7 @@ __device__ __forceinline__ float one_minus_exp(float d, float p) {
 struct GradRow {
     float lse, lo;  // log p = (x - lse) - lo
     float g, h, H;
-    float shift;    // the quick form: p = 2^(x log2(e) - shift), G = p (base - h x)
+    float shift;    // the quick form: p = 2^(x log2(e) - shift), G = p base - p h x
     float base;
     int32_t token;  // its column (the row of D for few rows), or -1
 };
@@ -195,12 +195,21 @@ __device__ __forceinline__ GradRow grad_row(const TileOut& o, int64_t row, int64
     return r;
 }
 
+// log p no lower than where p is 0 (and NaN where it is NaN): a masked logit, the type's lowest
+// value, times log2(e) or h is an infinity, and 0 times that a NaN. (1 % of fp32 gradients of 1,023
+// rows over 50,304 x 128; selecting 0 for a p of 0 took 5 %.)
+__device__ __forceinline__ float held(float d) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(d), "f"(-8192.0f));
+    return y;
+}
+
 // The gradient of the logit of the row's own token. Where p is near 1 it is what x and lse
 // differ by: x is the sum that lse was taken from, of the same terms in the same order, so that
 // what the tensor core lost of it is in both. (An exact x beside that lse: 1 - p of 1e-7 comes
 // out as -1e-5 for logits of 25.)
 __device__ __forceinline__ float own_grad(float x, const GradRow& r) {
-    const float d = (x - r.lse) - r.lo, p = exp_exact(d, 0.0f);
+    const float d = held((x - r.lse) - r.lo), p = exp_exact(d, 0.0f);
     return r.g * one_minus_exp(d, p) - r.h * p * (d + r.H);
 }
 
@@ -214,10 +223,12 @@ __device__ __forceinline__ float other_grad(float x, const GradRow& r) {
         float d = x - r.lse;
         const float b = x - d;  // (x - lse) - d, exactly: two-sum
         const float rest = ((x - (d + b)) + (b - r.lse)) - r.lo;
+        d = held(d);
         const float p = exp_exact(d, rest);
         return -p * fmaf(r.h, (d + rest) + r.H, r.g);
-    } else {
-        return exp2_fast(fmaf(x, kLog2e, -r.shift)) * fmaf(-r.h, x, r.base);
+    } else {  // (p h first: h x may be an infinity where p is 0)
+        const float p = exp2_fast(fmaf(x, kLog2e, -r.shift));
+        return fmaf(-(p * r.h), x, p * r.base);
     }
 }
 
