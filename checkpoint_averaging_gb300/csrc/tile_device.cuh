@@ -173,8 +173,16 @@ struct GradRow {
     float g, h, H;
     float shift;    // the quick form: p = 2^(x log2(e) - shift), G = p base - p h x
     float base;
+    float far, far_lo;  // what near() takes off the row's logits
     int32_t token;  // its column (the row of D for few rows), or -1
 };
+
+// exp_exact takes what is left over as a first-order term, the square of half of which has to be
+// below 2^-24: lo is up to 2^-12 for an lse of 2^13, and a half at 2^23. Rows beyond have lse and
+// lo taken off their logits first, which then are log p, off by 2^-24 of itself (the logits
+// there are rounded by more).
+constexpr float kFar = 8192.0f;
+__device__ __forceinline__ float near(float x, const GradRow& r) { return (x - r.far) - r.far_lo; }
 
 __device__ __forceinline__ GradRow grad_row(const TileOut& o, int64_t row, int64_t n) {
     GradRow r;
@@ -188,6 +196,11 @@ __device__ __forceinline__ GradRow grad_row(const TileOut& o, int64_t row, int64
     if (r.g != 0.0f && token >= o.vocab) r.lse = __int_as_float(0x7FC00000);
     // no gradient: zeros, whatever lse is (the row's logits are zeros: head.cu)
     if (r.g == 0.0f && r.h == 0.0f) r.lse = r.lo = r.H = 0.0f;
+    r.far = r.far_lo = 0.0f;
+    if (fabsf(r.lse) > kFar) {
+        r.far = r.lse, r.far_lo = r.lo;
+        r.lse = r.lo = 0.0f;
+    }
     r.shift = (r.lse + r.lo) * kLog2e;
     r.base = r.h * (r.lse - r.H) - r.g;
     const int64_t at = token - o.token0;
@@ -404,6 +417,12 @@ __device__ __forceinline__ void few_stats(const TileOut& o, int64_t M, int64_t N
 __device__ __forceinline__ void few_grad(const TileOut& o, int64_t N, const GradRow* rows, float* v,
                                          int64_t token, int64_t col0, bool in) {
     const int n = N - col0 < 32 ? int(N - col0) : 32;
+    const int lane = threadIdx.x & 31;
+    if (__any_sync(0xFFFFFFFFu, lane < n && rows[lane].far != 0.0f)) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (i < n) v[i] = near(v[i], rows[i]);
+    }
     uint32_t own = 0;  // the rows whose token this is
 #pragma unroll
     for (int i = 0; i < 32; ++i)

@@ -586,6 +586,10 @@ __global__ void __launch_bounds__(Geo<E4M3, PAIR, EPI, COLS>::kThreads, 1)
                 float* v = sum + 32 * c;
                 const int n = P.N - col < 32 ? int(P.N - col) : 32;
                 if constexpr (EPI == kTileGrad) {
+                    if (__any_sync(0xffffffffu, mine.far != 0.0f)) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = near(v[i], mine);
+                    }
                     int own = -1;  // the row's token, if it is among these
                     if (mine.token >= 0 && mine.token - int(col) >= 0 && mine.token - int(col) < 32) {
                         own = mine.token - int(col);
