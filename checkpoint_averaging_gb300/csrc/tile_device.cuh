@@ -142,15 +142,20 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
-constexpr float kLog2e = 1.4426950408889634f;
+// log2(e) in two binary32 numbers.
+constexpr double kLog2eExact = 1.4426950408889634074;
+constexpr float kLog2e = static_cast<float>(kLog2eExact);
+constexpr float kLog2eRest = static_cast<float>(kLog2eExact - static_cast<double>(kLog2e));
+constexpr float kLn2 = 0.69314718055994530942f;
 
-// exp(x - hi - lo) with what rounding x - hi and its product with log2(e) left out (both
-// matter in fp32 gradients: 2^-24 of an argument of 20 is 1e-6 of the exponential).
+// exp(d + rest) = 2^t 2^c: t is d log2(e) rounded, c what rounding that product (an fma gives it),
+// log2(e) itself, and `rest` leave of the exponent (all matter in fp32 gradients: 2^-24 of an
+// argument of 20 is 1e-6 of the exponential); 2^c is 1 + c ln 2.
 __device__ __forceinline__ float exp_exact(float d, float rest) {
     const float t = d * kLog2e;
-    const float c = fmaf(d, kLog2e, -t) + fmaf(d, 1.925963033500e-8f, rest * kLog2e);
+    const float c = fmaf(d, kLog2e, -t) + fmaf(d, kLog2eRest, rest * kLog2e);
     const float e = exp2_fast(t);
-    return fmaf(e, c * 0.69314718f, e);
+    return fmaf(e, c * kLn2, e);
 }
 
 // 1 - exp(d) for d near 0 and below, p = exp(d): the Taylor series of exp(d) - 1 where the

@@ -38,6 +38,24 @@ def apart(logits, base, dtype):
     return hidden.to(dtype).to(DEV), head.to(dtype).to(DEV)
 
 
+@pytest.mark.parametrize("rows,vocab", [(5, 3000), (64, 1 << 17), (100, 2000), (300, 1000)])
+def test_exponentials_of_the_gradients(rows, vocab):
+    gen = torch.Generator().manual_seed(rows)
+    logits = torch.rand(rows, vocab, generator=gen) * 80 - 60
+    hidden, head = apart(logits, 0.0, F32)
+    lse = (torch.rand(rows, generator=gen) * 30 - 10).to(DEV)
+    lo = lse * 2.0 ** -25
+    x = logits.to(DEV).double()
+    tokens = torch.zeros(rows, dtype=torch.int64, device=DEV)
+    g = torch.full((rows,), -1.0, device=DEV)
+    _, got = B.head_logprobs_backward(hidden, head, tokens, lse, lse, g, lse_lo=lo, need_hidden=False)
+    want = (x - lse.double()[:, None] - lo.double()[:, None]).exp()
+    G = got.double().t()[:rows]
+    off = ((G - want).abs() / want)[:, 1:]
+    fine = want[:, 1:] > 2.0 ** -100  # (smaller ones have fewer bits in three bf16 terms)
+    assert float(off[fine].max()) <= 2.0 ** -20
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("rows,vocab", [(5, 300), (64, 1 << 17), (100, 700), (300, 600)])
 @pytest.mark.parametrize("power", [10, 17, 20, 22, 23])
