@@ -222,6 +222,8 @@ def main_contexts(vocab: int = 8192, width: int = 512, rows: int = 1000, seed: i
             loss.backward()
             state = (state - 0.5 * state.grad).detach()
             weight = (weight - 0.5 * weight.grad).detach()
+    if B.operators_status() != 0:  # (then results are undefined, and no call has said so)
+        raise RuntimeError("an operator gave up waiting on a barrier")
     return eight, full, losses
 
 
