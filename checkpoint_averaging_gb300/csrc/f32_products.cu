@@ -18,6 +18,10 @@
 //                      tile (or 8 rows of K) each: copied, split
 //   warps 10..17       epilogue: a lane is a row of the matrix, its registers the few rows
 //
+// 18 warps leave 96 registers a thread, which the epilogues do not fit in: for 128 columns 740
+// bytes of stores and 992 of loads a thread are spilled for the statistics, 524 and 520 for G, 132 and
+// 156 for the gradients' products, for 64 columns 160 and 144, 116 and 112, and 8 and 16.
+//
 // Waits are bounded as in tile_products.cu.
 #include <algorithm>
 #include <atomic>
@@ -39,7 +43,7 @@ constexpr int kTermBytes = kRows32 * kStep * 2;  // one term of the matrix's til
 constexpr int kSplitWarps = 8;
 constexpr int kGroup = 4;          // of them work on one step (all eight on each: 30 % slower)
 constexpr int kSlot = 4096;        // a warp's share of a step, fp32
-// Steps of a run: 126 rows over 152,602 x 824 take 279 us, with eight 246; the entropy of one row
+// Steps of a run: 126 rows over 152,602 x 824 take 280 us, with eight 246; the entropy of one row
 // over 11,241 x 1,469 is off by 9.9e-7 of itself, with eight 1.8e-6.
 constexpr int kRun32 = 4;
 

@@ -443,8 +443,14 @@ int64_t piece_rows(const HeadCall& c, int64_t per, int64_t budget) {
     return ((c.vocab + n - 1) / n + kTileCols - 1) / kTileCols * kTileCols;
 }
 
-constexpr int64_t kForwardBudget = int64_t(1) << 29;   // a piece of the head in terms
-constexpr int64_t kBackwardBudget = int64_t(1) << 29;  // a piece of G, and of the head in terms
+// A piece of the head in terms; a piece of G, and of the head in terms. Each piece is launches of
+// its own, whose last rounds of tiles are short, and a reading of the hidden states: what smaller
+// ones keep in L2 is less than that. 2^25, 2^27, 2^28, 2^29 and 2^31 bytes: log probabilities of 300
+// fp32 rows over 400,000 x 1,024 3,068, 2,281, 2,056, 1,919 and 1,830 us; gradients of 1,023 fp32 rows
+// over 50,304 x 128 452, 329, 325, 280 and 281, of 842 over 10,385 x 2,997 1,503, 831, 750, 751 and 751,
+// of 4,096 bf16 rows over 73,760 x 2,048 2.60, 2.12, 2.05, 2.10 and 2.08 ms.
+constexpr int64_t kForwardBudget = int64_t(1) << 29;
+constexpr int64_t kBackwardBudget = int64_t(1) << 29;
 
 // Parts of the vocabulary with statistics of their own.
 int64_t stat_parts(const HeadCall& c) {
@@ -480,7 +486,8 @@ struct BackwardPlan {
 
 // Ranges of K for a product of `tiles` tiles of `steps` steps of K, `pairs` products of terms
 // each: enough units for `want`, and none longer than `most` products, but none shorter than
-// eight.
+// eight (gradients of 40 fp32 rows over 5,000 x 300: four 35.6 us, eight 37, sixteen 33.6; of larger
+// cases within 1 %).
 int32_t splits_for(int64_t tiles, int64_t steps, int64_t pairs, int64_t want, int64_t most) {
     const int64_t n = std::min(std::max((want + tiles - 1) / tiles, (steps * pairs + most - 1) / most),
                                std::max<int64_t>(1, std::min(steps, steps * pairs / 8)));
@@ -499,7 +506,9 @@ BackwardPlan backward_plan(const HeadCall& c, int sms, bool want_hidden, bool wa
     const int64_t pairs = c.terms == 3 ? 6 : c.grad_terms;
     p.part_ld = (c.width + 7) / 8 * 8;
     // both products share a launch: units of like length, the longer ones first, so that its
-    // last round is nearly full
+    // last round is nearly full (at least 16, 64 or 256 products in a unit of hidden's: 1,652 bf16 rows
+    // over 96,011 x 155 302, 310 and 301 us, 4,096 over 73,760 x 2,048 2.05, 2.10 and 2.12 ms, 200 over
+    // 30,000 x 700 100, 104 and 104 us)
     const int64_t head_steps = (c.rows + 63) / 64, hidden_steps = (piece + 63) / 64;
     p.head_splits = splits_for((piece + tile - 1) / tile * across, head_steps, pairs, grid, INT64_MAX / 2);
     p.hidden_splits = splits_for((c.rows + tile - 1) / tile * across, hidden_steps, pairs, 2 * grid,

@@ -852,10 +852,11 @@ int cam_matmul8(int64_t tokens, int64_t rows, int64_t cols, const void* x, int64
  * the logits x = hidden head^T, for `rows` rows of hidden [rows][width] and a
  * head [vocab][width] of the same dtype (fp32 or bf16), without storing the
  * logits: they are products summed in binary32 on the tensor cores and stay in
- * binary32. fp32 inputs are taken in three bf16 terms each (all 24 bits);
- * of their products those below 2^-23 of |hidden||head| are left out. logp (with
- * tokens), entropy, lse and lse_lo are as there; tokens and logp may both be
- * NULL, the others each. There are no alternatives: ask cam_token_logprobs.
+ * binary32. fp32 inputs are taken in three bf16 terms each (all 24 bits, of
+ * values below 2^-110 those from 2^-133 up); of their products those below
+ * 2^-23 of |hidden||head| are left out. logp (with tokens), entropy, lse and
+ * lse_lo are as there; tokens and logp may both be NULL, the others each. There
+ * are no alternatives: ask cam_token_logprobs.
  * A logit of the type's lowest value is a token that cannot occur (p = 0), by
  * a column of the head for hidden states of 1 there, say. A row with a logit
  * that is NaN, infinite or beyond binary32 has NaN throughout; one with logits
@@ -894,12 +895,16 @@ int cam_head_logprobs(int64_t rows, int64_t vocab, int64_t width, const void* hi
  * terms for at most 256 rows).
  * Either of grad_hidden and grad_head may be NULL, not both, and either of
  * grad_logp (with tokens) and grad_entropy (with entropy). lse, lse_lo (may be
- * NULL) and entropy are as cam_head_logprobs wrote them. A negative token id
- * counts as g = 0. Rows whose g and h are 0 give and get nothing, whatever
- * their hidden states hold; a row whose lse is NaN, or whose token id is `vocab`
- * or more (with g other than 0), has a G of NaN, and with it every row of
- * grad_head. rows = 0 writes zeros to grad_head. The gradients may not overlap
- * the inputs. Results are the same bits from call to call.
+ * NULL: then log p has lse's rounding) and entropy are as cam_head_logprobs
+ * wrote them for the same hidden states and head: the logits are summed as
+ * there, so that 1 - p of a row's token, a difference between the two, is right
+ * however small it is. An lse from other sums moves every p by what it is off.
+ * A masked logit (the type's lowest value) has a gradient of 0. A negative
+ * token id counts as g = 0. Rows whose g and h are 0 give and get nothing,
+ * whatever their hidden states hold; a row whose lse is NaN, or whose token id
+ * is `vocab` or more (with g other than 0), has a G of NaN, and with it every
+ * row of grad_head. rows = 0 writes zeros to grad_head. The gradients may not
+ * overlap the inputs. Results are the same bits from call to call.
  * workspace: cam_head_logprobs_backward_workspace bytes, 256-byte aligned, the
  * call's own until it has run. Errors: CAM_E_ARG, CAM_E_CUDA.
  */
