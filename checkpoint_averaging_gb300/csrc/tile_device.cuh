@@ -176,7 +176,7 @@ __device__ __forceinline__ float one_minus_exp(float d, float p) {
 struct GradRow {
     float lse, lo;  // log p = (x - lse) - lo
     float g, h, H;
-    float shift;    // the quick form: p = 2^(x log2(e) - shift), G = p base - p h x
+    float shift;  // the quick form, d = x - lse: p = 2^(d log2(e) - shift), G = -p h d - p base
     float base;
     float far, far_lo;  // what near() takes off the row's logits
     int32_t token;  // its column (the row of D for few rows), or -1
@@ -206,8 +206,8 @@ __device__ __forceinline__ GradRow grad_row(const TileOut& o, int64_t row, int64
         r.far = r.lse, r.far_lo = r.lo;
         r.lse = r.lo = 0.0f;
     }
-    r.shift = (r.lse + r.lo) * kLog2e;
-    r.base = r.h * (r.lse - r.H) - r.g;
+    r.shift = r.lo * kLog2e;
+    r.base = fmaf(r.h, r.H - r.lo, r.g);
     const int64_t at = token - o.token0;
     r.token = at >= 0 && at < n ? static_cast<int32_t>(at) : -1;
     return r;
@@ -232,9 +232,8 @@ __device__ __forceinline__ float own_grad(float x, const GradRow& r) {
 }
 
 // That of another's. FINE: for fp32 results, with all that matters there of d's rounding.
-// Otherwise p is off by 2^-24 of lse log2(e), a hundredth of what rounding G to bf16 costs
-// as long as |lse| is below kQuick.
-constexpr float kQuick = 256.0f;
+// Otherwise p is off by 2^-23 of log p, a hundredth of what rounding G to bf16 costs; near
+// p = 1, where log p + H is far smaller than lse, d is exact.
 template <bool FINE>
 __device__ __forceinline__ float other_grad(float x, const GradRow& r) {
     if constexpr (FINE) {
@@ -244,9 +243,9 @@ __device__ __forceinline__ float other_grad(float x, const GradRow& r) {
         d = held(d);
         const float p = exp_exact(d, rest);
         return -p * fmaf(r.h, (d + rest) + r.H, r.g);
-    } else {  // (p h first: h x may be an infinity where p is 0)
-        const float p = exp2_fast(fmaf(x, kLog2e, -r.shift));
-        return fmaf(-(p * r.h), x, p * r.base);
+    } else {  // (p h first: h d may be an infinity where p is 0)
+        const float d = x - r.lse, p = exp2_fast(fmaf(d, kLog2e, -r.shift));
+        return fmaf(-(p * r.h), d, -(p * r.base));
     }
 }
 
@@ -442,9 +441,7 @@ __device__ __forceinline__ void few_grad(const TileOut& o, int64_t N, const Grad
         if (i >= n) {
             v[i] = 0.0f;
         } else {
-            const GradRow r = rows[i];
-            const bool fine = three || fabsf(r.lse) > kQuick;  // (one row for every lane)
-            const float w = fine ? other_grad<true>(v[i], r) : other_grad<false>(v[i], r);
+            const float w = three ? other_grad<true>(v[i], rows[i]) : other_grad<false>(v[i], rows[i]);
             v[i] = own >> i & 1 ? v[i] : w;
         }
     }

@@ -597,7 +597,7 @@ __global__ void __launch_bounds__(Geo<E4M3, PAIR, EPI, COLS>::kThreads, 1)
                         own = mine.token - int(col);
                         put(v, own, own_grad(pick(v, own), mine));
                     }
-                    if (o.planes == 3 || __any_sync(0xffffffffu, fabsf(mine.lse) > kQuick)) {
+                    if (o.planes == 3) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             v[i] = own == i ? v[i] : other_grad<true>(v[i], mine);

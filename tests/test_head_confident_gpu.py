@@ -109,6 +109,32 @@ def test_gradients_by_the_forward_calls_lse(rows, vocab, width, dtype, entropy):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("rows,vocab,width", SIZES)
+@pytest.mark.parametrize("given", ["none", "negative", "another"])
+def test_entropy_gradients_of_rows_sure_of_another_id(rows, vocab, width, dtype, given):
+    """The id that has nearly all of the probability is not the row's token: log p + H of it is of
+    the size of 1 - p all the same."""
+    hidden, head, sure = confident(rows, vocab, width, dtype)
+    e = Exact(hidden, head, sure)
+    tokens = {"none": None, "negative": torch.full_like(sure, -1), "another": (sure + 1) % vocab}[given]
+    r = B.head_logprobs(hidden, head, tokens)
+    gen = torch.Generator().manual_seed(rows)
+    h = (torch.rand(rows, generator=gen) + 0.5).to(DEV)
+    zero = torch.zeros(rows, device=DEV)
+    got = B.head_logprobs_backward(hidden, head, tokens, r.lse, r.entropy, zero if given == "another" else None, h,
+                                   lse_lo=r.lse_lo)
+    G, dG = e.gradient(zero, h)
+    dG = dG + (2.0 ** -8 if dtype == BF16 else 2.0 ** -23) * G.abs()
+    for out, other, dGo, Go, n in ((got[0], e.w, dG, G, vocab), (got[1], e.a, dG.t(), G.t(), rows)):
+        want = Go @ other
+        tol = dGo @ other.abs() + (2 * min(n, 8192) / 16 + 64) * 2.0 ** -23 * (Go.abs() @ other.abs())
+        if dtype == BF16:
+            tol += 2.0 ** -8 * want.abs()
+        off = (out.double() - want).abs()
+        assert (off <= tol + 1e-37).all(), (float((off / (tol + 1e-37)).max()), int((off > tol).sum()))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("rows,vocab,width", [(9, 4200, 2048), (300, 900, 4096)])
 def test_rows_push_along_their_token(rows, vocab, width, dtype):
     """Through autograd: a row's gradient pushes it along its token's row of the head, by
